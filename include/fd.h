@@ -53,7 +53,8 @@ extern "C" {
 #endif
 
 /* FD_E4M3 (OCP FP8 E4M3, one byte) is a KV-cache element type for
- * fd_decode_fp8, fd_decode_gqa_fp8 and fd_decode_gqa_paged_fp8 only. */
+ * fd_decode_fp8, fd_decode_gqa_fp8, fd_decode_gqa_paged_fp8,
+ * fd_append_paged_fp8 and fd_extend_paged_fp8 only. */
 typedef enum { FD_F32 = 0, FD_F16 = 1, FD_BF16 = 2, FD_E4M3 = 3 } fd_dtype;
 
 typedef enum {
@@ -64,7 +65,8 @@ typedef enum {
     FD_ERR_CUDA = 4,            /* a CUDA runtime call or launch failed       */
     FD_ERR_DEVICE_TIMEOUT = 5,  /* a kernel gave up waiting on its own copies */
     FD_ERR_SCRATCH_TOO_SMALL = 6, /* fd_decode_noalloc: problem exceeds its scratch */
-    FD_ERR_BAD_PAGE = 7         /* a block-table entry named no page (see fd_decode_paged) */
+    FD_ERR_BAD_PAGE = 7,        /* a block-table entry named no page (see fd_decode_paged) */
+    FD_ERR_BAD_OFFSETS = 8      /* sequence offsets that do not ascend within the rows given */
 } fd_status;
 
 /* Human-readable name of a status code (static string, never NULL; an
@@ -346,8 +348,10 @@ fd_status fd_merge_lse(const float *o_a, const float *lse_a, const float *o_b, c
 /*
  * Reads (and if `reset` is non-zero, clears) the current device's status
  * word, which a kernel sets when it gives up waiting on its own copies or
- * meets a block-table entry that names no page.  Synchronises the device.
- * Returns FD_OK, FD_ERR_DEVICE_TIMEOUT, FD_ERR_BAD_PAGE or FD_ERR_CUDA.
+ * meets a block-table entry that names no page or offsets that do not
+ * ascend.  Synchronises the device.  Returns FD_OK, FD_ERR_DEVICE_TIMEOUT,
+ * FD_ERR_BAD_PAGE, FD_ERR_BAD_OFFSETS (the first of these that is set) or
+ * FD_ERR_CUDA.
  */
 fd_status fd_device_status(int reset);
 
@@ -414,6 +418,150 @@ fd_status fd_selftest_wait_timeout(void *stream);
 fd_status fd_decode_noalloc(const void *q, const void *k, const void *v, const int32_t *seqlens,
                             int B, int H, int N, int d, fd_dtype in_dtype, int num_splits,
                             float scale, void *out, fd_dtype out_dtype, float *lse, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Around decode: what fills a paged KV cache and attends with several new
+ * tokens a sequence.  A serving step is
+ *     fd_resize_pages   every sequence to its new length: pages and slots
+ *     fd_append_paged   the new tokens' K and V rows into those slots
+ *     fd_extend_paged   their attention over the cache (or, with one new
+ *                       token a sequence, fd_decode_gqa_paged)
+ * and fd_prefill attends over packed prompts without a cache.  The new
+ * tokens of all sequences are packed one behind the other, sequence b's at
+ * rows cu[b] .. cu[b+1]-1 of every packed tensor (cu [B+1] int32, device).
+ * ---------------------------------------------------------------------- */
+
+/*
+ * Every sequence of a paged cache to a target length, in place and on the
+ * GPU: growth takes pages from a stack of free pages, shrinking (to 0 when a
+ * request ends, by a few tokens when drafted tokens are rejected) gives them
+ * back.  With pages(n) = ceil(n / page_size):
+ *   seqlens       [B] int32, in: current lengths, out: the new ones
+ *   target        [B] int32: wanted lengths (negative counts as 0)
+ *   block_table   [B, max_pages] int32: entries pages(old)..pages(new)-1 of
+ *                 a growing sequence are filled in; all others, those of
+ *                 released pages among them, stay as they are
+ *   free_pages, free_count   the stack: free_pages[0..*free_count-1] of
+ *                 num_pages int32 entries, the top last
+ *   slots, positions  [max_tokens] int32, either may be NULL: for the i-th
+ *                 new token (sequences in order, positions ascending) its
+ *                 place table[b][pos/page_size]*page_size + pos%page_size
+ *                 and its position; -1 and 0 behind the last one
+ *   cu_new        [B+1] int32, required with slots or positions, else may
+ *                 be NULL: offsets of the sequences' new tokens
+ * Releases come first and in reverse order, so that a release undoes the
+ * growth before it; then the sequences grow in order of b.  A sequence whose
+ * target passes max_pages pages keeps its length and needs nothing; one
+ * that needs pages keeps its length when the needs of all up to it exceed
+ * what is free, and one that has new tokens when those of all up to it
+ * exceed max_tokens (with slots or positions only).  Compare seqlens with
+ * target to see which were given.  The result does not depend on the order
+ * of threads.  A released entry that names no page, or a stack that would
+ * pass num_pages, is reported as FD_ERR_BAD_PAGE by fd_device_status.
+ * page_size*max_pages and page_size*num_pages must be below 2^31.
+ */
+fd_status fd_resize_pages(int32_t *seqlens, const int32_t *target, int B, int32_t *block_table, int max_pages,
+                          int32_t *free_pages, int32_t *free_count, int num_pages, int page_size, int32_t *slots,
+                          int32_t *positions, int max_tokens, int32_t *cu_new, void *stream);
+
+/*
+ * New K and V rows into a paged cache: row t, head h of k to
+ * k_pages[slot / page_size][h][slot % page_size] with slot = slots[t],
+ * likewise v.
+ *   k, v      [total, Hkv, d] in `dtype` (f32, f16 or bf16); a token's
+ *             Hkv*d elements are contiguous and 16-byte aligned, tokens
+ *             k_stride / v_stride elements apart (views of a fused
+ *             projection need no copy)
+ *   slots     [total] int32; a negative slot skips its token, one past the
+ *             pool is skipped and reported as FD_ERR_BAD_PAGE; slots that
+ *             repeat leave either token's row, or parts of both
+ *   k_pages, v_pages  [num_pages, Hkv, page_size, d] in `dtype`
+ * d must be 64, 128 or 256.
+ */
+fd_status fd_append_paged(const void *k, const void *v, const int32_t *slots, int total, int Hkv, int d,
+                          long long k_stride, long long v_stride, fd_dtype dtype, void *k_pages, void *v_pages,
+                          int page_size, long long num_pages, void *stream);
+
+/*
+ * fd_append_paged into E4M3 pages: a byte is k / k_scale[b*Hkv+h] (float32,
+ * IEEE division) rounded to the nearest E4M3 value, ties to even, and
+ * saturated at +-448 (NaN stays NaN).
+ *   k_scale, v_scale  [B*Hkv] float32 (those the attention calls take)
+ *   cu_new            [B+1] int32: which rows are sequence b's; B >= 1; rows
+ *                     outside [cu_new[0], cu_new[B]) are skipped
+ */
+fd_status fd_append_paged_fp8(const void *k, const void *v, const float *k_scale, const float *v_scale,
+                              const int32_t *cu_new, const int32_t *slots, int B, int total, int Hkv, int d,
+                              long long k_stride, long long v_stride, fd_dtype dtype, void *k_pages, void *v_pages,
+                              int page_size, long long num_pages, void *stream);
+
+/*
+ * Bytes of device workspace fd_prefill, fd_extend_paged and
+ * fd_extend_paged_fp8 need for these sizes on the current device.  It needs
+ * no initialisation; calls that overlap on the GPU need workspaces of their
+ * own.  Returns 0 for sizes that are not supported, or on a CUDA error.
+ */
+size_t fd_workspace_size_extend(int B, int total_q, int Hq, int Hkv, int d);
+
+/*
+ * Attention over packed prompts (the whole-sequence attention of "从第一性
+ * 原理推导 Flash Attention" §3 with the grouped heads of §8): sequence b has
+ * n_b = cu_q[b+1]-cu_q[b] queries and m_b = cu_k[b+1]-cu_k[b] keys, the last
+ * of both aligned; with `causal` query i of it sees keys below
+ * m_b - n_b + i + 1, else all m_b.
+ *   q            [total_q, Hq, d], k, v [total_k, Hkv, d] in in_dtype (f16 or
+ *                bf16); a token's heads are contiguous and 16-byte aligned,
+ *                tokens q_stride / k_stride / v_stride elements apart
+ *   cu_q, cu_k   [B+1] int32, ascending within [0, total_q] and [0,
+ *                total_k]; offsets that do not ascend are clamped and
+ *                reported as FD_ERR_BAD_OFFSETS by fd_device_status
+ *   out          [total_q, Hq, d] in out_dtype; lse [total_q, Hq] or NULL;
+ *                rows outside the sequences stay as they were
+ *   scale        > 0
+ *   workspace    fd_workspace_size_extend(...) bytes, 256-byte aligned
+ * d must be 64 or 128; any Hq / Hkv.  A query that sees no key gives out = 0
+ * and lse = -inf.  The scores are float32; the weights exp(s - m) are
+ * rounded to in_dtype for the product with V, which is summed in float32.
+ * Keys that a query does not see do not touch it, whatever K holds there; a
+ * V row that is not finite reaches every query of its sequence whose tile
+ * of 128 keys holds it, seen or not.  Rows behind a sequence's keys, or of
+ * other sequences, never do.
+ */
+fd_status fd_prefill(const void *q, const void *k, const void *v, const int32_t *cu_q, const int32_t *cu_k, int B,
+                     int total_q, int total_k, int Hq, int Hkv, int d, long long q_stride, long long k_stride,
+                     long long v_stride, fd_dtype in_dtype, int causal, float scale, void *out, fd_dtype out_dtype,
+                     float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Attention of new tokens over a paged cache that holds them already (a
+ * chunk of a prompt, drafted tokens to verify, or a batch of both and of
+ * single tokens): fd_prefill's causal attention with the keys of sequence b
+ * being the seqlens[b] tokens of its pages.
+ *   q                 [total_q, Hq, d], tokens q_stride elements apart
+ *   k_pages, v_pages  [num_pages, Hkv, page_size, d] in in_dtype (f16, bf16)
+ *   block_table       [B, max_pages] int32, rules of fd_decode_paged
+ *   cu_q              [B+1] int32, as in fd_prefill
+ *   seqlens           [B] int32, the new tokens included; clamped to [0,
+ *                     max_pages*page_size]
+ * page_size must be a multiple of 16 and num_pages*Hkv below 2^31.  All
+ * else as in fd_prefill.
+ */
+fd_status fd_extend_paged(const void *q, const void *k_pages, const void *v_pages, const int32_t *block_table,
+                          const int32_t *cu_q, const int32_t *seqlens, int B, int total_q, int Hq, int Hkv, int d,
+                          long long q_stride, int page_size, int max_pages, long long num_pages, fd_dtype in_dtype,
+                          float scale, void *out, fd_dtype out_dtype, float *lse, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/*
+ * fd_extend_paged over E4M3 pages with the scales of fd_decode_gqa_paged_fp8
+ * (k_scale, v_scale [B*Hkv] float32); q_dtype f16 or bf16.
+ */
+fd_status fd_extend_paged_fp8(const void *q, fd_dtype q_dtype, const void *k_pages, const void *v_pages,
+                              const float *k_scale, const float *v_scale, const int32_t *block_table,
+                              const int32_t *cu_q, const int32_t *seqlens, int B, int total_q, int Hq, int Hkv,
+                              int d, long long q_stride, int page_size, int max_pages, long long num_pages,
+                              float scale, void *out, fd_dtype out_dtype, float *lse, void *workspace,
+                              size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

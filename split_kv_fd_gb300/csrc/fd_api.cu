@@ -4,6 +4,7 @@
 #include "fd.h"
 #include "fd_gqa.cuh"
 #include "fd_gqa_tc8.cuh"
+#include "fd_host.h"
 #include "fd_internal.h"
 #include "fd_split.cuh"
 
@@ -20,15 +21,16 @@ namespace fd {
 // its own copies.
 __device__ unsigned g_status_word;
 
+constexpr int MAX_DEVICES = 64;
+
 namespace {
 
-constexpr int MAX_DEVICES = 64;
 // Cached device address of g_status_word, per device.  Host threads whose
 // first calls on a device coincide may each look it up; they store the same
 // value, and the atomic makes that well defined.
 std::atomic<unsigned *> g_status_ptr[MAX_DEVICES];
 
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+}  // namespace
 
 int current_device()
 {
@@ -67,7 +69,7 @@ unsigned *status_ptr()
     return static_cast<unsigned *>(ptr);
 }
 
-size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+namespace {
 
 bool valid_dtype(int t) { return t == FD_F32 || t == FD_F16 || t == FD_BF16; }
 
@@ -241,12 +243,7 @@ fd_status launch(int dtype, int d, const SplitParams &p, int decomp, cudaStream_
     return e == cudaSuccess ? FD_OK : FD_ERR_CUDA;
 }
 
-// cuTensorMapEncodeTiled, fetched from the driver through the runtime (no
-// link-time dependency on the driver library).
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+}  // namespace
 
 EncodeTiledFn encode_tiled()
 {
@@ -265,6 +262,8 @@ EncodeTiledFn encode_tiled()
     fn.store(f, std::memory_order_release);
     return f;
 }
+
+namespace {
 
 // K or V as `blocks` blocks of n rows of d 16-bit elements (a (b, K/V head)
 // of a contiguous cache, or a (page, K/V head) of a paged one), viewed as
@@ -440,6 +439,8 @@ const char *fd_status_str(fd_status status)
     case FD_ERR_WORKSPACE: return "FD_ERR_WORKSPACE: workspace missing or too small";
     case FD_ERR_CUDA: return "FD_ERR_CUDA: a CUDA runtime call or launch failed";
     case FD_ERR_DEVICE_TIMEOUT: return "FD_ERR_DEVICE_TIMEOUT: a kernel gave up waiting on its copies";
+    case FD_ERR_BAD_OFFSETS:
+        return "FD_ERR_BAD_OFFSETS: offsets that do not ascend within the rows given";
     case FD_ERR_BAD_PAGE:
         return "FD_ERR_BAD_PAGE: a block-table entry named no page (its rows were read from page 0)";
     case FD_ERR_SCRATCH_TOO_SMALL:
@@ -670,7 +671,9 @@ fd_status fd_device_status(int reset)
     }
     if (v & STATUS_TIMEOUT)
         return FD_ERR_DEVICE_TIMEOUT;
-    return (v & STATUS_BAD_PAGE) ? FD_ERR_BAD_PAGE : FD_OK;
+    if (v & STATUS_BAD_PAGE)
+        return FD_ERR_BAD_PAGE;
+    return (v & STATUS_BAD_OFFSETS) ? FD_ERR_BAD_OFFSETS : FD_OK;
 }
 
 size_t fd_workspace_size_gqa(int B, int Hq, int Hkv, int N, int d, int num_splits)

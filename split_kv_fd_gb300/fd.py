@@ -20,7 +20,7 @@ from . import _build_lib
 FD_OK = 0
 STATUS_NAMES = {0: "FD_OK", 1: "FD_ERR_INVALID_ARG", 2: "FD_ERR_UNSUPPORTED",
                 3: "FD_ERR_WORKSPACE", 4: "FD_ERR_CUDA", 5: "FD_ERR_DEVICE_TIMEOUT",
-                6: "FD_ERR_SCRATCH_TOO_SMALL", 7: "FD_ERR_BAD_PAGE"}
+                6: "FD_ERR_SCRATCH_TOO_SMALL", 7: "FD_ERR_BAD_PAGE", 8: "FD_ERR_BAD_OFFSETS"}
 
 DTYPE_CODE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
@@ -30,7 +30,8 @@ EXPORTS = ["fd_status_str", "fd_version", "fd_num_sms", "fd_auto_num_splits",
            "fd_combine_lse", "fd_device_status", "fd_decode_noalloc", "fd_decode_paged",
            "fd_decode_fp8", "fd_merge_lse", "fd_decode_gqa", "fd_workspace_size_gqa",
            "fd_selftest_wait_timeout", "fd_decode_gqa_paged", "fd_decode_gqa_fp8",
-           "fd_decode_gqa_paged_fp8"]
+           "fd_decode_gqa_paged_fp8", "fd_resize_pages", "fd_append_paged", "fd_append_paged_fp8",
+           "fd_workspace_size_extend", "fd_prefill", "fd_extend_paged", "fd_extend_paged_fp8"]
 
 _lock = threading.Lock()
 _lib = None
@@ -103,6 +104,21 @@ def load(build_if_missing: bool = False):
         lib.fd_decode_gqa_paged_fp8.argtypes = [P, I, P, P, P, P, P, P, I, I, I, I, I, I, ctypes.c_longlong, I,
                                                 F, P, I, P, P, S, P]
         lib.fd_decode_gqa_paged_fp8.restype = I
+        L = ctypes.c_longlong
+        lib.fd_resize_pages.argtypes = [P, P, I, P, I, P, P, I, I, P, P, I, P, P]
+        lib.fd_resize_pages.restype = I
+        lib.fd_append_paged.argtypes = [P, P, P, I, I, I, L, L, I, P, P, I, L, P]
+        lib.fd_append_paged.restype = I
+        lib.fd_append_paged_fp8.argtypes = [P, P, P, P, P, P, I, I, I, I, L, L, I, P, P, I, L, P]
+        lib.fd_append_paged_fp8.restype = I
+        lib.fd_workspace_size_extend.argtypes = [I, I, I, I, I]
+        lib.fd_workspace_size_extend.restype = S
+        lib.fd_prefill.argtypes = [P, P, P, P, P, I, I, I, I, I, I, L, L, L, I, I, F, P, I, P, P, S, P]
+        lib.fd_prefill.restype = I
+        lib.fd_extend_paged.argtypes = [P, P, P, P, P, P, I, I, I, I, I, L, I, I, L, I, F, P, I, P, P, S, P]
+        lib.fd_extend_paged.restype = I
+        lib.fd_extend_paged_fp8.argtypes = [P, I, P, P, P, P, P, P, P, I, I, I, I, I, L, I, I, L, F, P, I, P, P, S, P]
+        lib.fd_extend_paged_fp8.restype = I
         _lib = lib
         return lib
 
@@ -517,6 +533,298 @@ def decode_gqa_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seq
     return out, lse
 
 
+def _on_one_device(*ts):
+    """The CUDA device that all given tensors are on."""
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("all tensors must be CUDA tensors (the library has no CPU path)")
+        if dev is not None and t.device != dev:
+            raise ValueError("all tensors must be on one device")
+        dev = t.device
+    return dev
+
+
+def _rows(t, name):
+    """Elements between the tokens of a packed [T, H, d] tensor whose tokens
+    are contiguous (a view of a fused projection has them further apart)."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [T, H, d]")
+    T, H, d = t.shape
+    if t.numel() == 0:
+        return H * d
+    if (d > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: the H*d elements of a token must be contiguous")
+    if T == 1:
+        return H * d
+    if t.stride(0) < H * d:
+        raise ValueError(f"{name}: tokens must not overlap")
+    return t.stride(0)
+
+
+def _offsets(t, B, name):
+    if t.dtype != torch.int32 or t.shape != (B + 1,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape [B + 1]")
+
+
+def _int32(t, shape, name):
+    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)}")
+
+
+def _keep(dev, stream, *ts):
+    """Tensors allocated here under the current stream but used on ``stream``
+    are not reused before that stream is done with them."""
+    if stream is not None and stream != torch.cuda.current_stream(dev):
+        for t in ts:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def resize_pages(seqlens, target, block_table, free_pages, free_count, page_size, slots=None, positions=None,
+                 cu_new=None, stream=None):
+    """Every sequence of a paged cache to its target length, in place
+    (fd_resize_pages): pages are taken from and given back to the stack
+    ``free_pages[:free_count]``.
+
+    seqlens, target int32 [B]; block_table int32 [B, max_pages]; free_pages
+    int32 [num_pages]; free_count int32 [1]; slots and positions int32
+    [max_tokens] receive the new tokens' places in the pool and positions
+    (-1 and 0 behind the last), cu_new int32 [B+1] the offsets of the
+    sequences' new tokens (allocated if only slots or positions are given).
+    Returns ``cu_new``.  A sequence that could not grow keeps its length.
+    """
+    dev = _on_one_device(seqlens, target, block_table, free_pages, free_count, slots, positions, cu_new)
+    if seqlens.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("seqlens [B], block_table [B, max_pages], free_pages [num_pages]")
+    B = seqlens.shape[0]
+    _int32(seqlens, (B,), "seqlens")
+    _int32(target, (B,), "target")
+    _int32(block_table, (B, block_table.shape[1]), "block_table")
+    _int32(free_pages, free_pages.shape, "free_pages")
+    _int32(free_count, (1,), "free_count")
+    room = 0
+    for t, n in ((slots, "slots"), (positions, "positions")):
+        if t is None:
+            continue
+        if t.dim() != 1 or (slots is not None and t.shape != slots.shape):
+            raise ValueError("slots and positions must be [max_tokens]")
+        _int32(t, t.shape, n)
+        room = t.shape[0]
+    own = None
+    if cu_new is not None:
+        _offsets(cu_new, B, "cu_new")
+    elif slots is not None or positions is not None:
+        own = cu_new = torch.empty(B + 1, dtype=torch.int32, device=dev)
+    with torch.cuda.device(dev):
+        st = load().fd_resize_pages(_ptr(seqlens), _ptr(target), B, _ptr(block_table), block_table.shape[1],
+                                    _ptr(free_pages), _ptr(free_count), free_pages.shape[0], int(page_size),
+                                    _ptr(slots), _ptr(positions), room, _ptr(cu_new), _stream(seqlens, stream))
+    _check(st, "fd_resize_pages")
+    _keep(dev, stream, own)
+    return cu_new
+
+
+def _append_args(k, v, slots, k_pages, v_pages):
+    k_stride, v_stride = _rows(k, "k"), _rows(v, "v")
+    if v.shape != k.shape or v.dtype != k.dtype or k.dtype not in DTYPE_CODE:
+        raise ValueError("k and v must share one shape and dtype among float32/float16/bfloat16")
+    T, H, d = k.shape
+    _int32(slots, (T,), "slots")
+    _need_cuda(k_pages, v_pages)
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype \
+            or k_pages.shape[1] != H or k_pages.shape[3] != d:
+        raise ValueError("k_pages/v_pages must be [num_pages, Hkv, page_size, d] with Hkv, d of k")
+    return T, H, d, k_stride, v_stride
+
+
+def append_paged(k, v, slots, k_pages, v_pages, stream=None):
+    """New K and V rows into a paged cache, in place (fd_append_paged).
+
+    k, v [T, Hkv, d] (a token's heads contiguous, tokens any multiple of 16
+    bytes apart); slots int32 [T], negative ones skipped; k_pages/v_pages
+    [num_pages, Hkv, page_size, d] of k's dtype.
+    """
+    dev = _on_one_device(k, v, slots, k_pages, v_pages)
+    T, H, d, k_stride, v_stride = _append_args(k, v, slots, k_pages, v_pages)
+    if k_pages.dtype != k.dtype:
+        raise ValueError("the pages must have k's dtype")
+    with torch.cuda.device(dev):
+        st = load().fd_append_paged(_ptr(k), _ptr(v), _ptr(slots), T, H, d, k_stride, v_stride, DTYPE_CODE[k.dtype],
+                                    _ptr(k_pages), _ptr(v_pages), k_pages.shape[2], k_pages.shape[0],
+                                    _stream(k, stream))
+    _check(st, "fd_append_paged")
+
+
+def append_paged_fp8(k, v, k_scale, v_scale, cu_new, slots, k_pages, v_pages, stream=None):
+    """New K and V rows into E4M3 pages, in place (fd_append_paged_fp8): each
+    row divided by its sequence's and head's scale and rounded to E4M3.
+
+    k, v, slots as in append_paged; k_scale, v_scale float32 [B, Hkv]; cu_new
+    int32 [B+1]; pages torch.float8_e4m3fn (or uint8 E4M3 bytes).
+    """
+    dev = _on_one_device(k, v, k_scale, v_scale, cu_new, slots, k_pages, v_pages)
+    T, H, d, k_stride, v_stride = _append_args(k, v, slots, k_pages, v_pages)
+    if k_pages.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise ValueError("pages must be float8_e4m3fn (or uint8 E4M3 bytes)")
+    B = k_scale.shape[0] if k_scale.dim() == 2 else 0
+    _need_cuda(k_scale, v_scale)
+    for t in (k_scale, v_scale):
+        if t.dtype != torch.float32 or t.shape != (B, H):
+            raise ValueError("k_scale/v_scale must be float32 [B, Hkv]")
+    _offsets(cu_new, B, "cu_new")
+    with torch.cuda.device(dev):
+        st = load().fd_append_paged_fp8(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(cu_new), _ptr(slots), B,
+                                        T, H, d, k_stride, v_stride, DTYPE_CODE[k.dtype], _ptr(k_pages),
+                                        _ptr(v_pages), k_pages.shape[2], k_pages.shape[0], _stream(k, stream))
+    _check(st, "fd_append_paged_fp8")
+
+
+def workspace_size_extend(B, total_q, Hq, Hkv, d) -> int:
+    """Bytes of workspace prefill, extend_paged and extend_paged_fp8 need."""
+    return load().fd_workspace_size_extend(B, total_q, Hq, Hkv, d)
+
+
+def _extend_out(dev, q, B, Hkv, scale, out_dtype, out, lse, return_lse, workspace):
+    """What the attention calls of several new tokens set alike; allocates
+    what the caller left out, the workspace for this one call."""
+    T, Hq, d = q.shape
+    mine = []
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty((T, Hq, d), dtype=out_dtype or q.dtype, device=dev)
+        mine.append(out)
+    if lse is None and return_lse:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+        mine.append(lse)
+    _need_cuda(out, lse)
+    if out.dtype not in DTYPE_CODE or out.shape != (T, Hq, d):
+        raise ValueError("out must be [T, Hq, d] float32/float16/bfloat16")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, Hq)):
+        raise ValueError("lse must be float32 [T, Hq]")
+    if workspace is None:
+        workspace = torch.empty(max(load().fd_workspace_size_extend(B, T, Hq, Hkv, d), 256), dtype=torch.uint8,
+                                device=dev)
+        mine.append(workspace)
+    _need_cuda(workspace)
+    _on_one_device(q, out, lse, workspace)
+    return scale, out, lse, workspace, mine
+
+
+def prefill(q, k, v, cu_seqlens_q, cu_seqlens_k=None, causal=True, scale=None, out_dtype=None, out=None, lse=None,
+            return_lse=True, workspace=None, stream=None):
+    """Attention over packed prompts (fd_prefill).  Returns ``(out, lse)``.
+
+    q [Tq, Hq, d], k, v [Tk, Hkv, d] float16 or bfloat16, Hq a multiple of
+    Hkv, d 64 or 128; a token's heads contiguous, tokens any multiple of 16
+    bytes apart.  Sequence b's rows are cu_seqlens_q[b] ..
+    cu_seqlens_q[b+1]-1 of q, and the same of cu_seqlens_k (default: the same
+    offsets) of k and v; with ``causal`` the last query sees all keys, the
+    one before all but the last, and so on.  out [Tq, Hq, d], lse [Tq, Hq]
+    float32; rows outside the sequences are not written.
+    """
+    cu_k = cu_seqlens_q if cu_seqlens_k is None else cu_seqlens_k
+    dev = _on_one_device(q, k, v, cu_seqlens_q, cu_k)
+    strides = [_rows(t, n) for t, n in ((q, "q"), (k, "k"), (v, "v"))]
+    if q.dtype not in (torch.float16, torch.bfloat16) or k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("q, k, v must share one dtype, float16 or bfloat16")
+    if v.shape != k.shape or k.shape[2] != q.shape[2] or k.shape[1] == 0 or q.shape[1] % k.shape[1]:
+        raise ValueError("shapes: q [Tq, Hq, d], k/v [Tk, Hkv, d], Hq % Hkv == 0")
+    if cu_seqlens_k is None and k.shape[0] != q.shape[0]:
+        raise ValueError("without cu_seqlens_k, k and v must have q's tokens")
+    B = cu_seqlens_q.numel() - 1
+    _offsets(cu_seqlens_q, B, "cu_seqlens_q")
+    _offsets(cu_k, B, "cu_seqlens_k")
+    T, Hq, d = q.shape
+    scale, out, lse, workspace, mine = _extend_out(dev, q, B, k.shape[1], scale, out_dtype, out, lse, return_lse,
+                                                   workspace)
+    with torch.cuda.device(dev):
+        st = load().fd_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens_q), _ptr(cu_k), B, T, k.shape[0], Hq,
+                               k.shape[1], d, *strides, DTYPE_CODE[q.dtype], int(bool(causal)), float(scale),
+                               _ptr(out), DTYPE_CODE[out.dtype], _ptr(lse), _ptr(workspace),
+                               workspace.numel() * workspace.element_size(), _stream(q, stream))
+    _check(st, "fd_prefill")
+    _keep(dev, stream, *mine)
+    return out, lse
+
+
+def _extend_args(q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens):
+    q_stride = _rows(q, "q")
+    if q.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("q must be float16 or bfloat16")
+    _need_cuda(k_pages, v_pages)
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype:
+        raise ValueError("k_pages/v_pages must be [num_pages, Hkv, page_size, d]")
+    num_pages, Hkv, page_size, d = k_pages.shape
+    if q.shape[2] != d or Hkv == 0 or q.shape[1] % Hkv:
+        raise ValueError("q must be [T, Hq, d] with Hq a multiple of the pages' Hkv")
+    B = seqlens.shape[0] if seqlens.dim() == 1 else -1
+    _int32(seqlens, (B,), "seqlens")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be int32 [B, max_pages]")
+    _int32(block_table, (B, block_table.shape[1]), "block_table")
+    _offsets(cu_seqlens_q, B, "cu_seqlens_q")
+    return B, q_stride, num_pages, Hkv, page_size
+
+
+def extend_paged(q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens, scale=None, out_dtype=None, out=None,
+                 lse=None, return_lse=True, workspace=None, stream=None):
+    """Attention of new tokens over a paged cache that holds them already
+    (fd_extend_paged).  Returns ``(out, lse)``.
+
+    q [T, Hq, d] float16 or bfloat16, sequence b's new tokens at rows
+    cu_seqlens_q[b] .. cu_seqlens_q[b+1]-1; k_pages/v_pages [num_pages, Hkv,
+    page_size, d] of q's dtype, page_size a multiple of 16; block_table int32
+    [B, max_pages]; seqlens int32 [B], the new tokens included.  A
+    sequence's last new token sees all seqlens[b] tokens, the one before all
+    but the last, and so on.
+    """
+    dev = _on_one_device(q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens)
+    B, q_stride, num_pages, Hkv, page_size = _extend_args(q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens)
+    if k_pages.dtype != q.dtype:
+        raise ValueError("the pages must have q's dtype")
+    T, Hq, d = q.shape
+    scale, out, lse, workspace, mine = _extend_out(dev, q, B, Hkv, scale, out_dtype, out, lse, return_lse, workspace)
+    with torch.cuda.device(dev):
+        st = load().fd_extend_paged(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(cu_seqlens_q),
+                                    _ptr(seqlens), B, T, Hq, Hkv, d, q_stride, page_size, block_table.shape[1],
+                                    num_pages, DTYPE_CODE[q.dtype], float(scale), _ptr(out), DTYPE_CODE[out.dtype],
+                                    _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                    _stream(q, stream))
+    _check(st, "fd_extend_paged")
+    _keep(dev, stream, *mine)
+    return out, lse
+
+
+def extend_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, cu_seqlens_q, seqlens, scale=None,
+                     out_dtype=None, out=None, lse=None, return_lse=True, workspace=None, stream=None):
+    """extend_paged over E4M3 pages (fd_extend_paged_fp8): pages
+    torch.float8_e4m3fn (or uint8 E4M3 bytes), k_scale, v_scale float32
+    [B, Hkv].  Returns ``(out, lse)``."""
+    dev = _on_one_device(q, k_pages, v_pages, k_scale, v_scale, block_table, cu_seqlens_q, seqlens)
+    B, q_stride, num_pages, Hkv, page_size = _extend_args(q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens)
+    if k_pages.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise ValueError("pages must be float8_e4m3fn (or uint8 E4M3 bytes)")
+    _need_cuda(k_scale, v_scale)
+    for t in (k_scale, v_scale):
+        if t.dtype != torch.float32 or t.shape != (B, Hkv):
+            raise ValueError("k_scale/v_scale must be float32 [B, Hkv]")
+    T, Hq, d = q.shape
+    scale, out, lse, workspace, mine = _extend_out(dev, q, B, Hkv, scale, out_dtype, out, lse, return_lse, workspace)
+    with torch.cuda.device(dev):
+        st = load().fd_extend_paged_fp8(_ptr(q), DTYPE_CODE[q.dtype], _ptr(k_pages), _ptr(v_pages), _ptr(k_scale),
+                                        _ptr(v_scale), _ptr(block_table), _ptr(cu_seqlens_q), _ptr(seqlens), B, T,
+                                        Hq, Hkv, d, q_stride, page_size, block_table.shape[1], num_pages,
+                                        float(scale), _ptr(out), DTYPE_CODE[out.dtype], _ptr(lse), _ptr(workspace),
+                                        workspace.numel() * workspace.element_size(), _stream(q, stream))
+    _check(st, "fd_extend_paged_fp8")
+    _keep(dev, stream, *mine)
+    return out, lse
+
+
 def decode_split(q, k, v, num_splits, seqlens=None, scale=None, stream=None, o_part=None,
                  m_part=None, l_part=None, lse_part=None):
     """Stage 1 alone (fd_decode_split).  Returns ``(o_part, m_part, l_part, lse_part)``.
@@ -628,5 +936,6 @@ def selftest_wait_timeout(stream=None) -> None:
 
 
 def device_status(reset: bool = True) -> int:
-    """FD_OK, or FD_ERR_DEVICE_TIMEOUT if a kernel gave up waiting (synchronises)."""
+    """FD_OK, or what a kernel recorded: FD_ERR_DEVICE_TIMEOUT, FD_ERR_BAD_PAGE
+    or FD_ERR_BAD_OFFSETS (synchronises)."""
     return load().fd_device_status(1 if reset else 0)
