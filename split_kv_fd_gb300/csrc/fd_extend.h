@@ -1,27 +1,63 @@
-// fd_extend.h -- parameter block and launcher of attention with several new
-// tokens a sequence (fd_extend.cuh): over a paged cache, or over packed
-// prompts.
+// fd_extend.h -- parameter block, plan and launchers of attention with
+// several new tokens a sequence (fd_extend.cuh): over a paged cache, or over
+// packed prompts.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
 
 namespace fd {
 
+// A tile's MMA rows are (token, query head of the slice) pairs, token major:
+// two sub-tiles of EXT_M rows, each of EXT_M / Gs tokens.
+constexpr int EXT_M = 128;
+// Keys per block.
+constexpr int EXT_CT = 128;
+// Boxes of a paged K/V block: at most EXT_CT / 16 row groups.
+constexpr int EXT_MIN_PAGE = 16;
+
+// One tile of a sequence's new tokens, written by the plan.
+struct ExtTile {
+    int row0;    // first token's row of q and out
+    int ntok;    // tokens
+    int b;       // sequence
+    int m;       // its keys
+    int lim;     // keys that the tile's first token sees (may be negative)
+    int k0;      // packed K/V: first row
+    int nblk;    // blocks of EXT_CT keys that any of its tokens sees
+    int pad;
+};
+
+// Where a CTA's share of the split tiles begins: an item (tile, virtual
+// head), the offset in it in cost units, and the block that offset lies in.
+struct ExtCut {
+    int item, off, blk, pad;
+};
+
+struct ExtPlanHeader {
+    int n_items;   // tiles * virtual heads
+    int waves;     // whole items each CTA takes: item w * grid + c (odd w: from the far end)
+};
+
 struct ExtendParams {
+    CUtensorMap tmq, tmk, tmv;
     const void *q;           // [total_q, Hq, d], q_stride elements between tokens
     long long q_stride;
     const void *k, *v;       // packed [total_k, Hkv, d] with strides, or pages [num_pages, Hkv, page_size, d]
     long long k_stride, v_stride;
-    int paged;
-    const int32_t *table;    // [B, max_pages]
-    int page_size, max_pages;
+    const int32_t *table;    // [B, max_pages] (paged)
+    int paged, page_size, max_pages;
+    int box_rows;            // rows of a K/V box
     long long num_pages;
     const int32_t *cu_q;     // [B + 1] rows of q
     const int32_t *cu_k;     // [B + 1] rows of k, v (packed)
     const int32_t *seqlens;  // [B] tokens in the cache, the new ones among them (paged)
     int B, total_q, total_k, Hq, Hkv, d;
+    int G;                   // query heads per K/V head
+    int NG, Gs;              // slices of a K/V head's query heads, heads per slice
+    int tps;                 // tokens per sub-tile
     int causal;
     float scale_log2;        // scale * log2(e): scores are kept in base 2
     int f8;                  // E4M3 K/V
@@ -31,8 +67,24 @@ struct ExtendParams {
     int out_dtype;
     float *lse;              // [total_q, Hq] or null
     unsigned *status;
+    // workspace
+    int grid, max_tiles;
+    ExtPlanHeader *header;
+    int *tile_start;         // [B + 1]
+    ExtTile *tiles;          // [max_tiles] by descending cost
+    long long *cost_sum;     // [max_tiles + 1] costs before, over the virtual heads
+    ExtCut *cuts;            // [grid + 1]
+    float *part_o;           // [slots][2 * EXT_M][d] sums of weights times V
+    float2 *part_ml;         // [slots][2 * EXT_M] (reference max, sum of weights)
 };
 
-cudaError_t launch_extend(const ExtendParams &p, cudaStream_t s);
+// Partial results: the piece that ends at a cut and the one that starts there.
+inline int ext_slots(int grid) { return 2 * (grid + 1); }
+
+cudaError_t launch_extend_e4m3(const ExtendParams &p, cudaStream_t s);
+cudaError_t launch_extend_plan(const ExtendParams &p, cudaStream_t s);
+cudaError_t launch_extend_bf16(const ExtendParams &p, cudaStream_t s);
+cudaError_t launch_extend_f16(const ExtendParams &p, cudaStream_t s);
+cudaError_t launch_extend_merge(const ExtendParams &p, cudaStream_t s);
 
 }  // namespace fd

@@ -1,4 +1,4 @@
-// fd_extend.cu -- attention with several new tokens a sequence: token t of
+// fd_extend_e4m3.cu -- attention with several new tokens a sequence: token t of
 // sequence b, the i-th of its n new ones over m keys, sees the keys below
 // m - n + i + 1 (causal) or all m,
 //     out = softmax(scale q K^T) V,   lse = ln sum exp(scale q K^T),
@@ -15,7 +15,7 @@ __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float
 __device__ __forceinline__ float to_f(__nv_fp8_e4m3 x) { return (float)x; }
 
 // One warp a (token, query head); lane l holds elements l, l + 32, ...
-template <typename T, typename KT, int D> __global__ void extend_kernel(const ExtendParams p)
+template <typename T, typename KT, int D> __global__ void extend_simple_kernel(const ExtendParams p)
 {
     constexpr int E = D / 32;
     const int lane = threadIdx.x & 31;
@@ -96,15 +96,14 @@ template <typename T, typename KT, int D> __global__ void extend_kernel(const Ex
 
 template <typename T> cudaError_t launch_t(const ExtendParams &p, cudaStream_t s)
 {
-    auto kern = p.d == 64 ? (p.f8 ? extend_kernel<T, __nv_fp8_e4m3, 64> : extend_kernel<T, T, 64>)
-                          : (p.f8 ? extend_kernel<T, __nv_fp8_e4m3, 128> : extend_kernel<T, T, 128>);
+    auto kern = p.d == 64 ? extend_simple_kernel<T, __nv_fp8_e4m3, 64> : extend_simple_kernel<T, __nv_fp8_e4m3, 128>;
     kern<<<p.total_q, 256, 0, s>>>(p);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_extend(const ExtendParams &p, cudaStream_t s)
+cudaError_t launch_extend_e4m3(const ExtendParams &p, cudaStream_t s)
 {
     return p.dtype == 1 ? launch_t<__half>(p, s) : launch_t<__nv_bfloat16>(p, s);
 }

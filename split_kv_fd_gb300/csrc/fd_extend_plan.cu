@@ -1,0 +1,376 @@
+// fd_extend_plan.cu -- what the attention of new tokens runs before and after
+// its main kernel: the plan, made on the GPU from the sequences' lengths,
+// and the merge of the tiles that were split over their keys.
+//
+// A tile costs its blocks of keys plus EXT_START for its queries, its result
+// and the pipeline's refill.  Items (tile, virtual head) are dealt in
+// descending cost: whole waves of one item a CTA, back and forth, as long as
+// no CTA gets more than its even share of the total; what is left is cut
+// into pieces that fill every CTA up to that share, at any block.  So few
+// long tiles (a few drafted tokens over a long cache) are split over all
+// SMs, many are mostly whole, and neighbours in a wave stream the same K/V.
+// Everything follows from prefix sums in a fixed order: the split, and with
+// it every rounding, is the same in every run.
+#include "fd_device.cuh"
+#include "fd_extend.h"
+
+namespace fd {
+namespace {
+
+constexpr int PT = 1024;        // threads of the planning CTA
+constexpr int PW = PT / 32;
+constexpr int BUCKETS = 64;     // of the sort by cost
+constexpr int EXT_START = 2;    // cost of an item beside its blocks, in blocks
+constexpr int EXT_MIN_CUT = 3;  // a share of the cut items is at least this cost
+
+__device__ __forceinline__ long long scan_block(long long x, long long *warp_sums, long long &total)
+{
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(FULL_MASK, x, o);
+        if (lane >= o)
+            x += y;
+    }
+    __syncthreads();   // the sums of the previous call have been read
+    if (lane == 31)
+        warp_sums[w] = x;
+    __syncthreads();
+    if (w == 0) {
+        long long s = warp_sums[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(FULL_MASK, s, o);
+            if (lane >= o)
+                s += y;
+        }
+        warp_sums[lane] = s;
+    }
+    __syncthreads();
+    total = warp_sums[31];
+    return x + (w ? warp_sums[w - 1] : 0);
+}
+
+__device__ __forceinline__ int max_block(int x, int *warp_max)
+{
+    x = __reduce_max_sync(FULL_MASK, x);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0)
+        warp_max[threadIdx.x >> 5] = x;
+    __syncthreads();
+    return __reduce_max_sync(FULL_MASK, warp_max[threadIdx.x & 31]);
+}
+
+// Sequence b's rows of q, clamped; true if the offsets had to be.
+__device__ __forceinline__ bool q_rows(const ExtendParams &p, int b, int &lo, int &n)
+{
+    const int a = p.cu_q[b], e = p.cu_q[b + 1];
+    lo = min(max(a, 0), p.total_q);
+    n = min(max(e, lo), p.total_q) - lo;
+    return lo != a || lo + n != e;
+}
+
+// Its keys, likewise.
+__device__ __forceinline__ bool k_rows(const ExtendParams &p, int b, int &lo, int &m)
+{
+    if (p.paged) {
+        lo = 0;
+        m = (int)min((long long)max(p.seqlens[b], 0), (long long)p.page_size * p.max_pages);
+        return false;
+    }
+    const int a = p.cu_k[b], e = p.cu_k[b + 1];
+    lo = min(max(a, 0), p.total_k);
+    m = min(max(e, lo), p.total_k) - lo;
+    return lo != a || lo + m != e;
+}
+
+// Tile i (of all, in order of the sequences).
+__device__ __forceinline__ ExtTile tile_at(const ExtendParams &p, int i)
+{
+    int lo = 0, hi = p.B - 1;   // the last b with tile_start[b] <= i
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.tile_start[mid] <= i)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    ExtTile t;
+    int r, n;
+    q_rows(p, lo, r, n);
+    k_rows(p, lo, t.k0, t.m);
+    const int first = (i - p.tile_start[lo]) * 2 * p.tps;
+    t.b = lo;
+    t.row0 = r + first;
+    t.ntok = min(2 * p.tps, n - first);
+    // a token that sees nothing counts as negative or 0; m - n + first + 1 fits
+    t.lim = p.causal ? t.m - n + first + 1 : t.m;
+    const int see = p.causal ? min(t.m, t.lim + t.ntok - 1) : t.m;
+    t.nblk = see > 0 ? (see + EXT_CT - 1) / EXT_CT : 0;
+    t.pad = 0;
+    return t;
+}
+
+__global__ void __launch_bounds__(PT, 1) extend_plan_kernel(const ExtendParams p)
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __shared__ long long sums[32];
+    __shared__ int maxs[32];
+    __shared__ int hist[BUCKETS * PW];   // bucket-major, then warp
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    const int Hv = p.Hkv * p.NG;
+    const int tt = 2 * p.tps;
+
+    // tiles before each sequence, and the most blocks of any tile
+    long long tiles = 0;
+    int top = 0;
+    bool bad = false;
+    for (int b0 = 0; b0 < p.B; b0 += PT) {
+        const int b = b0 + tid;
+        long long nt = 0, total;
+        if (b < p.B) {
+            int lo, n, k0, m;
+            bad |= q_rows(p, b, lo, n);
+            bad |= k_rows(p, b, k0, m);
+            nt = (n + tt - 1) / tt;
+            if (n > 0)
+                top = max(top, (m + EXT_CT - 1) / EXT_CT);
+        }
+        const long long s = tiles + scan_block(nt, sums, total);
+        tiles += total;
+        if (b < p.B)
+            p.tile_start[b] = (int)min(s - nt, (long long)p.max_tiles);
+    }
+    if (bad)
+        atomicOr(p.status, STATUS_BAD_OFFSETS);
+    const int n = (int)min(tiles, (long long)p.max_tiles);   // fewer only if offsets overlap
+    top = max(1, max_block(top, maxs));
+
+    // stable counting sort by descending cost, each warp its share in order
+    for (int i = tid; i < BUCKETS * PW; i += PT)
+        hist[i] = 0;
+    __syncthreads();
+    const int share = ((n + PW - 1) / PW + 31) & ~31;
+    const int i0 = w * share, i1 = min(n, i0 + share);
+    for (int i = i0; i < i1; i += 32) {
+        const bool on = i + lane < i1;
+        const int key = on ? BUCKETS - 1 - (int)((long long)tile_at(p, i + lane).nblk * (BUCKETS - 1) / top) : BUCKETS;
+        const unsigned same = __match_any_sync(FULL_MASK, key);
+        if (on && lane == __ffs(same) - 1)
+            hist[key * PW + w] += __popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+    {
+        const int h0 = hist[2 * tid], h1 = hist[2 * tid + 1];
+        long long total;
+        const int s = (int)scan_block(h0 + h1, sums, total);
+        hist[2 * tid] = s - h0 - h1;
+        hist[2 * tid + 1] = s - h1;
+    }
+    static_assert(BUCKETS * PW == 2 * PT, "two counts a thread");
+    __syncthreads();
+    for (int i = i0; i < i1; i += 32) {
+        const bool on = i + lane < i1;
+        ExtTile t = {};
+        int key = BUCKETS;
+        if (on) {
+            t = tile_at(p, i + lane);
+            key = BUCKETS - 1 - (int)((long long)t.nblk * (BUCKETS - 1) / top);
+        }
+        const unsigned same = __match_any_sync(FULL_MASK, key);
+        int at = 0;
+        if (on)
+            at = hist[key * PW + w] + __popc(same & ((1u << lane) - 1));
+        __syncwarp();
+        if (on) {
+            p.tiles[at] = t;
+            if (lane == __ffs(same) - 1)
+                hist[key * PW + w] += __popc(same);
+        }
+        __syncwarp();
+    }
+    __syncthreads();
+
+    // costs before each tile, over its virtual heads
+    long long all = 0;
+    for (int j0 = 0; j0 < n; j0 += PT) {
+        const int j = j0 + tid;
+        long long total;
+        const long long c = j < n ? (long long)Hv * (p.tiles[j].nblk + EXT_START) : 0;
+        const long long s = all + scan_block(c, sums, total);
+        all += total;
+        if (j < n)
+            p.cost_sum[j] = s - c;
+    }
+    if (tid == 0)
+        p.cost_sum[n] = all;
+    __syncthreads();
+
+    // whole waves, as many as leave every CTA within its even share
+    const int G = p.grid;
+    const long long items = (long long)n * Hv;
+    const long long even = (all + G - 1) / G;
+    int waves = (int)(items / G);
+    if (n > 0 && p.tiles[0].nblk + EXT_START > even)
+        waves = 0;
+    int load = 0;
+    auto cost_of = [&](int wave) {
+        const long long it = (long long)wave * G + ((wave & 1) ? G - 1 - tid : tid);
+        return p.tiles[it / Hv].nblk + EXT_START;
+    };
+    if (tid < G) {
+#pragma unroll 4
+        for (int x = 0; x < waves; ++x)
+            load += cost_of(x);
+    }
+    while (waves > 0 && max_block(load, maxs) > even) {
+        --waves;
+        if (tid < G)
+            load -= cost_of(waves);
+    }
+
+    // what is left, cut so that every CTA reaches the even share
+    const long long first = (long long)waves * G;
+    const int jf = (int)(first / Hv), hf = (int)(first % Hv);
+    const long long base = jf < n ? p.cost_sum[jf] + (long long)hf * (p.tiles[jf].nblk + EXT_START) : all;
+    const long long rest = all - base;
+    long long cap = 0;
+    if (tid < G) {
+        if (rest < (long long)EXT_MIN_CUT * G) {
+            // slivers are not worth a merge: fewer, even shares
+            const long long g = max(1LL, rest / EXT_MIN_CUT);
+            cap = tid < g ? (rest + g - 1) / g : 0;
+        } else {
+            cap = even - load;
+        }
+    }
+    long long total;
+    const long long cut = min(rest, scan_block(cap, sums, total) - cap) + base;
+    if (tid <= G) {
+        const long long v = tid < G ? cut : all;
+        ExtCut c = {(int)items, 0, 0, 0};
+        if (v < all) {
+            int lo = 0, hi = n - 1;   // the last tile with cost_sum <= v
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (p.cost_sum[mid] <= v)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            const int cost = p.tiles[lo].nblk + EXT_START;
+            const long long in = v - p.cost_sum[lo];
+            c.item = lo * Hv + (int)(in / cost);
+            c.off = (int)(in % cost);
+            c.blk = max(0, c.off - EXT_START);
+        }
+        p.cuts[tid] = c;
+    }
+    if (tid == 0) {
+        p.header->n_items = (int)items;
+        p.header->waves = waves;
+    }
+}
+
+// The merge of the split items: CTA (c, y) joins the pieces of the item whose
+// first cut is c, rows y * MROWS on, a warp a row, in the order of the cuts:
+//     M = max m_i,  out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.
+constexpr int MROWS = 16;
+
+template <int D> __global__ void __launch_bounds__(128) extend_merge_kernel(const ExtendParams p)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int c0 = blockIdx.x + 1;   // cuts 1 .. grid - 1 may lie inside an item
+    const ExtCut cut = p.cuts[c0];
+    if (cut.blk == 0)
+        return;
+    if (c0 > 1) {
+        const ExtCut before = p.cuts[c0 - 1];
+        if (before.item == cut.item && before.blk > 0)
+            return;   // not the item's first cut
+    }
+    int c1 = c0 + 1;   // the cuts inside the item: [c0, c1)
+    while (c1 < p.grid && p.cuts[c1].item == cut.item && p.cuts[c1].blk > 0)
+        ++c1;
+    const int Hv = p.Hkv * p.NG;
+    const ExtTile t = p.tiles[cut.item / Hv];
+    const int vh = cut.item % Hv, h = vh / p.NG, s = vh % p.NG;
+    const int gv = min(p.Gs, p.G - s * p.Gs), hq0 = h * p.G + s * p.Gs;
+    const float vs = p.f8 ? p.v_scale[(long long)t.b * p.Hkv + h] : 1.f;
+    const int lane = threadIdx.x & 31;
+    constexpr int E = D / 32;
+    for (int r = blockIdx.y * MROWS + (threadIdx.x >> 5); r < (int)(blockIdx.y + 1) * MROWS; r += 4) {
+        const int in = r % EXT_M, tok = r / EXT_M * p.tps + in / p.Gs, g = in % p.Gs;
+        if (in >= p.tps * p.Gs || tok >= t.ntok || g >= gv)
+            continue;
+        float o[E], M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            o[e] = 0.f;
+#pragma unroll 4
+        for (int i = c0 - 1; i < c1; ++i) {
+            // the piece left of the first cut, then the one right of each
+            // (none where two cuts coincide)
+            const int slot = i < c0 ? 2 * c0 : 2 * i + 1;
+            const bool some = i < c0 || p.cuts[i + 1].item != cut.item || p.cuts[i + 1].blk > p.cuts[i].blk;
+            if (!some)
+                continue;
+            const long long row = (long long)slot * 2 * EXT_M + r;
+            const float2 ml = __ldcg(p.part_ml + row);
+            float v[E];
+            const float *src = p.part_o + row * D + lane * E;
+            if (E == 4) {
+                const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
+                v[0] = x.x, v[1] = x.y, v[E - 2] = x.z, v[E - 1] = x.w;
+            } else {
+                const float2 x = __ldcg(reinterpret_cast<const float2 *>(src));
+                v[0] = x.x, v[1] = x.y;
+            }
+            if (!(ml.y <= 0.f)) {
+                const float mn = fmaxf(M, ml.x);
+                const float a = ex2(M - mn), b = ex2(ml.x - mn);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    o[e] = fmaf(b, v[e], a * o[e]);
+                L = fmaf(L, a, b * ml.y);
+                M = mn;
+            }
+        }
+        const long long qrow = (long long)(t.row0 + tok) * p.Hq + hq0 + g;
+        const bool any = !(L <= 0.f);   // NaN counts: it is the result then
+        const float inv = any ? vs / L : 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            store_out(p.out, qrow * D + lane * E + e, p.out_dtype, any ? o[e] * inv : 0.f);
+        if (p.lse && lane == 0)
+            p.lse[qrow] = any ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_extend_plan(const ExtendParams &p, cudaStream_t s)
+{
+    extend_plan_kernel<<<1, PT, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_extend_merge(const ExtendParams &p, cudaStream_t s)
+{
+    if (p.grid < 2)
+        return cudaSuccess;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.grid - 1, 2 * EXT_M / MROWS);
+    cfg.blockDim = dim3(128);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return p.d == 64 ? cudaLaunchKernelEx(&cfg, extend_merge_kernel<64>, p)
+                     : cudaLaunchKernelEx(&cfg, extend_merge_kernel<128>, p);
+}
+
+}  // namespace fd

@@ -45,20 +45,123 @@ fd_status check_extend_pointers(const ExtendParams &p)
     return FD_OK;
 }
 
+// A map of 16-bit elements [64, n1, n2, d/64 planes] with boxes [64, box1,
+// box2, 1] and the 128-byte swizzle; strides in bytes.
+bool map_16bit(CUtensorMap *m, const void *base, int dtype, int d, long long n1, long long s1, long long n2,
+               long long s2, int box1, int box2)
+{
+    EncodeTiledFn fn = encode_tiled();
+    if (!fn)
+        return false;
+    const cuuint64_t dims[4] = {64, (cuuint64_t)n1, (cuuint64_t)n2, (cuuint64_t)(d / 64)};
+    const cuuint64_t strides[3] = {(cuuint64_t)s1, (cuuint64_t)s2, 128};
+    const cuuint32_t box[4] = {64, (cuuint32_t)box1, (cuuint32_t)box2, 1};
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    return fn(m, dtype == FD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+              const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The slices, the tiles and the workspace of a call.
+struct ExtLayout {
+    int G, NG, Gs, tps, grid;
+    long long max_tiles;
+    size_t header, tile_start, tiles, cost_sum, cuts, part_ml, part_o, total;
+};
+
+bool ext_layout(int B, int total_q, int Hq, int Hkv, int d, ExtLayout &l)
+{
+    if (B < 0 || total_q < 0 || Hkv <= 0 || Hq < 0 || Hq % Hkv != 0 || (d != 64 && d != 128))
+        return false;
+    const int sms = sm_count();
+    if (sms <= 0)
+        return false;
+    l.grid = sms < 1023 ? sms : 1023;   // the plan deals in one CTA of 1024 threads
+    l.G = Hq > 0 ? Hq / Hkv : 1;
+    l.NG = (l.G + EXT_M - 1) / EXT_M;
+    l.Gs = (l.G + l.NG - 1) / l.NG;
+    l.tps = EXT_M / l.Gs;
+    l.max_tiles = total_q / (2 * l.tps) + (long long)B;
+    const long long slots = ext_slots(l.grid);
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t was = at;
+        at += round_up(bytes, 256);
+        return was;
+    };
+    l.header = take(sizeof(ExtPlanHeader));
+    l.tile_start = take((size_t)(B + 1) * sizeof(int));
+    l.tiles = take((size_t)l.max_tiles * sizeof(ExtTile));
+    l.cost_sum = take((size_t)(l.max_tiles + 1) * sizeof(long long));
+    l.cuts = take((size_t)(l.grid + 1) * sizeof(ExtCut));
+    l.part_ml = take((size_t)slots * 2 * EXT_M * sizeof(float2));
+    l.part_o = take((size_t)slots * 2 * EXT_M * d * sizeof(float));
+    l.total = at;
+    return l.max_tiles * Hkv * l.NG <= INT_MAX;
+}
+
 fd_status run_extend(ExtendParams &p, float scale, void *workspace, size_t workspace_bytes, void *stream)
 {
     p.scale_log2 = scale * 1.4426950408889634f;
     if (!(p.scale_log2 > 0.f) || isinf(p.scale_log2))
         return FD_ERR_INVALID_ARG;
-    const size_t need = fd_workspace_size_extend(p.B, p.total_q, p.Hq, p.Hkv, p.d);
-    if (need == 0)
+    if (sm_count() <= 0)
         return FD_ERR_CUDA;
-    if (!workspace || workspace_bytes < need || !aligned(workspace, 256))
+    ExtLayout l;
+    if (!ext_layout(p.B, p.total_q, p.Hq, p.Hkv, p.d, l))
+        return FD_ERR_UNSUPPORTED;   // more tiles than a 32-bit count
+    if (!workspace || workspace_bytes < l.total || !aligned(workspace, 256))
         return FD_ERR_WORKSPACE;
     p.status = status_ptr();
     if (!p.status)
         return FD_ERR_CUDA;
-    return launch_extend(p, stream_of(stream)) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
+    const cudaStream_t cs = stream_of(stream);
+    if (p.f8)
+        return launch_extend_e4m3(p, cs) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
+
+    p.G = l.G;
+    p.NG = l.NG;
+    p.Gs = l.Gs;
+    p.tps = l.tps;
+    p.grid = l.grid;
+    p.max_tiles = (int)l.max_tiles;
+    char *ws = static_cast<char *>(workspace);
+    p.header = reinterpret_cast<ExtPlanHeader *>(ws + l.header);
+    p.tile_start = reinterpret_cast<int *>(ws + l.tile_start);
+    p.tiles = reinterpret_cast<ExtTile *>(ws + l.tiles);
+    p.cost_sum = reinterpret_cast<long long *>(ws + l.cost_sum);
+    p.cuts = reinterpret_cast<ExtCut *>(ws + l.cuts);
+    p.part_ml = reinterpret_cast<float2 *>(ws + l.part_ml);
+    p.part_o = reinterpret_cast<float *>(ws + l.part_o);
+
+    const long long row = (long long)p.d * 2;
+    bool ok = map_16bit(&p.tmq, p.q, p.dtype, p.d, p.Hq, row, p.total_q, p.q_stride * 2, p.Gs, p.tps);
+    if (p.paged) {
+        p.box_rows = EXT_MIN_PAGE;   // the largest power of two up to a block that divides the page
+        while (p.box_rows < EXT_CT && p.page_size % (2 * p.box_rows) == 0)
+            p.box_rows *= 2;
+    }
+    if (p.paged ? p.max_pages > 0 : p.total_k > 0) {
+        for (int i = 0; i < 2; ++i) {
+            CUtensorMap *m = i ? &p.tmv : &p.tmk;
+            const void *x = i ? p.v : p.k;
+            ok = ok && (p.paged ? map_16bit(m, x, p.dtype, p.d, p.page_size, row, p.num_pages * p.Hkv,
+                                            row * p.page_size, p.box_rows, 1)
+                                : map_16bit(m, x, p.dtype, p.d, p.total_k, (i ? p.v_stride : p.k_stride) * 2, p.Hkv,
+                                            row, EXT_CT, 1));
+        }
+    } else {
+        p.tmk = p.tmv = p.tmq;   // no key anywhere: never used
+    }
+    if (!ok)
+        return FD_ERR_CUDA;
+    cudaError_t e = launch_extend_plan(p, cs);
+    if (e == cudaSuccess)
+        e = p.dtype == FD_BF16 ? launch_extend_bf16(p, cs) : launch_extend_f16(p, cs);
+    if (e == cudaSuccess)
+        e = launch_extend_merge(p, cs);
+    return e == cudaSuccess ? FD_OK : FD_ERR_CUDA;
 }
 
 fd_status extend_paged(const void *q, fd_dtype q_dtype, const void *k_pages, const void *v_pages,
@@ -118,9 +221,8 @@ extern "C" {
 
 size_t fd_workspace_size_extend(int B, int total_q, int Hq, int Hkv, int d)
 {
-    if (B < 0 || total_q < 0 || Hkv <= 0 || Hq < 0 || Hq % Hkv != 0 || (d != 64 && d != 128))
-        return 0;
-    return 256;
+    ExtLayout l;
+    return ext_layout(B, total_q, Hq, Hkv, d, l) ? l.total : 0;
 }
 
 fd_status fd_prefill(const void *q, const void *k, const void *v, const int32_t *cu_q, const int32_t *cu_k, int B,
