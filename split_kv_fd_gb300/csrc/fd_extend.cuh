@@ -20,12 +20,16 @@
 // before, so that S's commit also says that P.V is done: a row's rescale
 // needs no wait of its own.
 //
-// Warp roles (384 threads, one CTA per SM):
+// Warp roles (384 threads, 512 for E4M3 K/V, one CTA per SM):
 //  - warps 0-3, 4-7: softmax and results of sub-tile A, B;
 //  - warp 8: K and V by tensor-map TMA, in turn, into one ring;
 //  - warp 9: allocates TMEM, issues every MMA;
 //  - warp 10: Q by TMA, as soon as a sub-tile's last S is done;
-//  - warp 11: walks the CTA's share of the plan, segments into a small ring.
+//  - warp 11: walks the CTA's share of the plan, segments into a small ring;
+//  - E4M3 only, warps 12-15: widen the blocks that warp 8 copied as they are
+//    to the 16-bit type (exact: E4M3 has 4 significant bits and exponents
+//    from -9 to 8) for the same products.  The K scale is part of the
+//    score's, the V scale of the result's.
 // Every hand-off is an mbarrier, and every wait is bounded: on expiry a role
 // records FD_ERR_DEVICE_TIMEOUT, stops, waits for the copies it issued, and
 // the CTA frees its TMEM.
@@ -37,16 +41,24 @@
 
 namespace fd {
 
-template <typename T, int D> struct ExtCfg {
+template <typename T, int D, bool F8> struct ExtCfg {
     static constexpr int M = EXT_M, CT = EXT_CT;
     static constexpr int PLANES = D / 64;                // 128-byte planes of a row
     static constexpr int PLANE = CT * 128;               // one plane of a block, or of a sub-tile's Q
     static constexpr int BLOCK_BYTES = PLANES * PLANE;   // K or V of one block
     static constexpr int Q_BYTES = PLANES * PLANE;       // one sub-tile
-    static constexpr int STAGES = D == 128 ? 5 : 10;     // 160 KB of K and V in flight
+    // 16-bit K and V: 160 KB of copies in flight.  E4M3: the copies land in
+    // a ring of raw blocks, and two 16-bit stages (one K, one V) suffice.
+    static constexpr int STAGES = F8 ? (D == 128 ? 2 : 4) : (D == 128 ? 5 : 10);
+    static constexpr int RAW_BYTES = CT * D;             // an E4M3 block
+    static constexpr int RAWS = F8 ? (D == 128 ? 6 : 12) : 0;
     static constexpr int SEGS = 4;                       // segments the scheduler runs ahead
-    static constexpr int KV_WARP = 8, MMA_WARP = 9, Q_WARP = 10, SCHED_WARP = 11;
-    static constexpr int THREADS = 384;
+    static constexpr int KV_WARP = 8, MMA_WARP = 9, Q_WARP = 10, SCHED_WARP = 11, CVT_WARP = 12;
+    static constexpr int THREADS = F8 ? 512 : 384;
+    // registers a thread: the softmax warpgroups hold a row of S each; the
+    // shares add up to the launch's (168 x 384 and 128 x 512)
+    static constexpr int REGS_SOFTMAX = F8 ? 200 : 208, REGS_OTHER = F8 ? 56 : 88;
+    static_assert(2 * REGS_SOFTMAX + (THREADS / 128 - 2) * REGS_OTHER == (F8 ? 4 * 128 : 3 * 168), "register shares");
     // TMEM columns: S of A and B, O of A and B; P takes the first half of
     // its S (D = 128), or columns of its own where there are some (D = 64)
     static constexpr int TM_O = 2 * CT;
@@ -61,9 +73,10 @@ template <typename T, int D> struct ExtCfg {
     static constexpr float SHIFT = std::is_same<T, __half>::value ? 7.f : 0.f;
     static constexpr uint32_t SLEEP_NS = 100000;
     // barriers: ring full/empty, S, P, O, Q full, Q empty of both sub-tiles,
-    // segments full/empty, the last commit
-    static constexpr int NBAR = 2 * STAGES + 10 + 2 * SEGS + 1;
-    static constexpr int SMEM = 1024 + STAGES * BLOCK_BYTES + 2 * Q_BYTES + NBAR * 8 + 16 + SEGS * 64;
+    // segments full/empty, the last commit, raw ring full/empty
+    static constexpr int NBAR = 2 * STAGES + 10 + 2 * SEGS + 1 + 2 * RAWS;
+    static constexpr int SMEM = 1024 + STAGES * BLOCK_BYTES + RAWS * RAW_BYTES + 2 * Q_BYTES + NBAR * 8 + 16 + SEGS * 64;
+    static_assert(SMEM <= 232448, "shared memory");
 };
 
 // What the roles of a CTA need to know of a segment: a range of K/V blocks
@@ -99,18 +112,53 @@ __device__ __forceinline__ void store_out16(void *out, long long idx, int out_dt
     o[1] = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(ExtCfg<T, D>::THREADS, 1) extend_kernel(const __grid_constant__ ExtendParams p)
+// 16 E4M3 values as the 16-bit type, exactly: two 16-byte vectors.
+template <typename T> __device__ __forceinline__ void e4m3_widen16(const uint4 &u, uint4 &lo, uint4 &hi)
 {
-    using C = ExtCfg<T, D>;
+    const uint32_t in[4] = {u.x, u.y, u.z, u.w};
+    uint32_t r[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        asm("{\n\t.reg .b16 lo, hi;\n\t"
+            "mov.b32 {lo, hi}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+            : "=r"(r[2 * i]), "=r"(r[2 * i + 1])
+            : "r"(in[i]));
+    }
+    if (std::is_same<T, __nv_bfloat16>::value) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 f = Mma<__half>::unpack(r[i]);
+            r[i] = Mma<__nv_bfloat16>::pack(f.x, f.y);
+        }
+    }
+    lo = make_uint4(r[0], r[1], r[2], r[3]);
+    hi = make_uint4(r[4], r[5], r[6], r[7]);
+}
+
+__device__ __forceinline__ void sts128(uint32_t a, const uint4 &v)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+
+template <int R> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+
+template <typename T, int D, bool F8>
+__global__ void __launch_bounds__(ExtCfg<T, D, F8>::THREADS, 1) extend_kernel(const __grid_constant__ ExtendParams p)
+{
+    using C = ExtCfg<T, D, F8>;
     constexpr int ST = C::STAGES;
     extern __shared__ __align__(128) unsigned char smem_raw[];
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const uint32_t raw = smem_addr(smem_raw);
     unsigned char *smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);   // 1024-aligned
     const uint32_t ring = smem_addr(smem);
-    const uint32_t qbuf = ring + ST * C::BLOCK_BYTES;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + ST * C::BLOCK_BYTES + 2 * C::Q_BYTES);
+    const uint32_t rawring = ring + ST * C::BLOCK_BYTES;
+    const uint32_t qbuf = rawring + C::RAWS * C::RAW_BYTES;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + ST * C::BLOCK_BYTES + C::RAWS * C::RAW_BYTES + 2 * C::Q_BYTES);
     uint32_t *misc = reinterpret_cast<uint32_t *>(bars + C::NBAR);
     volatile ExtSeg *segs = reinterpret_cast<volatile ExtSeg *>(misc + 4);
     static_assert(sizeof(ExtSeg) <= 64, "segment slots");
@@ -126,10 +174,12 @@ __global__ void __launch_bounds__(ExtCfg<T, D>::THREADS, 1) extend_kernel(const 
     auto GFULL = [&](int s) { return bar0 + 8u * (uint32_t)(B0 + 10 + s); };
     auto GEMPTY = [&](int s) { return bar0 + 8u * (uint32_t)(B0 + 10 + C::SEGS + s); };
     const uint32_t FIN = bar0 + 8u * (uint32_t)(B0 + 10 + 2 * C::SEGS);
+    auto RFULL = [&](int s) { return FIN + 8u * (uint32_t)(1 + s); };
+    auto REMPTY = [&](int s) { return FIN + 8u * (uint32_t)(1 + C::RAWS + s); };
 
     if (tid == 0) {
         for (int s = 0; s < ST; ++s) {
-            mbar_init(FULL(s), 1);    // the producer's arrival plus the copy's bytes
+            mbar_init(FULL(s), F8 ? 4 : 1);   // the producer's arrival plus the copy's bytes, or the converting warps
             mbar_init(EMPTY(s), 1);   // commit behind the block's last MMA
         }
         for (int x = 0; x < 2; ++x) {
@@ -141,7 +191,11 @@ __global__ void __launch_bounds__(ExtCfg<T, D>::THREADS, 1) extend_kernel(const 
         }
         for (int s = 0; s < C::SEGS; ++s) {
             mbar_init(GFULL(s), 1);
-            mbar_init(GEMPTY(s), 11); // K/V, MMA, Q and the eight softmax warps
+            mbar_init(GEMPTY(s), F8 ? 15 : 11); // K/V, MMA, Q, the eight softmax warps and the converting ones
+        }
+        for (int s = 0; s < C::RAWS; ++s) {
+            mbar_init(RFULL(s), 1);
+            mbar_init(REMPTY(s), 4);
         }
         mbar_init(FIN, 1);
         prefetch_tmap(&p.tmq);
@@ -188,6 +242,9 @@ __global__ void __launch_bounds__(ExtCfg<T, D>::THREADS, 1) extend_kernel(const 
         return g.valid != 0;
     };
 
+    // (a warpgroup changes its share of the registers as a whole)
+    if (w >= 8) {
+        regs_dec<C::REGS_OTHER>();
     if (w == C::SCHED_WARP) {
         // ------------------------------------------------------------ scheduler
         if (lane == 0) {
@@ -256,7 +313,10 @@ __global__ void __launch_bounds__(ExtCfg<T, D>::THREADS, 1) extend_kernel(const 
         const int R = p.paged ? p.box_rows : C::CT;
         const int ng = C::CT / R;   // row groups (at most 8)
         const int grp = lane % ng, plane = lane / ng;
-        const bool mine = plane < C::PLANES;
+        const bool mine = plane < (F8 ? 1 : C::PLANES);
+        constexpr int NS = F8 ? C::RAWS : ST;
+        auto NFULL = [&](int s) { return F8 ? RFULL(s) : FULL(s); };
+        auto NEMPTY = [&](int s) { return F8 ? REMPTY(s) : EMPTY(s); };
         long long n = 0;            // blocks issued
         ExtSeg g;
         while (!dead && next_seg(g)) {
@@ -278,27 +338,82 @@ __global__ void __launch_bounds__(ExtCfg<T, D>::THREADS, 1) extend_kernel(const 
                     x = tok % p.page_size;
                     y = page * p.Hkv + g.h;
                 }
-                const uint32_t bytes = (uint32_t)__popc(__ballot_sync(FULL_MASK, load)) * (uint32_t)(R * 128);
+                const uint32_t bytes = (uint32_t)__popc(__ballot_sync(FULL_MASK, load)) * (uint32_t)(R * (F8 ? D : 128));
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv, ++n) {
-                    const int s = (int)(n % ST);
-                    if (n >= ST &&
-                        !mbar_wait_bounded_sleep(EMPTY(s), (uint32_t)(((n / ST) - 1) & 1), C::SLEEP_NS)) {
+                    const int s = (int)(n % NS);
+                    if (n >= NS &&
+                        !mbar_wait_bounded_sleep(NEMPTY(s), (uint32_t)(((n / NS) - 1) & 1), C::SLEEP_NS)) {
                         dead = true;
                         break;
                     }
                     if (lane == 0)
-                        mbar_arrive_expect_tx(FULL(s), bytes);
+                        mbar_arrive_expect_tx(NFULL(s), bytes);
                     __syncwarp();
-                    if (load)
-                        tma_load_4d(ring + (uint32_t)(s * C::BLOCK_BYTES + plane * C::PLANE + grp * R * 128),
-                                    kv ? &p.tmv : &p.tmk, 0, x, y, plane, FULL(s));
+                    const CUtensorMap *tm = kv ? &p.tmv : &p.tmk;
+                    if (F8 && load)
+                        tma_load_3d(rawring + (uint32_t)(s * C::RAW_BYTES + grp * R * D), tm, 0, x, y, NFULL(s));
+                    else if (load)
+                        tma_load_4d(ring + (uint32_t)(s * C::BLOCK_BYTES + plane * C::PLANE + grp * R * 128), tm, 0, x, y,
+                                    plane, NFULL(s));
                 }
             }
         }
         // no copy may be in flight when the CTA ends: the last fill of each stage
-        for (long long i = n > ST ? n - ST : 0; i < n; ++i)
-            mbar_wait_bounded_sleep(FULL((int)(i % ST)), (uint32_t)((i / ST) & 1), C::SLEEP_NS);
+        for (long long i = n > NS ? n - NS : 0; i < n; ++i)
+            mbar_wait_bounded_sleep(NFULL((int)(i % NS)), (uint32_t)((i / NS) & 1), C::SLEEP_NS);
+    } else if (F8 && w >= C::CVT_WARP) {
+        // ------------------------------------------------------------ E4M3 to 16 bits
+        // A thread widens 16 values of a row at a time into the swizzled
+        // planes that the MMAs read.  Eight lanes read 128 bytes in a row;
+        // at d = 128 the upper four write the other plane, their two halves
+        // in the other order, so that the eight 16-byte writes of a phase
+        // fall in different banks.
+        constexpr int NR = F8 ? C::RAWS : 1;
+        constexpr int CPR = D / 16;   // 16-value pieces of a row
+        const int ct = tid - C::CVT_WARP * 32;
+        const int c = ct % CPR, r0 = ct / CPR;
+        const bool swap = (c >> 2) != 0;
+        long long n = 0;
+        ExtSeg g;
+        while (!dead && next_seg(g)) {
+            const int end = ext_end(g);
+#pragma unroll 1
+            for (int j = g.blk0; j < end && !dead; ++j) {
+                const int left = g.m - j * C::CT;
+#pragma unroll 1
+                for (int kv = 0; kv < 2; ++kv, ++n) {
+                    const int rs = (int)(n % NR), s = (int)(n % ST);
+                    if (!mbar_wait_bounded_sleep(RFULL(rs), (uint32_t)((n / NR) & 1), C::SLEEP_NS) ||
+                        (n >= ST && !mbar_wait_bounded_sleep(EMPTY(s), (uint32_t)(((n / ST) - 1) & 1), C::SLEEP_NS))) {
+                        dead = true;
+                        break;
+                    }
+                    const uint32_t src = rawring + (uint32_t)(rs * C::RAW_BYTES);
+                    const uint32_t dst = ring + (uint32_t)(s * C::BLOCK_BYTES + (c >> 2) * C::PLANE);
+#pragma unroll 4
+                    for (int r = r0; r < C::CT; r += 128 / CPR) {
+                        uint4 v = lds128(src + (uint32_t)(r * D + c * 16));
+                        // rows behind the sequence's last key may hold
+                        // anything, and 0 * NaN is NaN
+                        if (r >= left)
+                            v = make_uint4(0, 0, 0, 0);
+                        uint4 lo, hi;
+                        e4m3_widen16<T>(v, lo, hi);
+                        const uint32_t a0 = dst + (uint32_t)(r * 128 + (((2 * (c & 3)) ^ (r & 7)) << 4));
+                        const uint32_t a1 = dst + (uint32_t)(r * 128 + (((2 * (c & 3) + 1) ^ (r & 7)) << 4));
+                        sts128(swap ? a1 : a0, swap ? hi : lo);
+                        sts128(swap ? a0 : a1, swap ? lo : hi);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(FULL(s));
+                        mbar_arrive(REMPTY(rs));
+                    }
+                }
+            }
+        }
     } else if (w == C::Q_WARP) {
         // ------------------------------------------------------------ Q
         // A sub-tile's rows: tps tokens of Gs heads each, plane by plane.
@@ -406,7 +521,7 @@ __global__ void __launch_bounds__(ExtCfg<T, D>::THREADS, 1) extend_kernel(const 
                 if (!wait(FULL(vs), vph))
                     break;
                 const int left = g.m - j * C::CT;
-                if (left < C::CT) {
+                if (!F8 && left < C::CT) {
                     // V's rows behind the sequence's last key may hold
                     // anything, and 0 * NaN is NaN: zeros instead
                     const uint32_t vb = ring + (uint32_t)(vs * C::BLOCK_BYTES);
@@ -460,7 +575,9 @@ __global__ void __launch_bounds__(ExtCfg<T, D>::THREADS, 1) extend_kernel(const 
                 dead = true;
         }
         dead = __any_sync(FULL_MASK, dead);
+    }
     } else {
+        regs_inc<C::REGS_SOFTMAX>();
         // ------------------------------------------------------------ softmax
         const int x = w >> 2;              // sub-tile
         const int row = tid & 127;         // its row = TMEM lane
@@ -477,7 +594,7 @@ __global__ void __launch_bounds__(ExtCfg<T, D>::THREADS, 1) extend_kernel(const 
             const int lim = p.causal ? min(g.m, g.lim + min(tok, g.ntok - 1)) : g.m;
             float sc = p.scale_log2;
             float vscale = 1.f;
-            if (p.f8) {
+            if (F8) {
                 sc *= __ldg(p.k_scale + (long long)g.b * p.Hkv + g.h);
                 vscale = __ldg(p.v_scale + (long long)g.b * p.Hkv + g.h);
             }
@@ -622,10 +739,10 @@ __global__ void __launch_bounds__(ExtCfg<T, D>::THREADS, 1) extend_kernel(const 
         tmem_dealloc(tmem, C::TMEM_COLS);
 }
 
-template <typename T, int D> static cudaError_t launch_extend_t(const ExtendParams &p, cudaStream_t s)
+template <typename T, int D, bool F8> static cudaError_t launch_extend_t(const ExtendParams &p, cudaStream_t s)
 {
-    using C = ExtCfg<T, D>;
-    auto kern = extend_kernel<T, D>;
+    using C = ExtCfg<T, D, F8>;
+    auto kern = extend_kernel<T, D, F8>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess)
         return e;

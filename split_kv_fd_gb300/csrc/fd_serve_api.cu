@@ -63,6 +63,21 @@ bool map_16bit(CUtensorMap *m, const void *base, int dtype, int d, long long n1,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A map of bytes [d, n1, n2] with boxes [d, box1, 1]: E4M3 blocks as they are.
+bool map_8bit(CUtensorMap *m, const void *base, int d, long long n1, long long n2, int box1)
+{
+    EncodeTiledFn fn = encode_tiled();
+    if (!fn)
+        return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)n1, (cuuint64_t)n2};
+    const cuuint64_t strides[2] = {(cuuint64_t)d, (cuuint64_t)n1 * d};
+    const cuuint32_t box[3] = {(cuuint32_t)d, (cuuint32_t)box1, 1};
+    const cuuint32_t es[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // The slices, the tiles and the workspace of a call.
 struct ExtLayout {
     int G, NG, Gs, tps, grid;
@@ -117,8 +132,6 @@ fd_status run_extend(ExtendParams &p, float scale, void *workspace, size_t works
     if (!p.status)
         return FD_ERR_CUDA;
     const cudaStream_t cs = stream_of(stream);
-    if (p.f8)
-        return launch_extend_e4m3(p, cs) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
 
     p.G = l.G;
     p.NG = l.NG;
@@ -146,10 +159,11 @@ fd_status run_extend(ExtendParams &p, float scale, void *workspace, size_t works
         for (int i = 0; i < 2; ++i) {
             CUtensorMap *m = i ? &p.tmv : &p.tmk;
             const void *x = i ? p.v : p.k;
-            ok = ok && (p.paged ? map_16bit(m, x, p.dtype, p.d, p.page_size, row, p.num_pages * p.Hkv,
-                                            row * p.page_size, p.box_rows, 1)
-                                : map_16bit(m, x, p.dtype, p.d, p.total_k, (i ? p.v_stride : p.k_stride) * 2, p.Hkv,
-                                            row, EXT_CT, 1));
+            ok = ok && (p.f8      ? map_8bit(m, x, p.d, p.page_size, p.num_pages * p.Hkv, p.box_rows)
+                        : p.paged ? map_16bit(m, x, p.dtype, p.d, p.page_size, row, p.num_pages * p.Hkv,
+                                              row * p.page_size, p.box_rows, 1)
+                                  : map_16bit(m, x, p.dtype, p.d, p.total_k, (i ? p.v_stride : p.k_stride) * 2,
+                                              p.Hkv, row, EXT_CT, 1));
         }
     } else {
         p.tmk = p.tmv = p.tmq;   // no key anywhere: never used
@@ -158,7 +172,8 @@ fd_status run_extend(ExtendParams &p, float scale, void *workspace, size_t works
         return FD_ERR_CUDA;
     cudaError_t e = launch_extend_plan(p, cs);
     if (e == cudaSuccess)
-        e = p.dtype == FD_BF16 ? launch_extend_bf16(p, cs) : launch_extend_f16(p, cs);
+        e = p.dtype == FD_BF16 ? (p.f8 ? launch_extend_bf16_e4m3(p, cs) : launch_extend_bf16(p, cs))
+                               : (p.f8 ? launch_extend_f16_e4m3(p, cs) : launch_extend_f16(p, cs));
     if (e == cudaSuccess)
         e = launch_extend_merge(p, cs);
     return e == cudaSuccess ? FD_OK : FD_ERR_CUDA;
