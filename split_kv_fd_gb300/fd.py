@@ -9,6 +9,7 @@ if the library is missing or no GPU is present, the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -533,45 +534,34 @@ def decode_gqa_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seq
     return out, lse
 
 
-def _on_one_device(*ts):
-    """The CUDA device that all given tensors are on."""
-    dev = None
+def _one_device(*ts):
+    """The index of the CUDA device that all given tensors are on."""
+    dev = ts[0].get_device()
     for t in ts:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("all tensors must be CUDA tensors (the library has no CPU path)")
-        if dev is not None and t.device != dev:
-            raise ValueError("all tensors must be on one device")
-        dev = t.device
+        if t is not None and t.get_device() != dev:
+            raise ValueError("all tensors must be on one device" if t.is_cuda else
+                             "all tensors must be CUDA tensors (the library has no CPU path)")
+    if dev < 0:
+        raise ValueError("all tensors must be CUDA tensors (the library has no CPU path)")
     return dev
 
 
-def _rows(t, name):
-    """Elements between the tokens of a packed [T, H, d] tensor whose tokens
-    are contiguous (a view of a fused projection has them further apart)."""
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [T, H, d]")
-    T, H, d = t.shape
-    if t.numel() == 0:
-        return H * d
-    if (d > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != d):
-        raise ValueError(f"{name}: the H*d elements of a token must be contiguous")
-    if T == 1:
-        return H * d
-    if t.stride(0) < H * d:
-        raise ValueError(f"{name}: tokens must not overlap")
-    return t.stride(0)
+def _call(what, dev, stream, *args):
+    """The library's call ``what`` with device ``dev`` current, on ``stream``
+    (default: the device's current one)."""
+    fn = getattr(_lib or load(), what)
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, raw)
+    if st != FD_OK:
+        raise FDError(st, what)
 
 
-def _offsets(t, B, name):
-    if t.dtype != torch.int32 or t.shape != (B + 1,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape [B + 1]")
-
-
-def _int32(t, shape, name):
-    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)}")
+def _address(t):
+    return None if t is None else t.data_ptr()
 
 
 def _keep(dev, stream, *ts):
@@ -581,6 +571,35 @@ def _keep(dev, stream, *ts):
         for t in ts:
             if t is not None:
                 t.record_stream(stream)
+
+
+def _rows(t, name):
+    """Elements between the tokens of a packed [T, H, d] tensor whose tokens
+    are contiguous (a view of a fused projection has them further apart)."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [T, H, d]")
+    (T, H, d), (far, head, one) = t.shape, t.stride()
+    row = H * d
+    if T == 0 or row == 0:
+        return row
+    if (d > 1 and one != 1) or (H > 1 and head != d):
+        raise ValueError(f"{name}: the H*d elements of a token must be contiguous")
+    if T == 1:
+        return row
+    if far < row:
+        raise ValueError(f"{name}: tokens must not overlap")
+    return far
+
+
+def _int32(t, shape, name):
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)}")
+
+
+def _whole(*ts):
+    for t in ts:
+        if t is not None and not t.is_contiguous():
+            raise ValueError("all tensors but packed rows must be contiguous")
 
 
 def resize_pages(seqlens, target, block_table, free_pages, free_count, page_size, slots=None, positions=None,
@@ -596,33 +615,29 @@ def resize_pages(seqlens, target, block_table, free_pages, free_count, page_size
     sequences' new tokens (allocated if only slots or positions are given).
     Returns ``cu_new``.  A sequence that could not grow keeps its length.
     """
-    dev = _on_one_device(seqlens, target, block_table, free_pages, free_count, slots, positions, cu_new)
+    dev = _one_device(seqlens, target, block_table, free_pages, free_count, slots, positions, cu_new)
     if seqlens.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
         raise ValueError("seqlens [B], block_table [B, max_pages], free_pages [num_pages]")
     B = seqlens.shape[0]
+    width, pool, room = block_table.shape[1], free_pages.shape[0], 0
     _int32(seqlens, (B,), "seqlens")
     _int32(target, (B,), "target")
-    _int32(block_table, (B, block_table.shape[1]), "block_table")
-    _int32(free_pages, free_pages.shape, "free_pages")
+    _int32(block_table, (B, width), "block_table")
+    _int32(free_pages, (pool,), "free_pages")
     _int32(free_count, (1,), "free_count")
-    room = 0
-    for t, n in ((slots, "slots"), (positions, "positions")):
-        if t is None:
-            continue
-        if t.dim() != 1 or (slots is not None and t.shape != slots.shape):
-            raise ValueError("slots and positions must be [max_tokens]")
-        _int32(t, t.shape, n)
-        room = t.shape[0]
     own = None
-    if cu_new is not None:
-        _offsets(cu_new, B, "cu_new")
-    elif slots is not None or positions is not None:
-        own = cu_new = torch.empty(B + 1, dtype=torch.int32, device=dev)
-    with torch.cuda.device(dev):
-        st = load().fd_resize_pages(_ptr(seqlens), _ptr(target), B, _ptr(block_table), block_table.shape[1],
-                                    _ptr(free_pages), _ptr(free_count), free_pages.shape[0], int(page_size),
-                                    _ptr(slots), _ptr(positions), room, _ptr(cu_new), _stream(seqlens, stream))
-    _check(st, "fd_resize_pages")
+    if slots is not None or positions is not None:
+        room = (positions if slots is None else slots).numel()
+        for t, n in ((slots, "slots"), (positions, "positions")):
+            if t is not None:
+                _int32(t, (room,), n)
+        if cu_new is None:
+            own = cu_new = torch.empty(B + 1, dtype=torch.int32, device=seqlens.device)
+    if cu_new is not None and own is None:
+        _int32(cu_new, (B + 1,), "cu_new")
+    _call("fd_resize_pages", dev, stream, seqlens.data_ptr(), target.data_ptr(), B, block_table.data_ptr(), width,
+          free_pages.data_ptr(), free_count.data_ptr(), pool, page_size, _address(slots), _address(positions), room,
+          _address(cu_new))
     _keep(dev, stream, own)
     return cu_new
 
@@ -633,11 +648,11 @@ def _append_args(k, v, slots, k_pages, v_pages):
         raise ValueError("k and v must share one shape and dtype among float32/float16/bfloat16")
     T, H, d = k.shape
     _int32(slots, (T,), "slots")
-    _need_cuda(k_pages, v_pages)
-    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype \
-            or k_pages.shape[1] != H or k_pages.shape[3] != d:
+    _whole(k_pages, v_pages)
+    shape = k_pages.shape
+    if len(shape) != 4 or v_pages.shape != shape or v_pages.dtype != k_pages.dtype or shape[1] != H or shape[3] != d:
         raise ValueError("k_pages/v_pages must be [num_pages, Hkv, page_size, d] with Hkv, d of k")
-    return T, H, d, k_stride, v_stride
+    return T, H, d, k_stride, v_stride, DTYPE_CODE[k.dtype], k_pages.data_ptr(), v_pages.data_ptr(), shape[2], shape[0]
 
 
 def append_paged(k, v, slots, k_pages, v_pages, stream=None):
@@ -647,15 +662,17 @@ def append_paged(k, v, slots, k_pages, v_pages, stream=None):
     bytes apart); slots int32 [T], negative ones skipped; k_pages/v_pages
     [num_pages, Hkv, page_size, d] of k's dtype.
     """
-    dev = _on_one_device(k, v, slots, k_pages, v_pages)
-    T, H, d, k_stride, v_stride = _append_args(k, v, slots, k_pages, v_pages)
+    dev = _one_device(k, v, slots, k_pages, v_pages)
+    args = _append_args(k, v, slots, k_pages, v_pages)
     if k_pages.dtype != k.dtype:
         raise ValueError("the pages must have k's dtype")
-    with torch.cuda.device(dev):
-        st = load().fd_append_paged(_ptr(k), _ptr(v), _ptr(slots), T, H, d, k_stride, v_stride, DTYPE_CODE[k.dtype],
-                                    _ptr(k_pages), _ptr(v_pages), k_pages.shape[2], k_pages.shape[0],
-                                    _stream(k, stream))
-    _check(st, "fd_append_paged")
+    _call("fd_append_paged", dev, stream, k.data_ptr(), v.data_ptr(), slots.data_ptr(), *args)
+
+
+def _scales(k_scale, v_scale, shape):
+    for t in (k_scale, v_scale):
+        if t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous():
+            raise ValueError("k_scale/v_scale must be contiguous float32 [B, Hkv]")
 
 
 def append_paged_fp8(k, v, k_scale, v_scale, cu_new, slots, k_pages, v_pages, stream=None):
@@ -665,21 +682,15 @@ def append_paged_fp8(k, v, k_scale, v_scale, cu_new, slots, k_pages, v_pages, st
     k, v, slots as in append_paged; k_scale, v_scale float32 [B, Hkv]; cu_new
     int32 [B+1]; pages torch.float8_e4m3fn (or uint8 E4M3 bytes).
     """
-    dev = _on_one_device(k, v, k_scale, v_scale, cu_new, slots, k_pages, v_pages)
-    T, H, d, k_stride, v_stride = _append_args(k, v, slots, k_pages, v_pages)
+    dev = _one_device(k, v, k_scale, v_scale, cu_new, slots, k_pages, v_pages)
+    args = _append_args(k, v, slots, k_pages, v_pages)
     if k_pages.dtype not in (torch.float8_e4m3fn, torch.uint8):
         raise ValueError("pages must be float8_e4m3fn (or uint8 E4M3 bytes)")
-    B = k_scale.shape[0] if k_scale.dim() == 2 else 0
-    _need_cuda(k_scale, v_scale)
-    for t in (k_scale, v_scale):
-        if t.dtype != torch.float32 or t.shape != (B, H):
-            raise ValueError("k_scale/v_scale must be float32 [B, Hkv]")
-    _offsets(cu_new, B, "cu_new")
-    with torch.cuda.device(dev):
-        st = load().fd_append_paged_fp8(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(cu_new), _ptr(slots), B,
-                                        T, H, d, k_stride, v_stride, DTYPE_CODE[k.dtype], _ptr(k_pages),
-                                        _ptr(v_pages), k_pages.shape[2], k_pages.shape[0], _stream(k, stream))
-    _check(st, "fd_append_paged_fp8")
+    B = cu_new.numel() - 1
+    _scales(k_scale, v_scale, (B, args[1]))
+    _int32(cu_new, (B + 1,), "cu_new")
+    _call("fd_append_paged_fp8", dev, stream, k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+          cu_new.data_ptr(), slots.data_ptr(), B, *args)
 
 
 def workspace_size_extend(B, total_q, Hq, Hkv, d) -> int:
@@ -687,31 +698,44 @@ def workspace_size_extend(B, total_q, Hq, Hkv, d) -> int:
     return load().fd_workspace_size_extend(B, total_q, Hq, Hkv, d)
 
 
-def _extend_out(dev, q, B, Hkv, scale, out_dtype, out, lse, return_lse, workspace):
-    """What the attention calls of several new tokens set alike; allocates
-    what the caller left out, the workspace for this one call."""
-    T, Hq, d = q.shape
-    mine = []
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
+@functools.lru_cache(maxsize=1024)
+def _extend_bytes(dev, *sizes):
+    """workspace_size_extend on a device, which depends on nothing else."""
+    with torch.cuda.device(dev):
+        return max(workspace_size_extend(*sizes), 256)
+
+
+def _extend_out(dev, q, B, Hkv, out_dtype, out, lse, return_lse, workspace):
+    """out, lse and the workspace of the attention calls of several new
+    tokens, checked or allocated (the workspace for this one call), and
+    those that were allocated."""
+    shape = T, Hq, d = q.shape
+    where, mine = q.device, []
     if out is None:
-        out = torch.empty((T, Hq, d), dtype=out_dtype or q.dtype, device=dev)
+        out = torch.empty(shape, dtype=out_dtype or q.dtype, device=where)
         mine.append(out)
-    if lse is None and return_lse:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+    elif out.shape != shape or out.get_device() != dev or not out.is_contiguous():
+        raise ValueError("out must be contiguous [T, Hq, d] on q's device")
+    if out.dtype not in DTYPE_CODE:
+        raise ValueError("out must be float32/float16/bfloat16")
+    if lse is not None:
+        if lse.dtype != torch.float32 or lse.shape != (T, Hq) or lse.get_device() != dev or not lse.is_contiguous():
+            raise ValueError("lse must be contiguous float32 [T, Hq] on q's device")
+    elif return_lse:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=where)
         mine.append(lse)
-    _need_cuda(out, lse)
-    if out.dtype not in DTYPE_CODE or out.shape != (T, Hq, d):
-        raise ValueError("out must be [T, Hq, d] float32/float16/bfloat16")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, Hq)):
-        raise ValueError("lse must be float32 [T, Hq]")
     if workspace is None:
-        workspace = torch.empty(max(load().fd_workspace_size_extend(B, T, Hq, Hkv, d), 256), dtype=torch.uint8,
-                                device=dev)
+        workspace = torch.empty(_extend_bytes(dev, B, T, Hq, Hkv, d), dtype=torch.uint8, device=where)
         mine.append(workspace)
-    _need_cuda(workspace)
-    _on_one_device(q, out, lse, workspace)
-    return scale, out, lse, workspace, mine
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on q's device")
+    return out, lse, workspace, mine
+
+
+def _tail(d, scale, out, lse, workspace):
+    """The arguments that the attention calls of several new tokens end with."""
+    return (1.0 / math.sqrt(d) if scale is None else scale, out.data_ptr(), DTYPE_CODE[out.dtype], _address(lse),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size())
 
 
 def prefill(q, k, v, cu_seqlens_q, cu_seqlens_k=None, causal=True, scale=None, out_dtype=None, out=None, lse=None,
@@ -727,26 +751,22 @@ def prefill(q, k, v, cu_seqlens_q, cu_seqlens_k=None, causal=True, scale=None, o
     float32; rows outside the sequences are not written.
     """
     cu_k = cu_seqlens_q if cu_seqlens_k is None else cu_seqlens_k
-    dev = _on_one_device(q, k, v, cu_seqlens_q, cu_k)
-    strides = [_rows(t, n) for t, n in ((q, "q"), (k, "k"), (v, "v"))]
+    dev = _one_device(q, k, v, cu_seqlens_q, cu_k)
+    q_stride, k_stride, v_stride = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
     if q.dtype not in (torch.float16, torch.bfloat16) or k.dtype != q.dtype or v.dtype != q.dtype:
         raise ValueError("q, k, v must share one dtype, float16 or bfloat16")
-    if v.shape != k.shape or k.shape[2] != q.shape[2] or k.shape[1] == 0 or q.shape[1] % k.shape[1]:
+    (T, Hq, d), (Tk, Hkv, dk) = q.shape, k.shape
+    if v.shape != k.shape or dk != d or Hkv == 0 or Hq % Hkv:
         raise ValueError("shapes: q [Tq, Hq, d], k/v [Tk, Hkv, d], Hq % Hkv == 0")
-    if cu_seqlens_k is None and k.shape[0] != q.shape[0]:
+    if cu_seqlens_k is None and Tk != T:
         raise ValueError("without cu_seqlens_k, k and v must have q's tokens")
     B = cu_seqlens_q.numel() - 1
-    _offsets(cu_seqlens_q, B, "cu_seqlens_q")
-    _offsets(cu_k, B, "cu_seqlens_k")
-    T, Hq, d = q.shape
-    scale, out, lse, workspace, mine = _extend_out(dev, q, B, k.shape[1], scale, out_dtype, out, lse, return_lse,
-                                                   workspace)
-    with torch.cuda.device(dev):
-        st = load().fd_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens_q), _ptr(cu_k), B, T, k.shape[0], Hq,
-                               k.shape[1], d, *strides, DTYPE_CODE[q.dtype], int(bool(causal)), float(scale),
-                               _ptr(out), DTYPE_CODE[out.dtype], _ptr(lse), _ptr(workspace),
-                               workspace.numel() * workspace.element_size(), _stream(q, stream))
-    _check(st, "fd_prefill")
+    _int32(cu_seqlens_q, (B + 1,), "cu_seqlens_q")
+    _int32(cu_k, (B + 1,), "cu_seqlens_k")
+    out, lse, workspace, mine = _extend_out(dev, q, B, Hkv, out_dtype, out, lse, return_lse, workspace)
+    _call("fd_prefill", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens_q.data_ptr(),
+          cu_k.data_ptr(), B, T, Tk, Hq, Hkv, d, q_stride, k_stride, v_stride, DTYPE_CODE[q.dtype], bool(causal),
+          *_tail(d, scale, out, lse, workspace))
     _keep(dev, stream, *mine)
     return out, lse
 
@@ -755,19 +775,20 @@ def _extend_args(q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens):
     q_stride = _rows(q, "q")
     if q.dtype not in (torch.float16, torch.bfloat16):
         raise ValueError("q must be float16 or bfloat16")
-    _need_cuda(k_pages, v_pages)
+    _whole(k_pages, v_pages)
     if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype:
         raise ValueError("k_pages/v_pages must be [num_pages, Hkv, page_size, d]")
-    num_pages, Hkv, page_size, d = k_pages.shape
-    if q.shape[2] != d or Hkv == 0 or q.shape[1] % Hkv:
+    (num_pages, Hkv, page_size, dk), (T, Hq, d) = k_pages.shape, q.shape
+    if dk != d or Hkv == 0 or Hq % Hkv:
         raise ValueError("q must be [T, Hq, d] with Hq a multiple of the pages' Hkv")
-    B = seqlens.shape[0] if seqlens.dim() == 1 else -1
+    B = seqlens.numel()
     _int32(seqlens, (B,), "seqlens")
+    _int32(cu_seqlens_q, (B + 1,), "cu_seqlens_q")
     if block_table.dim() != 2:
         raise ValueError("block_table must be int32 [B, max_pages]")
-    _int32(block_table, (B, block_table.shape[1]), "block_table")
-    _offsets(cu_seqlens_q, B, "cu_seqlens_q")
-    return B, q_stride, num_pages, Hkv, page_size
+    width = block_table.shape[1]
+    _int32(block_table, (B, width), "block_table")
+    return B, T, Hq, Hkv, d, q_stride, page_size, width, num_pages
 
 
 def extend_paged(q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens, scale=None, out_dtype=None, out=None,
@@ -782,19 +803,14 @@ def extend_paged(q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens, scale=
     sequence's last new token sees all seqlens[b] tokens, the one before all
     but the last, and so on.
     """
-    dev = _on_one_device(q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens)
-    B, q_stride, num_pages, Hkv, page_size = _extend_args(q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens)
+    dev = _one_device(q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens)
+    args = _extend_args(q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens)
     if k_pages.dtype != q.dtype:
         raise ValueError("the pages must have q's dtype")
-    T, Hq, d = q.shape
-    scale, out, lse, workspace, mine = _extend_out(dev, q, B, Hkv, scale, out_dtype, out, lse, return_lse, workspace)
-    with torch.cuda.device(dev):
-        st = load().fd_extend_paged(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(cu_seqlens_q),
-                                    _ptr(seqlens), B, T, Hq, Hkv, d, q_stride, page_size, block_table.shape[1],
-                                    num_pages, DTYPE_CODE[q.dtype], float(scale), _ptr(out), DTYPE_CODE[out.dtype],
-                                    _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                    _stream(q, stream))
-    _check(st, "fd_extend_paged")
+    out, lse, workspace, mine = _extend_out(dev, q, args[0], args[3], out_dtype, out, lse, return_lse, workspace)
+    _call("fd_extend_paged", dev, stream, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+          block_table.data_ptr(), cu_seqlens_q.data_ptr(), seqlens.data_ptr(), *args, DTYPE_CODE[q.dtype],
+          *_tail(args[4], scale, out, lse, workspace))
     _keep(dev, stream, *mine)
     return out, lse
 
@@ -804,23 +820,15 @@ def extend_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, cu_seql
     """extend_paged over E4M3 pages (fd_extend_paged_fp8): pages
     torch.float8_e4m3fn (or uint8 E4M3 bytes), k_scale, v_scale float32
     [B, Hkv].  Returns ``(out, lse)``."""
-    dev = _on_one_device(q, k_pages, v_pages, k_scale, v_scale, block_table, cu_seqlens_q, seqlens)
-    B, q_stride, num_pages, Hkv, page_size = _extend_args(q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens)
+    dev = _one_device(q, k_pages, v_pages, k_scale, v_scale, block_table, cu_seqlens_q, seqlens)
+    args = _extend_args(q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens)
     if k_pages.dtype not in (torch.float8_e4m3fn, torch.uint8):
         raise ValueError("pages must be float8_e4m3fn (or uint8 E4M3 bytes)")
-    _need_cuda(k_scale, v_scale)
-    for t in (k_scale, v_scale):
-        if t.dtype != torch.float32 or t.shape != (B, Hkv):
-            raise ValueError("k_scale/v_scale must be float32 [B, Hkv]")
-    T, Hq, d = q.shape
-    scale, out, lse, workspace, mine = _extend_out(dev, q, B, Hkv, scale, out_dtype, out, lse, return_lse, workspace)
-    with torch.cuda.device(dev):
-        st = load().fd_extend_paged_fp8(_ptr(q), DTYPE_CODE[q.dtype], _ptr(k_pages), _ptr(v_pages), _ptr(k_scale),
-                                        _ptr(v_scale), _ptr(block_table), _ptr(cu_seqlens_q), _ptr(seqlens), B, T,
-                                        Hq, Hkv, d, q_stride, page_size, block_table.shape[1], num_pages,
-                                        float(scale), _ptr(out), DTYPE_CODE[out.dtype], _ptr(lse), _ptr(workspace),
-                                        workspace.numel() * workspace.element_size(), _stream(q, stream))
-    _check(st, "fd_extend_paged_fp8")
+    _scales(k_scale, v_scale, (args[0], args[3]))
+    out, lse, workspace, mine = _extend_out(dev, q, args[0], args[3], out_dtype, out, lse, return_lse, workspace)
+    _call("fd_extend_paged_fp8", dev, stream, q.data_ptr(), DTYPE_CODE[q.dtype], k_pages.data_ptr(),
+          v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), cu_seqlens_q.data_ptr(),
+          seqlens.data_ptr(), *args, *_tail(args[4], scale, out, lse, workspace))
     _keep(dev, stream, *mine)
     return out, lse
 
