@@ -72,9 +72,9 @@ template <typename T, int D, bool F8> struct ExtCfg {
     // bf16 has float32's range and needs none.
     static constexpr float SHIFT = std::is_same<T, __half>::value ? 7.f : 0.f;
     static constexpr uint32_t SLEEP_NS = 100000;
-    // barriers: ring full/empty, S, P, O, Q full, Q empty of both sub-tiles,
+    // barriers: ring full/empty, S, both halves of P, O, Q full, Q empty of both sub-tiles,
     // segments full/empty, the last commit, raw ring full/empty
-    static constexpr int NBAR = 2 * STAGES + 10 + 2 * SEGS + 1 + 2 * RAWS;
+    static constexpr int NBAR = 2 * STAGES + 12 + 2 * SEGS + 1 + 2 * RAWS;
     static constexpr int SMEM = 1024 + STAGES * BLOCK_BYTES + RAWS * RAW_BYTES + 2 * Q_BYTES + NBAR * 8 + 16 + SEGS * 64;
     static_assert(SMEM <= 232448, "shared memory");
 };
@@ -167,13 +167,13 @@ __global__ void __launch_bounds__(ExtCfg<T, D, F8>::THREADS, 1) extend_kernel(co
     auto EMPTY = [&](int s) { return bar0 + 8u * (uint32_t)(ST + s); };
     constexpr int B0 = 2 * ST;
     auto SFULL = [&](int x) { return bar0 + 8u * (uint32_t)(B0 + x); };
-    auto PFULL = [&](int x) { return bar0 + 8u * (uint32_t)(B0 + 2 + x); };
-    auto OFULL = [&](int x) { return bar0 + 8u * (uint32_t)(B0 + 4 + x); };
-    auto QFULL = [&](int x) { return bar0 + 8u * (uint32_t)(B0 + 6 + x); };
-    auto QEMPTY = [&](int x) { return bar0 + 8u * (uint32_t)(B0 + 8 + x); };
-    auto GFULL = [&](int s) { return bar0 + 8u * (uint32_t)(B0 + 10 + s); };
-    auto GEMPTY = [&](int s) { return bar0 + 8u * (uint32_t)(B0 + 10 + C::SEGS + s); };
-    const uint32_t FIN = bar0 + 8u * (uint32_t)(B0 + 10 + 2 * C::SEGS);
+    auto PFULL = [&](int x, int half) { return bar0 + 8u * (uint32_t)(B0 + 2 + 2 * x + half); };
+    auto OFULL = [&](int x) { return bar0 + 8u * (uint32_t)(B0 + 6 + x); };
+    auto QFULL = [&](int x) { return bar0 + 8u * (uint32_t)(B0 + 8 + x); };
+    auto QEMPTY = [&](int x) { return bar0 + 8u * (uint32_t)(B0 + 10 + x); };
+    auto GFULL = [&](int s) { return bar0 + 8u * (uint32_t)(B0 + 12 + s); };
+    auto GEMPTY = [&](int s) { return bar0 + 8u * (uint32_t)(B0 + 12 + C::SEGS + s); };
+    const uint32_t FIN = bar0 + 8u * (uint32_t)(B0 + 12 + 2 * C::SEGS);
     auto RFULL = [&](int s) { return FIN + 8u * (uint32_t)(1 + s); };
     auto REMPTY = [&](int s) { return FIN + 8u * (uint32_t)(1 + C::RAWS + s); };
 
@@ -184,7 +184,9 @@ __global__ void __launch_bounds__(ExtCfg<T, D, F8>::THREADS, 1) extend_kernel(co
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(SFULL(x), 1);   // commit behind S
-            mbar_init(PFULL(x), 4);   // the sub-tile's warps: S read, O rescaled, P written
+            // the sub-tile's warps: S read, O rescaled, a half of P written
+            mbar_init(PFULL(x, 0), 4);
+            mbar_init(PFULL(x, 1), 4);
             mbar_init(OFULL(x), 1);   // commit behind the segment's last P.V
             mbar_init(QFULL(x), 1);
             mbar_init(QEMPTY(x), 1);  // commit behind the segment's last S
@@ -217,7 +219,7 @@ __global__ void __launch_bounds__(ExtCfg<T, D, F8>::THREADS, 1) extend_kernel(co
     // The next segment, by a whole warp; false at the end (or on expiry).
     auto next_seg = [&](ExtSeg &g) {
         const int s = sg % C::SEGS;
-        if (!mbar_wait_bounded_sleep(GFULL(s), (uint32_t)((sg / C::SEGS) & 1), C::SLEEP_NS)) {
+        if (!mbar_wait_bounded_soon(GFULL(s), (uint32_t)((sg / C::SEGS) & 1), C::SLEEP_NS)) {
             dead = true;
             return false;
         }
@@ -343,7 +345,7 @@ __global__ void __launch_bounds__(ExtCfg<T, D, F8>::THREADS, 1) extend_kernel(co
                 for (int kv = 0; kv < 2; ++kv, ++n) {
                     const int s = (int)(n % NS);
                     if (n >= NS &&
-                        !mbar_wait_bounded_sleep(NEMPTY(s), (uint32_t)(((n / NS) - 1) & 1), C::SLEEP_NS)) {
+                        !mbar_wait_bounded_soon(NEMPTY(s), (uint32_t)(((n / NS) - 1) & 1), C::SLEEP_NS)) {
                         dead = true;
                         break;
                     }
@@ -361,7 +363,7 @@ __global__ void __launch_bounds__(ExtCfg<T, D, F8>::THREADS, 1) extend_kernel(co
         }
         // no copy may be in flight when the CTA ends: the last fill of each stage
         for (long long i = n > NS ? n - NS : 0; i < n; ++i)
-            mbar_wait_bounded_sleep(NFULL((int)(i % NS)), (uint32_t)((i / NS) & 1), C::SLEEP_NS);
+            mbar_wait_bounded_soon(NFULL((int)(i % NS)), (uint32_t)((i / NS) & 1), C::SLEEP_NS);
     } else if (F8 && w >= C::CVT_WARP) {
         // ------------------------------------------------------------ E4M3 to 16 bits
         // A thread widens 16 values of a row at a time into the swizzled
@@ -384,8 +386,8 @@ __global__ void __launch_bounds__(ExtCfg<T, D, F8>::THREADS, 1) extend_kernel(co
 #pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv, ++n) {
                     const int rs = (int)(n % NR), s = (int)(n % ST);
-                    if (!mbar_wait_bounded_sleep(RFULL(rs), (uint32_t)((n / NR) & 1), C::SLEEP_NS) ||
-                        (n >= ST && !mbar_wait_bounded_sleep(EMPTY(s), (uint32_t)(((n / ST) - 1) & 1), C::SLEEP_NS))) {
+                    if (!mbar_wait_bounded_soon(RFULL(rs), (uint32_t)((n / NR) & 1), C::SLEEP_NS) ||
+                        (n >= ST && !mbar_wait_bounded_soon(EMPTY(s), (uint32_t)(((n / ST) - 1) & 1), C::SLEEP_NS))) {
                         dead = true;
                         break;
                     }
@@ -455,31 +457,33 @@ __global__ void __launch_bounds__(ExtCfg<T, D, F8>::THREADS, 1) extend_kernel(co
         int ns[2] = {0, 0};           // P of each sub-tile taken
         int nq[2] = {0, 0};           // Q of each sub-tile taken
         auto wait = [&](uint32_t bar, int phase) {
-            if (!dead && !mbar_wait_bounded_sleep(bar, (uint32_t)(phase & 1), C::SLEEP_NS))
+            if (!dead && !mbar_wait_bounded_soon(bar, (uint32_t)(phase & 1), C::SLEEP_NS))
                 dead = true;
             return !dead;
         };
+        // Descriptors: a base, plus offsets in its units of 16 bytes (an
+        // address fits the field, so no carry leaves it).
+        const uint64_t qdesc = smem_desc_sw128(qbuf, 16, 1024), kdesc = smem_desc_sw128(ring, 16, 1024);
+        const uint64_t vdesc = smem_desc_sw128(ring, (uint32_t)C::PLANE, 1024);
+        const uint32_t one = elect_one();
         auto issue_s = [&](int x, int st) {
-            if (lane == 0) {
-                const uint32_t kb = ring + (uint32_t)(st * C::BLOCK_BYTES), qb = qbuf + (uint32_t)(x * C::Q_BYTES);
+            const uint64_t a = qdesc + (uint64_t)(x * (C::Q_BYTES >> 4)), b = kdesc + (uint64_t)(st * (C::BLOCK_BYTES >> 4));
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    // 16 elements = 32 bytes of each 128-byte row of plane ks / 4
-                    const uint32_t o = (uint32_t)((ks >> 2) * C::PLANE + (ks & 3) * 32);
-                    tc_mma_ss(tmem + (uint32_t)C::tm_s(x), smem_desc_sw128(qb + o, 16, 1024),
-                              smem_desc_sw128(kb + o, 16, 1024), ID_S, ks > 0 ? 1u : 0u);
-                }
-                tc_commit(SFULL(x));
+            for (int ks = 0; ks < D / 16; ++ks) {
+                // 16 elements = 32 bytes of each 128-byte row of plane ks / 4
+                const uint64_t o = (uint64_t)(((ks >> 2) * C::PLANE + (ks & 3) * 32) >> 4);
+                tc_mma_ss_if(one, tmem + (uint32_t)C::tm_s(x), a + o, b + o, ID_S, ks > 0 ? 1u : 0u);
             }
+            tc_commit_if(one, SFULL(x));
         };
-        auto issue_pv = [&](int x, int st, bool first) {
-            if (lane == 0) {
-                const uint32_t vb = ring + (uint32_t)(st * C::BLOCK_BYTES);
+        // the keys of one half of P
+        auto issue_pv = [&](int x, int st, int half, bool first) {
+            const uint64_t b = vdesc + (uint64_t)(st * (C::BLOCK_BYTES >> 4));
 #pragma unroll
-                for (int ks = 0; ks < C::CT / 16; ++ks)
-                    tc_mma_ts(tmem + (uint32_t)C::tm_o(x), tmem + (uint32_t)(C::tm_p(x) + ks * 8),
-                              smem_desc_sw128(vb + (uint32_t)(ks * 2048), (uint32_t)C::PLANE, 1024), ID_O,
-                              (!first || ks > 0) ? 1u : 0u);
+            for (int i = 0; i < C::CT / 32; ++i) {
+                const int ks = half * (C::CT / 32) + i;
+                tc_mma_ts_if(one, tmem + (uint32_t)C::tm_o(x), tmem + (uint32_t)(C::tm_p(x) + ks * 8),
+                             b + (uint64_t)(ks * (2048 >> 4)), ID_O, (!first || ks > 0) ? 1u : 0u);
             }
         };
         ExtSeg g;
@@ -501,13 +505,12 @@ __global__ void __launch_bounds__(ExtCfg<T, D, F8>::THREADS, 1) extend_kernel(co
                     ++nq[x];
                     tc_fence_after();
                     issue_s(x, s);
-                    if (lane == 0 && g.blk[x] == g.blk0 + 1)
-                        tc_commit(QEMPTY(x));
+                    if (g.blk[x] == g.blk0 + 1)
+                        tc_commit_if(one, QEMPTY(x));
                 }
                 if (dead)
                     break;
-                if (lane == 0)
-                    tc_commit(EMPTY(s));
+                tc_commit_if(one, EMPTY(s));
                 ++n;
             }
 #pragma unroll 1
@@ -539,42 +542,43 @@ __global__ void __launch_bounds__(ExtCfg<T, D, F8>::THREADS, 1) extend_kernel(co
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     if (j < g.blk[x]) {
-                        if (!wait(PFULL(x), ns[x]))
+                        if (!wait(PFULL(x, 0), ns[x]))
+                            break;
+                        tc_fence_after();
+                        issue_pv(x, vs, 0, j == g.blk0);
+                        if (!wait(PFULL(x, 1), ns[x]))
                             break;
                         ++ns[x];
                         tc_fence_after();
-                        issue_pv(x, vs, j == g.blk0);
-                        if (lane == 0 && j + 1 == g.blk[x])
-                            tc_commit(OFULL(x));
+                        issue_pv(x, vs, 1, false);
+                        if (j + 1 == g.blk[x])
+                            tc_commit_if(one, OFULL(x));
                     }
-                    if (x == 1 && lane == 0)
-                        tc_commit(EMPTY(vs));
+                    if (x == 1)
+                        tc_commit_if(one, EMPTY(vs));
                     if (j + 1 < g.blk[x]) {
                         if (!kready && !wait(FULL(ks), kph))
                             break;
                         kready = true;
                         tc_fence_after();
                         issue_s(x, ks);
-                        if (lane == 0 && j + 2 == g.blk[x])
-                            tc_commit(QEMPTY(x));
+                        if (j + 2 == g.blk[x])
+                            tc_commit_if(one, QEMPTY(x));
                     }
                 }
                 if (dead)
                     break;
                 if (more) {
-                    if (lane == 0)
-                        tc_commit(EMPTY(ks));
+                    tc_commit_if(one, EMPTY(ks));
                     ++n;
                 }
             }
         }
-        // every MMA this thread issued has completed before TMEM is freed
-        if (lane == 0) {
-            tc_commit(FIN);
-            if (!mbar_wait_bounded_sleep_thread(FIN, 0, C::SLEEP_NS))
-                dead = true;
-        }
-        dead = __any_sync(FULL_MASK, dead);
+        // every MMA issued here has completed before TMEM is freed
+        __syncwarp();
+        tc_commit_if(one, FIN);
+        if (!mbar_wait_bounded_soon(FIN, 0, C::SLEEP_NS))
+            dead = true;
     }
     } else {
         regs_inc<C::REGS_SOFTMAX>();
@@ -600,9 +604,11 @@ __global__ void __launch_bounds__(ExtCfg<T, D, F8>::THREADS, 1) extend_kernel(co
             }
             float mref = -INFINITY, l = 0.f;
             const int end = g.blk[x];
+            // blocks below this one hide nothing from any row of the warp
+            const int whole = __reduce_min_sync(FULL_MASK, max(lim, 0)) / C::CT;
 #pragma unroll 1
             for (int j = g.blk0; j < end; ++j) {
-                if (!mbar_wait_bounded_sleep(SFULL(x), (uint32_t)(ns & 1), C::SLEEP_NS)) {
+                if (!mbar_wait_bounded_soon(SFULL(x), (uint32_t)(ns & 1), C::SLEEP_NS)) {
                     dead = true;
                     break;
                 }
@@ -614,26 +620,28 @@ __global__ void __launch_bounds__(ExtCfg<T, D, F8>::THREADS, 1) extend_kernel(co
                     tmem_ld32(tl + (uint32_t)(C::tm_s(x) + 32 * i), s[i]);
                 tmem_wait_ld();
                 float sx = sc;
-                if (!(sc > 0.f)) {   // a K scale that is not positive
+                if (F8 && !(sc > 0.f)) {   // a K scale that is not positive
 #pragma unroll
                     for (int i = 0; i < 128; ++i)
                         s[i >> 5][i & 31] *= sc;
                     sx = 1.f;
                 }
-                const int see = lim - j * C::CT;
-                if (__any_sync(FULL_MASK, see < C::CT)) {
+                if (j >= whole) {
+                    const int see = lim - j * C::CT;
 #pragma unroll
                     for (int i = 0; i < 128; ++i)
                         s[i >> 5][i & 31] = i < see ? s[i >> 5][i & 31] : -INFINITY;
                 }
+                // four chains of three-input maxima
                 float mx[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    mx[i] = s[i][0];
+                for (int i = 0; i < 4; ++i)
+                    mx[i] = fmaxf(s[i][0], s[i][1]);
 #pragma unroll
-                    for (int e = 1; e < 32; ++e)
-                        mx[i] = fmaxf(mx[i], s[i][e]);
-                }
+                for (int e = 2; e < 32; e += 2)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        mx[i] = fmaxf(mx[i], fmaxf(s[i][e], s[i][e + 1]));
                 const float mc = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sx;
                 const bool grow = mc > mref + C::TAU;
                 float a = 1.f;
@@ -658,8 +666,8 @@ __global__ void __launch_bounds__(ExtCfg<T, D, F8>::THREADS, 1) extend_kernel(co
                     }
                 }
                 const float nm = mref == -INFINITY ? 0.f : C::SHIFT - mref;
-                const uint64_t sc2 = pack2(sx, sx), nm2 = pack2(nm, nm), one2 = pack2(1.f, 1.f);
-                uint64_t ls2 = pack2(0.f, 0.f);
+                const uint64_t sc2 = pack2(sx, sx), nm2 = pack2(nm, nm);
+                uint64_t ls[4] = {0, 0, 0, 0};   // pairs of zeros
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     uint32_t ph[16];
@@ -668,19 +676,22 @@ __global__ void __launch_bounds__(ExtCfg<T, D, F8>::THREADS, 1) extend_kernel(co
                         float x0, x1;
                         unpack2(fma2(pack2(s[i][2 * e], s[i][2 * e + 1]), sc2, nm2), x0, x1);
                         const float p0 = ex2(x0), p1 = ex2(x1);
-                        ls2 = fma2(pack2(p0, p1), one2, ls2);
+                        ls[e & 3] = add2(ls[e & 3], pack2(p0, p1));
                         ph[e] = Mma<T>::pack(p0, p1);
                     }
                     tmem_st16u(tl + (uint32_t)(C::tm_p(x) + 16 * i), ph);
+                    if (i & 1) {
+                        // half of P: its product with V may start
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(PFULL(x, i >> 1));
+                    }
                 }
                 float la, lb;
-                unpack2(ls2, la, lb);
+                unpack2(add2(add2(ls[0], ls[1]), add2(ls[2], ls[3])), la, lb);
                 l += la + lb;
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(PFULL(x));
             }
             if (dead)
                 break;
@@ -688,7 +699,7 @@ __global__ void __launch_bounds__(ExtCfg<T, D, F8>::THREADS, 1) extend_kernel(co
             // ---- the segment's result ----
             const bool some = end > g.blk0;
             if (some) {
-                if (!mbar_wait_bounded_sleep(OFULL(x), (uint32_t)(no & 1), C::SLEEP_NS)) {
+                if (!mbar_wait_bounded_soon(OFULL(x), (uint32_t)(no & 1), C::SLEEP_NS)) {
                     dead = true;
                     break;
                 }
