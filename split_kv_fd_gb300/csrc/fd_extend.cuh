@@ -92,24 +92,47 @@ struct ExtSeg {
 
 __device__ __forceinline__ int ext_end(const ExtSeg &g) { return max(g.blk[0], g.blk[1]); }
 
-// Sixteen consecutive outputs from index idx (a multiple of 16).
-__device__ __forceinline__ void store_out16(void *out, long long idx, int out_dtype, const float *x)
+// 32 bytes at a 32-byte aligned address in one store.
+__device__ __forceinline__ void stg256(void *ptr, const uint32_t (&w)[8])
 {
-    if (out_dtype == 0) {
-        float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(out) + idx);
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(ptr), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// 32 consecutive outputs, times f, from index idx (a multiple of 32) of a
+// 16-byte aligned tensor.  A thread writes its own row, so a store touches
+// as many lines as the warp has rows whatever its width: 32-byte stores (a
+// whole sector each) where the tensor allows them.
+__device__ __forceinline__ void store_out32(void *out, long long idx, int out_dtype, const float *x, float f)
+{
+    char *at = static_cast<char *>(out) + idx * (out_dtype == 0 ? 4 : 2);
+    const bool wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
+    const int step = out_dtype == 0 ? 8 : 16;   // elements of 32 bytes
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            o[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-        return;
+    for (int i = 0; i < 4; ++i) {
+        if (i * step >= 32)
+            break;
+        uint32_t w[8];
+        if (out_dtype == 0) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                w[e] = __float_as_uint(x[8 * i + e] * f);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float a = x[(16 * i + 2 * e) & 31] * f, b = x[(16 * i + 2 * e + 1) & 31] * f;
+                w[e] = out_dtype == 1 ? Mma<__half>::pack(a, b) : Mma<__nv_bfloat16>::pack(a, b);
+            }
+        }
+        if (wide) {
+            stg256(at + 32 * i, w);
+        } else {
+            uint4 *o = reinterpret_cast<uint4 *>(at + 32 * i);
+            o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
     }
-    uint32_t w[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        w[i] = out_dtype == 1 ? Mma<__half>::pack(x[2 * i], x[2 * i + 1])
-                              : Mma<__nv_bfloat16>::pack(x[2 * i], x[2 * i + 1]);
-    uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + idx);
-    o[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    o[1] = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
 // 16 E4M3 values as the 16-bit type, exactly: two 16-byte vectors.
@@ -151,6 +174,7 @@ __global__ void __launch_bounds__(ExtCfg<T, D, F8>::THREADS, 1) extend_kernel(co
 {
     using C = ExtCfg<T, D, F8>;
     constexpr int ST = C::STAGES;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the merge waits for this grid's end
     extern __shared__ __align__(128) unsigned char smem_raw[];
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const uint32_t raw = smem_addr(smem_raw);
@@ -710,25 +734,23 @@ __global__ void __launch_bounds__(ExtCfg<T, D, F8>::THREADS, 1) extend_kernel(co
             const float inv = any ? vscale / l : 0.f;
             const long long qrow = (long long)(g.row0 + tok) * p.Hq + g.h * p.G + g.slice * p.Gs + rg;
             const long long prow = ((long long)g.slot * 2 + x) * C::M + row;
-#pragma unroll 1
-            for (int q = 0; q < D / 16; ++q) {
-                float o[16];
-                if (some) {
-                    tmem_ld16(tl + (uint32_t)(C::tm_o(x) + 16 * q), o);
-                    tmem_wait_ld();
-                } else {
+            // an empty row is 0 whatever its accumulator holds
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
+            for (int q = 0; q < D / 32; ++q) {
+                float o[32];
+                if (some) {
+                    tmem_ld32(tl + (uint32_t)(C::tm_o(x) + 32 * q), o);
+                    tmem_wait_ld();
+                }
+                if (!some || !any) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
                         o[e] = 0.f;
                 }
-                if (live && g.slot >= 0) {
-                    store_out16(p.part_o, prow * D + 16 * q, 0, o);
-                } else if (live) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        o[e] = any ? o[e] * inv : 0.f;
-                    store_out16(p.out, qrow * D + 16 * q, p.out_dtype, o);
-                }
+                if (live && g.slot >= 0)
+                    store_out32(p.part_o, prow * D + 32 * q, 0, o, 1.f);
+                else if (live)
+                    store_out32(p.out, qrow * D + 32 * q, p.out_dtype, o, inv);
                 __syncwarp();
             }
             tc_fence_before();   // the next segment's P.V overwrites O behind this warp's next P

@@ -70,7 +70,8 @@ struct ExtendParams {
     // workspace
     int grid, max_tiles;
     ExtPlanHeader *header;
-    int *tile_start;         // [B + 1]
+    int *tile_start;         // [B] tiles before each sequence
+    int *tile_blk;           // [max_tiles] blocks of the sorted tiles
     ExtTile *tiles;          // [max_tiles] by descending cost
     long long *cost_sum;     // [max_tiles + 1] costs before, over the virtual heads
     ExtCut *cuts;            // [grid + 1]

@@ -22,6 +22,7 @@ constexpr int PW = PT / 32;
 constexpr int BUCKETS = 64;     // of the sort by cost
 constexpr int EXT_START = 2;    // cost of an item beside its blocks, in blocks
 constexpr int EXT_MIN_CUT = 3;  // a share of the cut items is at least this cost
+constexpr int NEAR = 2048;      // up to so many sequences, or tiles, the tables below are in shared memory
 
 __device__ __forceinline__ long long scan_block(long long x, long long *warp_sums, long long &total)
 {
@@ -84,13 +85,14 @@ __device__ __forceinline__ bool k_rows(const ExtendParams &p, int b, int &lo, in
     return lo != a || lo + m != e;
 }
 
-// Tile i (of all, in order of the sequences).
-__device__ __forceinline__ ExtTile tile_at(const ExtendParams &p, int i)
+// Tile i (of all, in order of the sequences), of the tiles before each
+// sequence.
+__device__ __forceinline__ ExtTile tile_at(const ExtendParams &p, const int *tile_start, int i)
 {
     int lo = 0, hi = p.B - 1;   // the last b with tile_start[b] <= i
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (p.tile_start[mid] <= i)
+        if (tile_start[mid] <= i)
             lo = mid;
         else
             hi = mid - 1;
@@ -99,7 +101,7 @@ __device__ __forceinline__ ExtTile tile_at(const ExtendParams &p, int i)
     int r, n;
     q_rows(p, lo, r, n);
     k_rows(p, lo, t.k0, t.m);
-    const int first = (i - p.tile_start[lo]) * 2 * p.tps;
+    const int first = (i - tile_start[lo]) * 2 * p.tps;
     t.b = lo;
     t.row0 = r + first;
     t.ntok = min(2 * p.tps, n - first);
@@ -117,9 +119,13 @@ __global__ void __launch_bounds__(PT, 1) extend_plan_kernel(const ExtendParams p
     __shared__ long long sums[32];
     __shared__ int maxs[32];
     __shared__ int hist[BUCKETS * PW];   // bucket-major, then warp
+    __shared__ int near_start[NEAR], near_blk[NEAR];
+    __shared__ long long near_sum[NEAR + 1];
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int Hv = p.Hkv * p.NG;
     const int tt = 2 * p.tps;
+
+    int *start = p.B <= NEAR ? near_start : p.tile_start;
 
     // tiles before each sequence, and the most blocks of any tile
     long long tiles = 0;
@@ -139,12 +145,14 @@ __global__ void __launch_bounds__(PT, 1) extend_plan_kernel(const ExtendParams p
         const long long s = tiles + scan_block(nt, sums, total);
         tiles += total;
         if (b < p.B)
-            p.tile_start[b] = (int)min(s - nt, (long long)p.max_tiles);
+            start[b] = (int)min(s - nt, (long long)p.max_tiles);
     }
     if (bad)
         atomicOr(p.status, STATUS_BAD_OFFSETS);
     const int n = (int)min(tiles, (long long)p.max_tiles);   // fewer only if offsets overlap
     top = max(1, max_block(top, maxs));
+    int *blk = n <= NEAR ? near_blk : p.tile_blk;   // blocks of the sorted tiles
+    long long *sum = n <= NEAR ? near_sum : p.cost_sum;
 
     // stable counting sort by descending cost, each warp its share in order
     for (int i = tid; i < BUCKETS * PW; i += PT)
@@ -154,7 +162,7 @@ __global__ void __launch_bounds__(PT, 1) extend_plan_kernel(const ExtendParams p
     const int i0 = w * share, i1 = min(n, i0 + share);
     for (int i = i0; i < i1; i += 32) {
         const bool on = i + lane < i1;
-        const int key = on ? BUCKETS - 1 - (int)((long long)tile_at(p, i + lane).nblk * (BUCKETS - 1) / top) : BUCKETS;
+        const int key = on ? BUCKETS - 1 - (int)((long long)tile_at(p, start, i + lane).nblk * (BUCKETS - 1) / top) : BUCKETS;
         const unsigned same = __match_any_sync(FULL_MASK, key);
         if (on && lane == __ffs(same) - 1)
             hist[key * PW + w] += __popc(same);
@@ -175,7 +183,7 @@ __global__ void __launch_bounds__(PT, 1) extend_plan_kernel(const ExtendParams p
         ExtTile t = {};
         int key = BUCKETS;
         if (on) {
-            t = tile_at(p, i + lane);
+            t = tile_at(p, start, i + lane);
             key = BUCKETS - 1 - (int)((long long)t.nblk * (BUCKETS - 1) / top);
         }
         const unsigned same = __match_any_sync(FULL_MASK, key);
@@ -185,6 +193,7 @@ __global__ void __launch_bounds__(PT, 1) extend_plan_kernel(const ExtendParams p
         __syncwarp();
         if (on) {
             p.tiles[at] = t;
+            blk[at] = t.nblk;
             if (lane == __ffs(same) - 1)
                 hist[key * PW + w] += __popc(same);
         }
@@ -197,14 +206,14 @@ __global__ void __launch_bounds__(PT, 1) extend_plan_kernel(const ExtendParams p
     for (int j0 = 0; j0 < n; j0 += PT) {
         const int j = j0 + tid;
         long long total;
-        const long long c = j < n ? (long long)Hv * (p.tiles[j].nblk + EXT_START) : 0;
+        const long long c = j < n ? (long long)Hv * (blk[j] + EXT_START) : 0;
         const long long s = all + scan_block(c, sums, total);
         all += total;
         if (j < n)
-            p.cost_sum[j] = s - c;
+            sum[j] = s - c;
     }
     if (tid == 0)
-        p.cost_sum[n] = all;
+        sum[n] = all;
     __syncthreads();
 
     // whole waves, as many as leave every CTA within its even share
@@ -212,12 +221,12 @@ __global__ void __launch_bounds__(PT, 1) extend_plan_kernel(const ExtendParams p
     const long long items = (long long)n * Hv;
     const long long even = (all + G - 1) / G;
     int waves = (int)(items / G);
-    if (n > 0 && p.tiles[0].nblk + EXT_START > even)
+    if (n > 0 && blk[0] + EXT_START > even)
         waves = 0;
     int load = 0;
     auto cost_of = [&](int wave) {
         const long long it = (long long)wave * G + ((wave & 1) ? G - 1 - tid : tid);
-        return p.tiles[it / Hv].nblk + EXT_START;
+        return blk[(int)it / Hv] + EXT_START;
     };
     if (tid < G) {
 #pragma unroll 4
@@ -233,7 +242,7 @@ __global__ void __launch_bounds__(PT, 1) extend_plan_kernel(const ExtendParams p
     // what is left, cut so that every CTA reaches the even share
     const long long first = (long long)waves * G;
     const int jf = (int)(first / Hv), hf = (int)(first % Hv);
-    const long long base = jf < n ? p.cost_sum[jf] + (long long)hf * (p.tiles[jf].nblk + EXT_START) : all;
+    const long long base = jf < n ? sum[jf] + (long long)hf * (blk[jf] + EXT_START) : all;
     const long long rest = all - base;
     long long cap = 0;
     if (tid < G) {
@@ -254,13 +263,13 @@ __global__ void __launch_bounds__(PT, 1) extend_plan_kernel(const ExtendParams p
             int lo = 0, hi = n - 1;   // the last tile with cost_sum <= v
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
-                if (p.cost_sum[mid] <= v)
+                if (sum[mid] <= v)
                     lo = mid;
                 else
                     hi = mid - 1;
             }
-            const int cost = p.tiles[lo].nblk + EXT_START;
-            const long long in = v - p.cost_sum[lo];
+            const int cost = blk[lo] + EXT_START;
+            const long long in = v - sum[lo];
             c.item = lo * Hv + (int)(in / cost);
             c.off = (int)(in % cost);
             c.blk = max(0, c.off - EXT_START);
@@ -273,70 +282,124 @@ __global__ void __launch_bounds__(PT, 1) extend_plan_kernel(const ExtendParams p
     }
 }
 
-// The merge of the split items: CTA (c, y) joins the pieces of the item whose
-// first cut is c, rows y * MROWS on, a warp a row, in the order of the cuts:
+// The merge of the split items, a warp a row, the pieces in the order of the
+// cuts:
 //     M = max m_i,  out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.
-constexpr int MROWS = 16;
+// Every CTA reads the cuts, lists the split items and their rows, and takes
+// its share of all those rows.
+constexpr int MT = 128;         // threads
+constexpr int MAX_CUTS = 1024;
 
-template <int D> __global__ void __launch_bounds__(128) extend_merge_kernel(const ExtendParams p)
+template <int D> __global__ void __launch_bounds__(MT) extend_merge_kernel(const ExtendParams p)
 {
+    __shared__ ExtCut cuts[MAX_CUTS + 1];
+    __shared__ int first[MAX_CUTS];      // the first cut of each split item
+    __shared__ int rows[MAX_CUTS + 1];   // rows before it
+    __shared__ int warp_n[MT / 32], warp_r[MT / 32];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int c0 = blockIdx.x + 1;   // cuts 1 .. grid - 1 may lie inside an item
-    const ExtCut cut = p.cuts[c0];
-    if (cut.blk == 0)
-        return;
-    if (c0 > 1) {
-        const ExtCut before = p.cuts[c0 - 1];
-        if (before.item == cut.item && before.blk > 0)
-            return;   // not the item's first cut
-    }
-    int c1 = c0 + 1;   // the cuts inside the item: [c0, c1)
-    while (c1 < p.grid && p.cuts[c1].item == cut.item && p.cuts[c1].blk > 0)
-        ++c1;
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int Hv = p.Hkv * p.NG;
-    const ExtTile t = p.tiles[cut.item / Hv];
-    const int vh = cut.item % Hv, h = vh / p.NG, s = vh % p.NG;
-    const int gv = min(p.Gs, p.G - s * p.Gs), hq0 = h * p.G + s * p.Gs;
-    const float vs = p.f8 ? p.v_scale[(long long)t.b * p.Hkv + h] : 1.f;
-    const int lane = threadIdx.x & 31;
+    for (int c = tid; c <= p.grid; c += MT)
+        cuts[c] = p.cuts[c];
+    __syncthreads();
+    // cuts inside an item: 1 .. grid - 1 with blocks before them
+    int n = 0, total = 0;
+    for (int base = 1; base < p.grid; base += MT) {
+        const int c = base + tid;
+        const bool is = c < p.grid && cuts[c].blk > 0 && !(cuts[c - 1].item == cuts[c].item && cuts[c - 1].blk > 0);
+        int r = 0;
+        if (is)
+            r = min(p.tiles[cuts[c].item / Hv].ntok, 2 * p.tps) * p.Gs;
+        const unsigned vote = __ballot_sync(FULL_MASK, is);
+        int sum = r;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(FULL_MASK, sum, o);
+            if (lane >= o)
+                sum += y;
+        }
+        if (lane == 31) {
+            warp_n[w] = __popc(vote);
+            warp_r[w] = sum;
+        }
+        __syncthreads();
+        int bn = n, br = total;
+        for (int i = 0; i < MT / 32; ++i) {
+            if (i < w) {
+                bn += warp_n[i];
+                br += warp_r[i];
+            }
+            n += warp_n[i];
+            total += warp_r[i];
+        }
+        if (is) {
+            const int at = bn + __popc(vote & ((1u << lane) - 1));
+            first[at] = c;
+            rows[at] = br + sum - r;
+        }
+        __syncthreads();
+    }
+
     constexpr int E = D / 32;
-    for (int r = blockIdx.y * MROWS + (threadIdx.x >> 5); r < (int)(blockIdx.y + 1) * MROWS; r += 4) {
-        const int in = r % EXT_M, tok = r / EXT_M * p.tps + in / p.Gs, g = in % p.Gs;
-        if (in >= p.tps * p.Gs || tok >= t.ntok || g >= gv)
+    for (int x = blockIdx.x * (MT / 32) + w; x < total; x += gridDim.x * (MT / 32)) {
+        int lo = 0, hi = n - 1;   // the last item with rows <= x
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (rows[mid] <= x)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        const int c0 = first[lo];
+        const ExtCut cut = cuts[c0];
+        const ExtTile t = p.tiles[cut.item / Hv];
+        const int vh = cut.item % Hv, h = vh / p.NG, s = vh % p.NG;
+        const int gv = min(p.Gs, p.G - s * p.Gs), hq0 = h * p.G + s * p.Gs;
+        const int tok = (x - rows[lo]) / p.Gs, g = (x - rows[lo]) % p.Gs;
+        if (g >= gv)
             continue;
+        const int r = tok / p.tps * EXT_M + tok % p.tps * p.Gs + g;   // its row of the partials
         float o[E], M = -INFINITY, L = 0.f;
 #pragma unroll
         for (int e = 0; e < E; ++e)
             o[e] = 0.f;
-#pragma unroll 4
-        for (int i = c0 - 1; i < c1; ++i) {
-            // the piece left of the first cut, then the one right of each
-            // (none where two cuts coincide)
-            const int slot = i < c0 ? 2 * c0 : 2 * i + 1;
-            const bool some = i < c0 || p.cuts[i + 1].item != cut.item || p.cuts[i + 1].blk > p.cuts[i].blk;
-            if (!some)
-                continue;
-            const long long row = (long long)slot * 2 * EXT_M + r;
-            const float2 ml = __ldcg(p.part_ml + row);
-            float v[E];
-            const float *src = p.part_o + row * D + lane * E;
-            if (E == 4) {
-                const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
-                v[0] = x.x, v[1] = x.y, v[E - 2] = x.z, v[E - 1] = x.w;
-            } else {
-                const float2 x = __ldcg(reinterpret_cast<const float2 *>(src));
-                v[0] = x.x, v[1] = x.y;
-            }
-            if (!(ml.y <= 0.f)) {
-                const float mn = fmaxf(M, ml.x);
-                const float a = ex2(M - mn), b = ex2(ml.x - mn);
+        // the piece left of the first cut, then the one right of each cut
+        // inside the item (none where two cuts coincide)
+        for (int i = c0 - 1; i == c0 - 1 || (i < p.grid && cuts[i].item == cut.item); i += 4) {
+            float2 ml[4];
+            float v[4][E];
 #pragma unroll
-                for (int e = 0; e < E; ++e)
-                    o[e] = fmaf(b, v[e], a * o[e]);
-                L = fmaf(L, a, b * ml.y);
-                M = mn;
+            for (int u = 0; u < 4; ++u) {
+                const int k = i + u;
+                const bool some = k < c0 || (k < p.grid && cuts[k].item == cut.item &&
+                                             (cuts[k + 1].item != cut.item || cuts[k + 1].blk > cuts[k].blk));
+                const long long row = (long long)(some ? (k < c0 ? 2 * c0 : 2 * k + 1) : 2 * c0) * 2 * EXT_M + r;
+                ml[u] = __ldcg(p.part_ml + row);
+                const float *src = p.part_o + row * D + lane * E;
+                if (E == 4) {
+                    const float4 y = __ldcg(reinterpret_cast<const float4 *>(src));
+                    v[u][0] = y.x, v[u][1] = y.y, v[u][E - 2] = y.z, v[u][E - 1] = y.w;
+                } else {
+                    const float2 y = __ldcg(reinterpret_cast<const float2 *>(src));
+                    v[u][0] = y.x, v[u][1] = y.y;
+                }
+                if (!some)
+                    ml[u].y = 0.f;
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (!(ml[u].y <= 0.f)) {
+                    const float mn = fmaxf(M, ml[u].x);
+                    const float a = ex2(M - mn), b = ex2(ml[u].x - mn);
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        o[e] = fmaf(b, v[u][e], a * o[e]);
+                    L = fmaf(L, a, b * ml[u].y);
+                    M = mn;
+                }
             }
         }
+        const float vs = p.f8 ? p.v_scale[(long long)t.b * p.Hkv + h] : 1.f;
         const long long qrow = (long long)(t.row0 + tok) * p.Hq + hq0 + g;
         const bool any = !(L <= 0.f);   // NaN counts: it is the result then
         const float inv = any ? vs / L : 0.f;
@@ -361,8 +424,8 @@ cudaError_t launch_extend_merge(const ExtendParams &p, cudaStream_t s)
     if (p.grid < 2)
         return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.grid - 1, 2 * EXT_M / MROWS);
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3(4 * p.grid);
+    cfg.blockDim = dim3(MT);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

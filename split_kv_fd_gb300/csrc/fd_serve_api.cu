@@ -82,7 +82,7 @@ bool map_8bit(CUtensorMap *m, const void *base, int d, long long n1, long long n
 struct ExtLayout {
     int G, NG, Gs, tps, grid;
     long long max_tiles;
-    size_t header, tile_start, tiles, cost_sum, cuts, part_ml, part_o, total;
+    size_t header, tile_start, tile_blk, tiles, cost_sum, cuts, part_ml, part_o, total;
 };
 
 bool ext_layout(int B, int total_q, int Hq, int Hkv, int d, ExtLayout &l)
@@ -106,7 +106,8 @@ bool ext_layout(int B, int total_q, int Hq, int Hkv, int d, ExtLayout &l)
         return was;
     };
     l.header = take(sizeof(ExtPlanHeader));
-    l.tile_start = take((size_t)(B + 1) * sizeof(int));
+    l.tile_start = take((size_t)B * sizeof(int));
+    l.tile_blk = take((size_t)l.max_tiles * sizeof(int));
     l.tiles = take((size_t)l.max_tiles * sizeof(ExtTile));
     l.cost_sum = take((size_t)(l.max_tiles + 1) * sizeof(long long));
     l.cuts = take((size_t)(l.grid + 1) * sizeof(ExtCut));
@@ -142,6 +143,7 @@ fd_status run_extend(ExtendParams &p, float scale, void *workspace, size_t works
     char *ws = static_cast<char *>(workspace);
     p.header = reinterpret_cast<ExtPlanHeader *>(ws + l.header);
     p.tile_start = reinterpret_cast<int *>(ws + l.tile_start);
+    p.tile_blk = reinterpret_cast<int *>(ws + l.tile_blk);
     p.tiles = reinterpret_cast<ExtTile *>(ws + l.tiles);
     p.cost_sum = reinterpret_cast<long long *>(ws + l.cost_sum);
     p.cuts = reinterpret_cast<ExtCut *>(ws + l.cuts);
