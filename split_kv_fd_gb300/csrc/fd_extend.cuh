@@ -15,21 +15,34 @@
 // P is rounded to the inputs' 16-bit type for the product with V (half a
 // step of each weight), sums of weights stay float32 and unrounded.
 //
-// While one sub-tile's softmax runs, the tensor cores work on the other's
-// products.  S of a sub-tile's next block is issued behind P.V of the one
-// before, so that S's commit also says that P.V is done: a row's rescale
-// needs no wait of its own.
+// Two engines, each with a warpgroup of softmax and S, P and O of its own in
+// tensor memory, keep the tensor cores busy by turns: engine x takes
+// sub-tile x, both on the same K/V blocks.  Where a tile has only one
+// sub-tile (a few drafted tokens), the engines share it instead: engine x
+// takes every other block and the two results are joined at the end, so
+// that the time of a block is half that of the chain S, softmax, P.V.
 //
-// Warp roles (384 threads, 512 for E4M3 K/V, one CTA per SM):
-//  - warps 0-3, 4-7: softmax and results of sub-tile A, B;
-//  - warp 8: K and V by tensor-map TMA, in turn, into one ring;
-//  - warp 9: allocates TMEM, issues every MMA;
+// P lies in the columns of its S, and S of an engine's next block follows
+// P.V of the one before, so S's commit also says that P.V is done.  (At
+// d = 64 there is room for P beside S; with S of the next block issued as
+// soon as the softmax had read this one, both engines fell into step on the
+// special-function units: 373 us against 325 for 8192 tokens of 32 heads.)
+//
+// Warp roles (384 threads, 640 for E4M3 K/V, one CTA per SM):
+//  - warps 0-3, 4-7: softmax and results of engines 0 and 1;
+//  - warp 8: K and V by tensor-map TMA into one ring;
+//  - warp 9: allocates TMEM, issues every MMA, engine 0's and engine 1's by
+//    turns (a warp for each engine let them fall into step on the
+//    special-function units: 3050 us against 2590 for 16384 tokens of 64
+//    heads);
 //  - warp 10: Q by TMA, as soon as a sub-tile's last S is done;
 //  - warp 11: walks the CTA's share of the plan, segments into a small ring;
-//  - E4M3 only, warps 12-15: widen the blocks that warp 8 copied as they are
-//    to the 16-bit type (exact: E4M3 has 4 significant bits and exponents
-//    from -9 to 8) for the same products.  The K scale is part of the
-//    score's, the V scale of the result's.
+//  - E4M3 only, warps 12-19: widen the blocks that warp 8 copied as they are
+//    to f16 (exact: E4M3 has 4 significant bits and exponents from -9 to 8)
+//    for the same products.  A bf16 Q becomes f16 too, each row brought to
+//    a maximum in [2^8, 2^9) by a power of two that its scores undo: exact
+//    but for elements 2^22 times smaller than that.  The K scale is part of
+//    the score's, the V scale of the result's.
 // Every hand-off is an mbarrier, and every wait is bounded: on expiry a role
 // records FD_ERR_DEVICE_TIMEOUT, stops, waits for the copies it issued, and
 // the CTA frees its TMEM.
@@ -41,6 +54,7 @@
 
 namespace fd {
 
+// T: the type of the MMAs (f16 for E4M3 K/V).
 template <typename T, int D, bool F8> struct ExtCfg {
     static constexpr int M = EXT_M, CT = EXT_CT;
     static constexpr int PLANES = D / 64;                // 128-byte planes of a row
@@ -48,23 +62,26 @@ template <typename T, int D, bool F8> struct ExtCfg {
     static constexpr int BLOCK_BYTES = PLANES * PLANE;   // K or V of one block
     static constexpr int Q_BYTES = PLANES * PLANE;       // one sub-tile
     // 16-bit K and V: 160 KB of copies in flight.  E4M3: the copies land in
-    // a ring of raw blocks, and two 16-bit stages (one K, one V) suffice.
-    static constexpr int STAGES = F8 ? (D == 128 ? 2 : 4) : (D == 128 ? 5 : 10);
+    // a ring of raw blocks, and two 16-bit stages suffice.
+#ifndef FD_EXT_F8_STAGES
+#define FD_EXT_F8_STAGES 3
+#endif
+    static constexpr int STAGES = (F8 ? FD_EXT_F8_STAGES : 5) * (128 / D);
     static constexpr int RAW_BYTES = CT * D;             // an E4M3 block
-    static constexpr int RAWS = F8 ? (D == 128 ? 6 : 12) : 0;
-    static constexpr int SEGS = 4;                       // segments the scheduler runs ahead
+    static constexpr int RAWS = F8 ? 2 * (5 - FD_EXT_F8_STAGES) * (128 / D) : 0;
+    static constexpr int SEGS = 3;                       // segments the scheduler runs ahead
     static constexpr int KV_WARP = 8, MMA_WARP = 9, Q_WARP = 10, SCHED_WARP = 11, CVT_WARP = 12;
-    static constexpr int THREADS = F8 ? 512 : 384;
+    static constexpr int CVT_WARPS = 8;
+    static constexpr int THREADS = F8 ? 640 : 384;
     // registers a thread: the softmax warpgroups hold a row of S each; the
-    // shares add up to the launch's (168 x 384 and 128 x 512)
-    static constexpr int REGS_SOFTMAX = F8 ? 200 : 208, REGS_OTHER = F8 ? 56 : 88;
-    static_assert(2 * REGS_SOFTMAX + (THREADS / 128 - 2) * REGS_OTHER == (F8 ? 4 * 128 : 3 * 168), "register shares");
-    // TMEM columns: S of A and B, O of A and B; P takes the first half of
-    // its S (D = 128), or columns of its own where there are some (D = 64)
+    // shares add up to the launch's (168 x 384 and 96 x 640)
+    static constexpr int REGS_SOFTMAX = F8 ? 168 : 208, REGS_OTHER = F8 ? 48 : 88;
+    static_assert(2 * REGS_SOFTMAX + (THREADS / 128 - 2) * REGS_OTHER == (F8 ? 5 * 96 : 3 * 168), "register shares");
+    // TMEM columns: S and O of both engines, P in the first half of its S
     static constexpr int TM_O = 2 * CT;
     __host__ __device__ static constexpr int tm_s(int x) { return x * CT; }
     __host__ __device__ static constexpr int tm_o(int x) { return TM_O + x * D; }
-    __host__ __device__ static constexpr int tm_p(int x) { return D == 128 ? x * CT : TM_O + 2 * D + x * (CT / 2); }
+    __host__ __device__ static constexpr int tm_p(int x) { return x * CT; }
     static constexpr uint32_t TMEM_COLS = 512;
     static constexpr float TAU = 8.f;
     // f16 weights carry a factor 2^7 (the sum does too): below 2^-14 an f16
@@ -72,10 +89,21 @@ template <typename T, int D, bool F8> struct ExtCfg {
     // bf16 has float32's range and needs none.
     static constexpr float SHIFT = std::is_same<T, __half>::value ? 7.f : 0.f;
     static constexpr uint32_t SLEEP_NS = 100000;
-    // barriers: ring full/empty, S, both halves of P, O, Q full, Q empty of both sub-tiles,
-    // segments full/empty, the last commit, raw ring full/empty
-    static constexpr int NBAR = 2 * STAGES + 12 + 2 * SEGS + 1 + 2 * RAWS;
-    static constexpr int SMEM = 1024 + STAGES * BLOCK_BYTES + RAWS * RAW_BYTES + 2 * Q_BYTES + NBAR * 8 + 16 + SEGS * 64;
+    // P is handed over in two parts, so that its product with V runs while
+    // the softmax computes the rest: the first part's product takes longer
+    // than that.
+#ifndef FD_EXT_PART
+#define FD_EXT_PART 96
+#endif
+    static constexpr int PART = FD_EXT_PART;
+    // barriers: ring full/empty; S full, both parts of P, O, Q
+    // full, Q empty, Q widened of each engine or sub-tile; the engines'
+    // meeting, the last commit; segments full/empty; raw ring full/empty
+    static constexpr int NBAR = 2 * STAGES + 14 + 2 + 2 * SEGS + 2 * RAWS;
+    static constexpr int XCH_BYTES = 2 * M * 8;          // (reference, sum) of both engines' rows
+    static constexpr int QEXP_BYTES = F8 ? 2 * 2 * M : 0;   // exponents of Q's rows, two in flight
+    static constexpr int SMEM = STAGES * BLOCK_BYTES + RAWS * RAW_BYTES + 2 * Q_BYTES + NBAR * 8 + 16 + SEGS * 56 +
+                                XCH_BYTES + QEXP_BYTES;
     static_assert(SMEM <= 232448, "shared memory");
 };
 
@@ -87,10 +115,31 @@ struct ExtSeg {
     int h, slice, b;
     int m, lim, k0;
     int blk0, blk[2];    // blocks [blk0, blk[x]) of sub-tile x
+    int twin;            // one sub-tile, its blocks dealt to both engines
     int slot;            // partial result, or -1: the whole item
 };
 
-__device__ __forceinline__ int ext_end(const ExtSeg &g) { return max(g.blk[0], g.blk[1]); }
+__device__ __forceinline__ int ext_blocks(const ExtSeg &g) { return max(g.blk[0], g.blk[1]) - g.blk0; }
+
+// The order of a segment's n blocks in the ring: K(0), V(0), K(1), V(1), ...,
+// or with K one block ahead (S of the next block is wanted before P.V of
+// this one) K(0), K(1), V(0), K(2), V(1), ..., V(n-1).
+struct ExtOrder {
+    bool ahead;
+    int n;
+    __device__ __forceinline__ int k_at(int i) const { return ahead && i ? 2 * i - 1 : 2 * i; }
+    __device__ __forceinline__ int v_at(int i) const { return ahead && i < n - 1 ? 2 * i + 2 : 2 * i + 1; }
+    // The other way round: item t of 2n is V (or K) of block i.
+    __device__ __forceinline__ bool item(int t, int &i) const
+    {
+        if (!ahead || t == 0 || t == 2 * n - 1) {
+            i = t >> 1;
+            return t & 1;
+        }
+        i = (t & 1) ? (t + 1) >> 1 : (t >> 1) - 1;
+        return !(t & 1);
+    }
+};
 
 // 32 bytes at a 32-byte aligned address in one store.
 __device__ __forceinline__ void stg256(void *ptr, const uint32_t (&w)[8])
@@ -100,11 +149,11 @@ __device__ __forceinline__ void stg256(void *ptr, const uint32_t (&w)[8])
                  : "memory");
 }
 
-// 32 consecutive outputs, times f, from index idx (a multiple of 32) of a
+// 32 consecutive outputs from index idx (a multiple of 32) of a
 // 16-byte aligned tensor.  A thread writes its own row, so a store touches
 // as many lines as the warp has rows whatever its width: 32-byte stores (a
 // whole sector each) where the tensor allows them.
-__device__ __forceinline__ void store_out32(void *out, long long idx, int out_dtype, const float *x, float f)
+__device__ __forceinline__ void store_out32(void *out, long long idx, int out_dtype, const float *x)
 {
     char *at = static_cast<char *>(out) + idx * (out_dtype == 0 ? 4 : 2);
     const bool wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
@@ -117,11 +166,11 @@ __device__ __forceinline__ void store_out32(void *out, long long idx, int out_dt
         if (out_dtype == 0) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                w[e] = __float_as_uint(x[8 * i + e] * f);
+                w[e] = __float_as_uint(x[8 * i + e]);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float a = x[(16 * i + 2 * e) & 31] * f, b = x[(16 * i + 2 * e + 1) & 31] * f;
+                const float a = x[(16 * i + 2 * e) & 31], b = x[(16 * i + 2 * e + 1) & 31];
                 w[e] = out_dtype == 1 ? Mma<__half>::pack(a, b) : Mma<__nv_bfloat16>::pack(a, b);
             }
         }
@@ -135,8 +184,8 @@ __device__ __forceinline__ void store_out32(void *out, long long idx, int out_dt
     }
 }
 
-// 16 E4M3 values as the 16-bit type, exactly: two 16-byte vectors.
-template <typename T> __device__ __forceinline__ void e4m3_widen16(const uint4 &u, uint4 &lo, uint4 &hi)
+// 16 E4M3 values as f16, exactly: two 16-byte vectors.
+__device__ __forceinline__ void e4m3_widen16(const uint4 &u, uint4 &lo, uint4 &hi)
 {
     const uint32_t in[4] = {u.x, u.y, u.z, u.w};
     uint32_t r[8];
@@ -148,13 +197,6 @@ template <typename T> __device__ __forceinline__ void e4m3_widen16(const uint4 &
             "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
             : "=r"(r[2 * i]), "=r"(r[2 * i + 1])
             : "r"(in[i]));
-    }
-    if (std::is_same<T, __nv_bfloat16>::value) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float2 f = Mma<__half>::unpack(r[i]);
-            r[i] = Mma<__nv_bfloat16>::pack(f.x, f.y);
-        }
     }
     lo = make_uint4(r[0], r[1], r[2], r[3]);
     hi = make_uint4(r[4], r[5], r[6], r[7]);
@@ -169,84 +211,85 @@ __device__ __forceinline__ void sts128(uint32_t a, const uint4 &v)
 template <int R> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 
-template <typename T, int D, bool F8>
-__global__ void __launch_bounds__(ExtCfg<T, D, F8>::THREADS, 1) extend_kernel(const __grid_constant__ ExtendParams p)
-{
+// The CTA's shared memory, and a segment ring cursor per warp.
+template <typename T, int D, bool F8> struct ExtCta {
     using C = ExtCfg<T, D, F8>;
-    constexpr int ST = C::STAGES;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the merge waits for this grid's end
-    extern __shared__ __align__(128) unsigned char smem_raw[];
-    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-    const uint32_t raw = smem_addr(smem_raw);
-    unsigned char *smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);   // 1024-aligned
-    const uint32_t ring = smem_addr(smem);
-    const uint32_t rawring = ring + ST * C::BLOCK_BYTES;
-    const uint32_t qbuf = rawring + C::RAWS * C::RAW_BYTES;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + ST * C::BLOCK_BYTES + C::RAWS * C::RAW_BYTES + 2 * C::Q_BYTES);
-    uint32_t *misc = reinterpret_cast<uint32_t *>(bars + C::NBAR);
-    volatile ExtSeg *segs = reinterpret_cast<volatile ExtSeg *>(misc + 4);
-    static_assert(sizeof(ExtSeg) <= 64, "segment slots");
-    const uint32_t bar0 = smem_addr(bars);
-    auto FULL = [&](int s) { return bar0 + 8u * (uint32_t)s; };
-    auto EMPTY = [&](int s) { return bar0 + 8u * (uint32_t)(ST + s); };
-    constexpr int B0 = 2 * ST;
-    auto SFULL = [&](int x) { return bar0 + 8u * (uint32_t)(B0 + x); };
-    auto PFULL = [&](int x, int half) { return bar0 + 8u * (uint32_t)(B0 + 2 + 2 * x + half); };
-    auto OFULL = [&](int x) { return bar0 + 8u * (uint32_t)(B0 + 6 + x); };
-    auto QFULL = [&](int x) { return bar0 + 8u * (uint32_t)(B0 + 8 + x); };
-    auto QEMPTY = [&](int x) { return bar0 + 8u * (uint32_t)(B0 + 10 + x); };
-    auto GFULL = [&](int s) { return bar0 + 8u * (uint32_t)(B0 + 12 + s); };
-    auto GEMPTY = [&](int s) { return bar0 + 8u * (uint32_t)(B0 + 12 + C::SEGS + s); };
-    const uint32_t FIN = bar0 + 8u * (uint32_t)(B0 + 12 + 2 * C::SEGS);
-    auto RFULL = [&](int s) { return FIN + 8u * (uint32_t)(1 + s); };
-    auto REMPTY = [&](int s) { return FIN + 8u * (uint32_t)(1 + C::RAWS + s); };
+    uint32_t ring, raw, qbuf, bar0;
+    volatile ExtSeg *segs;
+    float2 *xch;            // [2][M]
+    signed char *qexp;      // [2 in flight][2][M]
+    int lane;
+    int sg = 0;             // segments taken so far
+    bool dead = false;
 
-    if (tid == 0) {
-        for (int s = 0; s < ST; ++s) {
-            mbar_init(FULL(s), F8 ? 4 : 1);   // the producer's arrival plus the copy's bytes, or the converting warps
-            mbar_init(EMPTY(s), 1);   // commit behind the block's last MMA
+    __device__ __forceinline__ uint32_t bar(int i) const { return bar0 + 8u * (uint32_t)i; }
+    __device__ __forceinline__ uint32_t full(int s) const { return bar(s); }
+    __device__ __forceinline__ uint32_t empty(int s) const { return bar(C::STAGES + s); }
+    static constexpr int B0 = 2 * C::STAGES;
+    __device__ __forceinline__ uint32_t s_full(int x) const { return bar(B0 + x); }
+    __device__ __forceinline__ uint32_t p_full(int x, int part) const { return bar(B0 + 2 + 2 * x + part); }
+    __device__ __forceinline__ uint32_t o_full(int x) const { return bar(B0 + 6 + x); }
+    __device__ __forceinline__ uint32_t q_full(int x) const { return bar(B0 + 8 + x); }
+    __device__ __forceinline__ uint32_t q_empty(int x) const { return bar(B0 + 10 + x); }
+    __device__ __forceinline__ uint32_t q_wide(int x) const { return bar(B0 + 12 + x); }
+    __device__ __forceinline__ uint32_t meet() const { return bar(B0 + 14); }
+    __device__ __forceinline__ uint32_t fin() const { return bar(B0 + 15); }
+    static constexpr int B1 = B0 + 16;
+    __device__ __forceinline__ uint32_t g_full(int s) const { return bar(B1 + s); }
+    __device__ __forceinline__ uint32_t g_empty(int s) const { return bar(B1 + C::SEGS + s); }
+    static constexpr int B2 = B1 + 2 * C::SEGS;
+    __device__ __forceinline__ uint32_t r_full(int s) const { return bar(B2 + s); }
+    __device__ __forceinline__ uint32_t r_empty(int s) const { return bar(B2 + C::RAWS + s); }
+    static_assert(B2 + 2 * C::RAWS == C::NBAR, "barrier count");
+
+    __device__ __forceinline__ void init()
+    {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(full(s), F8 ? 4 : 1);   // the producer's arrival plus the copy's bytes, or the widening warps
+            mbar_init(empty(s), 1);           // commit behind the block's last MMA
         }
         for (int x = 0; x < 2; ++x) {
-            mbar_init(SFULL(x), 1);   // commit behind S
-            // the sub-tile's warps: S read, O rescaled, a half of P written
-            mbar_init(PFULL(x, 0), 4);
-            mbar_init(PFULL(x, 1), 4);
-            mbar_init(OFULL(x), 1);   // commit behind the segment's last P.V
-            mbar_init(QFULL(x), 1);
-            mbar_init(QEMPTY(x), 1);  // commit behind the segment's last S
+            mbar_init(s_full(x), 1);          // commit behind S
+            mbar_init(p_full(x, 0), 4);       // the engine's warps: S read, O rescaled, a part of P written
+            mbar_init(p_full(x, 1), 4);
+            mbar_init(o_full(x), 1);          // commit behind the segment's last P.V
+            mbar_init(q_full(x), 1);
+            mbar_init(q_empty(x), 1);         // commit behind the segment's last S
+            mbar_init(q_wide(x), 4);          // a group of the widening warps
         }
+        mbar_init(meet(), 8);                 // the softmax warps of both engines
+        mbar_init(fin(), 1);
         for (int s = 0; s < C::SEGS; ++s) {
-            mbar_init(GFULL(s), 1);
-            mbar_init(GEMPTY(s), F8 ? 15 : 11); // K/V, MMA, Q, the eight softmax warps and the converting ones
+            mbar_init(g_full(s), 1);
+            mbar_init(g_empty(s), F8 ? 11 + C::CVT_WARPS : 11);   // every warp but the scheduler
         }
         for (int s = 0; s < C::RAWS; ++s) {
-            mbar_init(RFULL(s), 1);
-            mbar_init(REMPTY(s), 4);
+            mbar_init(r_full(s), 1);
+            mbar_init(r_empty(s), 4);
         }
-        mbar_init(FIN, 1);
-        prefetch_tmap(&p.tmq);
-        prefetch_tmap(&p.tmk);
-        prefetch_tmap(&p.tmv);
     }
-    if (w == C::MMA_WARP) {
-        tmem_alloc(smem_addr(misc), C::TMEM_COLS);
-        tmem_relinquish();
+
+    // Wait of a whole warp for the n-th (from 0) completion of a barrier.
+    __device__ __forceinline__ bool wait(uint32_t b, int n)
+    {
+        if (!dead && !mbar_wait_bounded_soon(b, (uint32_t)(n & 1), C::SLEEP_NS))
+            dead = true;
+        return !dead;
     }
-    fence_mbar_init();
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = misc[0];
-    bool dead = false;
-    int sg = 0;   // segments taken so far
+
+    __device__ __forceinline__ void arrive(uint32_t b)
+    {
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(b);
+    }
 
     // The next segment, by a whole warp; false at the end (or on expiry).
-    auto next_seg = [&](ExtSeg &g) {
+    __device__ __forceinline__ bool next(ExtSeg &g)
+    {
         const int s = sg % C::SEGS;
-        if (!mbar_wait_bounded_soon(GFULL(s), (uint32_t)((sg / C::SEGS) & 1), C::SLEEP_NS)) {
-            dead = true;
+        if (!wait(g_full(s), sg / C::SEGS))
             return false;
-        }
         const volatile ExtSeg &x = segs[s];
         g.valid = x.valid;
         g.row0 = x.row0;
@@ -260,510 +303,713 @@ __global__ void __launch_bounds__(ExtCfg<T, D, F8>::THREADS, 1) extend_kernel(co
         g.blk0 = x.blk0;
         g.blk[0] = x.blk[0];
         g.blk[1] = x.blk[1];
+        g.twin = x.twin;
         g.slot = x.slot;
-        __syncwarp();
-        if (lane == 0)
-            mbar_arrive(GEMPTY(s));
+        arrive(g_empty(s));
         ++sg;
         return g.valid != 0;
-    };
+    }
+};
 
-    // (a warpgroup changes its share of the registers as a whole)
-    if (w >= 8) {
-        regs_dec<C::REGS_OTHER>();
-    if (w == C::SCHED_WARP) {
-        // ------------------------------------------------------------ scheduler
-        if (lane == 0) {
-            asm volatile("griddepcontrol.wait;" ::: "memory");
-            const int G = p.grid, c = blockIdx.x, Hv = p.Hkv * p.NG;
-            const ExtPlanHeader hd = *p.header;
-            const ExtCut a = p.cuts[c], e = p.cuts[c + 1];
-            // a segment of item `it`, blocks [blk0, blk1)
-            auto push = [&](int it, const ExtTile &t, int blk0, int blk1, int slot) {
-                const int s = sg % C::SEGS;
-                if (sg >= C::SEGS && !mbar_wait_bounded_sleep_thread(GEMPTY(s), (uint32_t)(((sg / C::SEGS) - 1) & 1),
-                                                                     C::SLEEP_NS)) {
-                    dead = true;
-                    return;
-                }
-                volatile ExtSeg &g = segs[s];
-                const int vh = it < 0 ? 0 : it % Hv;
-                g.valid = it >= 0;
-                g.row0 = t.row0;
-                g.ntok = t.ntok;
-                g.h = vh / p.NG;
-                g.slice = vh % p.NG;
-                g.b = t.b;
-                g.m = t.m;
-                g.lim = t.lim;
-                g.k0 = t.k0;
-                g.blk0 = blk0;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int n = min(t.ntok - x * p.tps, p.tps);   // the sub-tile's tokens
-                    const int see = n <= 0 ? 0 : p.causal ? min(t.m, t.lim + x * p.tps + n - 1) : t.m;
-                    const int end = see > 0 ? (see + C::CT - 1) / C::CT : 0;
-                    g.blk[x] = max(blk0, min(blk1, end));
-                }
-                g.slot = slot;
-                mbar_arrive(GFULL(s));
-                ++sg;
-            };
-            for (int it = a.item; it < hd.n_items && !dead; ++it) {
-                const bool last = it == e.item;
-                if (it > e.item || (last && e.off == 0))
-                    break;
-                const ExtTile t = p.tiles[it / Hv];
-                const bool fresh = it > a.item || a.off == 0;
-                const int b0 = it > a.item ? 0 : a.blk, b1 = last ? e.blk : t.nblk;
-                if (t.nblk == 0 ? !fresh : b1 <= b0)
-                    continue;
-                const bool whole = b0 == 0 && b1 == t.nblk;
-                push(it, t, b0, b1, whole ? -1 : b0 > 0 ? 2 * c + 1 : 2 * (c + 1));
-            }
-            for (int x = 0; x < hd.waves && !dead; ++x) {
-                const int it = x * G + ((x & 1) ? G - 1 - c : c);
-                const ExtTile t = p.tiles[it / Hv];
-                push(it, t, 0, t.nblk, -1);
-            }
-            if (!dead) {
-                const ExtTile none = {};
-                push(-1, none, 0, 0, -1);
-            }
+// ---------------------------------------------------------------- scheduler
+// One lane: the CTA's cut pieces first, then its whole items.
+template <typename T, int D, bool F8>
+__device__ __forceinline__ void ext_schedule(const ExtendParams &p, ExtCta<T, D, F8> &cta)
+{
+    using C = ExtCfg<T, D, F8>;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int G = p.grid, c = blockIdx.x, Hv = p.Hkv * p.NG;
+    const ExtPlanHeader hd = *p.header;
+    const ExtCut a = p.cuts[c], e = p.cuts[c + 1];
+    int sg = 0;
+    // a segment of item `it`, blocks [blk0, blk1)
+    auto push = [&](int it, const ExtTile &t, int blk0, int blk1, int slot) {
+        const int s = sg % C::SEGS;
+        if (sg >= C::SEGS &&
+            !mbar_wait_bounded_sleep_thread(cta.g_empty(s), (uint32_t)(((sg / C::SEGS) - 1) & 1), C::SLEEP_NS)) {
+            cta.dead = true;
+            return;
         }
-        __syncwarp();
-    } else if (w == C::KV_WARP) {
-        // ------------------------------------------------------------ K and V
-        // Blocks K(j), V(j), K(j+1), ...: each lane one box of a block (row
-        // group, plane), so the rows of a block may come from several pages.
-        const int R = p.paged ? p.box_rows : C::CT;
-        const int ng = C::CT / R;   // row groups (at most 8)
-        const int grp = lane % ng, plane = lane / ng;
-        const bool mine = plane < (F8 ? 1 : C::PLANES);
-        constexpr int NS = F8 ? C::RAWS : ST;
-        auto NFULL = [&](int s) { return F8 ? RFULL(s) : FULL(s); };
-        auto NEMPTY = [&](int s) { return F8 ? REMPTY(s) : EMPTY(s); };
-        long long n = 0;            // blocks issued
-        ExtSeg g;
-        while (!dead && next_seg(g)) {
-            const int end = ext_end(g);
-#pragma unroll 1
-            for (int j = g.blk0; j < end && !dead; ++j) {
-                int x = 0, y = 0;
-                const int tok = j * C::CT + grp * R;
-                const bool load = mine && tok < g.m;
-                if (!p.paged) {
-                    x = g.k0 + tok;
-                    y = g.h;
-                } else if (load) {
-                    int page = p.table[(long long)g.b * p.max_pages + tok / p.page_size];
-                    if (page < 0 || page >= p.num_pages) {
-                        atomicOr(p.status, STATUS_BAD_PAGE);
-                        page = 0;
-                    }
-                    x = tok % p.page_size;
-                    y = page * p.Hkv + g.h;
-                }
-                const uint32_t bytes = (uint32_t)__popc(__ballot_sync(FULL_MASK, load)) * (uint32_t)(R * (F8 ? D : 128));
+        volatile ExtSeg &g = cta.segs[s];
+        const int vh = it < 0 ? 0 : it % Hv;
+        g.valid = it >= 0;
+        g.row0 = t.row0;
+        g.ntok = t.ntok;
+        g.h = vh / p.NG;
+        g.slice = vh % p.NG;
+        g.b = t.b;
+        g.m = t.m;
+        g.lim = t.lim;
+        g.k0 = t.k0;
+        g.blk0 = blk0;
 #pragma unroll
-                for (int kv = 0; kv < 2; ++kv, ++n) {
-                    const int s = (int)(n % NS);
-                    if (n >= NS &&
-                        !mbar_wait_bounded_soon(NEMPTY(s), (uint32_t)(((n / NS) - 1) & 1), C::SLEEP_NS)) {
-                        dead = true;
-                        break;
-                    }
-                    if (lane == 0)
-                        mbar_arrive_expect_tx(NFULL(s), bytes);
-                    __syncwarp();
-                    const CUtensorMap *tm = kv ? &p.tmv : &p.tmk;
-                    if (F8 && load)
-                        tma_load_3d(rawring + (uint32_t)(s * C::RAW_BYTES + grp * R * D), tm, 0, x, y, NFULL(s));
-                    else if (load)
-                        tma_load_4d(ring + (uint32_t)(s * C::BLOCK_BYTES + plane * C::PLANE + grp * R * 128), tm, 0, x, y,
-                                    plane, NFULL(s));
-                }
-            }
+        for (int x = 0; x < 2; ++x) {
+            const int n = min(t.ntok - x * p.tps, p.tps);   // the sub-tile's tokens
+            const int see = n <= 0 ? 0 : p.causal ? min(t.m, t.lim + x * p.tps + n - 1) : t.m;
+            const int end = see > 0 ? (see + C::CT - 1) / C::CT : 0;
+            g.blk[x] = max(blk0, min(blk1, end));
         }
-        // no copy may be in flight when the CTA ends: the last fill of each stage
-        for (long long i = n > NS ? n - NS : 0; i < n; ++i)
-            mbar_wait_bounded_soon(NFULL((int)(i % NS)), (uint32_t)((i / NS) & 1), C::SLEEP_NS);
-    } else if (F8 && w >= C::CVT_WARP) {
-        // ------------------------------------------------------------ E4M3 to 16 bits
-        // A thread widens 16 values of a row at a time into the swizzled
-        // planes that the MMAs read.  Eight lanes read 128 bytes in a row;
-        // at d = 128 the upper four write the other plane, their two halves
-        // in the other order, so that the eight 16-byte writes of a phase
-        // fall in different banks.
-        constexpr int NR = F8 ? C::RAWS : 1;
-        constexpr int CPR = D / 16;   // 16-value pieces of a row
-        const int ct = tid - C::CVT_WARP * 32;
-        const int c = ct % CPR, r0 = ct / CPR;
-        const bool swap = (c >> 2) != 0;
-        long long n = 0;
-        ExtSeg g;
-        while (!dead && next_seg(g)) {
-            const int end = ext_end(g);
-#pragma unroll 1
-            for (int j = g.blk0; j < end && !dead; ++j) {
-                const int left = g.m - j * C::CT;
-#pragma unroll 1
-                for (int kv = 0; kv < 2; ++kv, ++n) {
-                    const int rs = (int)(n % NR), s = (int)(n % ST);
-                    if (!mbar_wait_bounded_soon(RFULL(rs), (uint32_t)((n / NR) & 1), C::SLEEP_NS) ||
-                        (n >= ST && !mbar_wait_bounded_soon(EMPTY(s), (uint32_t)(((n / ST) - 1) & 1), C::SLEEP_NS))) {
-                        dead = true;
-                        break;
+        g.twin = t.ntok <= p.tps && blk1 - blk0 > 1;
+        g.slot = slot;
+        mbar_arrive(cta.g_full(s));
+        ++sg;
+    };
+    for (int it = a.item; it < hd.n_items && !cta.dead; ++it) {
+        const bool last = it == e.item;
+        if (it > e.item || (last && e.off == 0))
+            break;
+        const ExtTile t = p.tiles[it / Hv];
+        const bool fresh = it > a.item || a.off == 0;
+        const int b0 = it > a.item ? 0 : a.blk, b1 = last ? e.blk : t.nblk;
+        if (t.nblk == 0 ? !fresh : b1 <= b0)
+            continue;
+        const bool whole = b0 == 0 && b1 == t.nblk;
+        push(it, t, b0, b1, whole ? -1 : b0 > 0 ? 2 * c + 1 : 2 * (c + 1));
+    }
+    for (int x = 0; x < hd.waves && !cta.dead; ++x) {
+        const int it = x * G + ((x & 1) ? G - 1 - c : c);
+        const ExtTile t = p.tiles[it / Hv];
+        push(it, t, 0, t.nblk, -1);
+    }
+    if (!cta.dead) {
+        const ExtTile none = {};
+        push(-1, none, 0, 0, -1);
+    }
+}
+
+// ---------------------------------------------------------------- K and V
+// Each lane one box of a block (row group, plane), so the rows of a block
+// may come from several pages.
+template <typename T, int D, bool F8>
+__device__ __forceinline__ void ext_load_kv(const ExtendParams &p, ExtCta<T, D, F8> &cta)
+{
+    using C = ExtCfg<T, D, F8>;
+    constexpr int NS = F8 ? C::RAWS : C::STAGES;
+    const int R = p.paged ? p.box_rows : C::CT;
+    const int ng = C::CT / R;   // row groups (at most 8)
+    const int grp = cta.lane % ng, plane = cta.lane / ng;
+    const bool mine = plane < (F8 ? 1 : C::PLANES);
+    int n = 0;                  // blocks issued
+    ExtSeg g;
+    while (cta.next(g)) {
+        const int nb = ext_blocks(g);
+        // where this lane's rows of a block are: row in its page (or of
+        // all), page and head (or head); x < 0: behind the sequence's keys
+        struct At {
+            int x, y;
+        };
+        auto page_of = [&](int i) {
+            const int tok = (g.blk0 + i) * C::CT + grp * R;
+            return (p.paged && mine && i < nb && tok < g.m)
+                       ? __ldg(p.table + (long long)g.b * p.max_pages + tok / p.page_size)
+                       : 0;
+        };
+        const ExtOrder order = {g.twin != 0, nb};
+        int page = page_of(0);   // the table is read a block ahead
+        int ki = 0;              // k: where K(ki) is, before: K(ki - 1)
+        At k = {-1, 0}, before = {-1, 0};
+        for (int t = 0; t < 2 * nb && !cta.dead; ++t) {
+            int i;
+            const bool isv = order.item(t, i);
+            if (!isv) {
+                before = k;
+                ki = i;
+                const int tok = (g.blk0 + i) * C::CT + grp * R;
+                k = {-1, 0};
+                if (mine && tok < g.m) {
+                    if (!p.paged) {
+                        k = {g.k0 + tok, g.h};
+                    } else {
+                        if (page < 0 || page >= p.num_pages) {
+                            atomicOr(p.status, STATUS_BAD_PAGE);
+                            page = 0;
+                        }
+                        k = {tok % p.page_size, page * p.Hkv + g.h};
                     }
-                    const uint32_t src = rawring + (uint32_t)(rs * C::RAW_BYTES);
-                    const uint32_t dst = ring + (uint32_t)(s * C::BLOCK_BYTES + (c >> 2) * C::PLANE);
+                }
+                page = page_of(i + 1);
+            }
+            const At at = i == ki ? k : before;
+            const uint32_t bytes =
+                (uint32_t)__popc(__ballot_sync(FULL_MASK, at.x >= 0)) * (uint32_t)(R * (F8 ? D : 128));
+            const int s = n % NS;
+            const uint32_t full = F8 ? cta.r_full(s) : cta.full(s);
+            if (n >= NS && !cta.wait(F8 ? cta.r_empty(s) : cta.empty(s), n / NS - 1))
+                break;
+            if (cta.lane == 0)
+                mbar_arrive_expect_tx(full, bytes);
+            __syncwarp();
+            const CUtensorMap *tm = isv ? &p.tmv : &p.tmk;
+            if (F8 && at.x >= 0)
+                tma_load_3d(cta.raw + (uint32_t)(s * C::RAW_BYTES + grp * R * D), tm, 0, at.x, at.y, full);
+            else if (at.x >= 0)
+                tma_load_4d(cta.ring + (uint32_t)(s * C::BLOCK_BYTES + plane * C::PLANE + grp * R * 128), tm, 0, at.x,
+                            at.y, plane, full);
+            ++n;
+        }
+    }
+    // no copy may be in flight when the CTA ends: the last fill of each stage
+    for (int i = n > NS ? n - NS : 0; i < n; ++i)
+        mbar_wait_bounded_soon(F8 ? cta.r_full(i % NS) : cta.full(i % NS), (uint32_t)((i / NS) & 1), C::SLEEP_NS);
+}
+
+// ---------------------------------------------------------------- Q
+// A sub-tile's rows: tps tokens of Gs heads each, plane by plane.  Rows
+// behind the sequence's are other sequences' (or zeros): they are computed
+// and not written out.
+template <typename T, int D, bool F8>
+__device__ __forceinline__ void ext_load_q(const ExtendParams &p, ExtCta<T, D, F8> &cta)
+{
+    using C = ExtCfg<T, D, F8>;
+    int n[2] = {0, 0};
+    ExtSeg g;
+    while (cta.next(g)) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            if (g.blk[x] <= g.blk0)
+                continue;
+            if (n[x] > 0 && !cta.wait(cta.q_empty(x), n[x] - 1))
+                break;
+            if (cta.lane == 0) {
+                mbar_arrive_expect_tx(cta.q_full(x), (uint32_t)(C::PLANES * p.tps * p.Gs * 128));
+                for (int pl = 0; pl < C::PLANES; ++pl)
+                    tma_load_4d(cta.qbuf + (uint32_t)(x * C::Q_BYTES + pl * C::PLANE), &p.tmq, 0,
+                                g.h * p.G + g.slice * p.Gs, g.row0 + x * p.tps, pl, cta.q_full(x));
+            }
+            ++n[x];
+        }
+    }
+    for (int x = 0; x < 2; ++x)
+        if (n[x] > 0)
+            mbar_wait_bounded_soon(cta.q_full(x), (uint32_t)((n[x] - 1) & 1), C::SLEEP_NS);
+}
+
+// ---------------------------------------------------------------- E4M3 to f16
+template <typename T, int D, bool F8>
+__device__ __forceinline__ void ext_widen(const ExtendParams &p, ExtCta<T, D, F8> &cta)
+{
+    using C = ExtCfg<T, D, F8>;
+    constexpr int NR = F8 ? C::RAWS : 1, ST = C::STAGES;
+    // A thread widens 16 values of a row at a time into the swizzled planes
+    // that the MMAs read.  Eight lanes read 128 bytes in a row; at d = 128
+    // the upper four write the other plane, their two halves in the other
+    // order, so that the eight 16-byte writes of a phase fall in different
+    // banks.
+    constexpr int CPR = D / 16;   // 16-value pieces of a row
+    // Two groups of four warps take the blocks by turns, and the Q of one
+    // sub-tile each.
+    const int group = ((int)threadIdx.x - C::CVT_WARP * 32) / 128, ct = (int)(threadIdx.x & 127);
+    const int c = ct % CPR, r0 = ct / CPR;
+    const bool swap = (c >> 2) != 0;
+    int n = 0, nq[2] = {0, 0};
+    ExtSeg g;
+    while (cta.next(g)) {
+        const int nb = ext_blocks(g);
+        // Q of the segment, a thread a row, in place
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            if (g.blk[x] <= g.blk0 || x != group)
+                continue;
+            if (!cta.wait(cta.q_full(x), nq[x]))
+                break;
+            int sh = 0;
+            if (p.dtype == 2) {
+                const uint32_t row = cta.qbuf + (uint32_t)(x * C::Q_BYTES + ct * 128);
+                uint32_t top = 0;   // the largest magnitude's bits
+#pragma unroll
+                for (int i = 0; i < C::PLANES * 8; ++i) {
+                    const uint4 u = lds128(row + (uint32_t)((i >> 3) * C::PLANE + (((i & 7) ^ (ct & 7)) << 4)));
+                    const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        top = max(top, max((v[e] << 16) & 0x7fff0000u, v[e] & 0x7fff0000u));
+                }
+                if (top)
+                    sh = min(max(8 + 127 - (int)(top >> 23), -120), 120);
+                const float f = __uint_as_float((uint32_t)(127 + sh) << 23);
+#pragma unroll
+                for (int i = 0; i < C::PLANES * 8; ++i) {
+                    const uint32_t a = row + (uint32_t)((i >> 3) * C::PLANE + (((i & 7) ^ (ct & 7)) << 4));
+                    float y[8];
+                    Elem<__nv_bfloat16>::widen(lds128(a), y);
+                    sts128(a, make_uint4(Mma<__half>::pack(y[0] * f, y[1] * f), Mma<__half>::pack(y[2] * f, y[3] * f),
+                                         Mma<__half>::pack(y[4] * f, y[5] * f), Mma<__half>::pack(y[6] * f, y[7] * f)));
+                }
+                fence_proxy_async_smem();
+            }
+            cta.qexp[((nq[x] & 1) * 2 + x) * C::M + ct] = (signed char)sh;
+            cta.arrive(cta.q_wide(x));
+            ++nq[x];
+        }
+        const ExtOrder order = {g.twin != 0, nb};
+        for (int t = 0; t < 2 * nb && !cta.dead; ++t, ++n) {
+            int i;
+            order.item(t, i);
+            if ((n & 1) != group)
+                continue;
+            const int left = g.m - (g.blk0 + i) * C::CT;
+            const int rs = n % NR, s = n % ST;
+            if (!cta.wait(cta.r_full(rs), n / NR) || (n >= ST && !cta.wait(cta.empty(s), n / ST - 1)))
+                break;
+            const uint32_t src = cta.raw + (uint32_t)(rs * C::RAW_BYTES);
+            const uint32_t dst = cta.ring + (uint32_t)(s * C::BLOCK_BYTES + (c >> 2) * C::PLANE);
 #pragma unroll 4
-                    for (int r = r0; r < C::CT; r += 128 / CPR) {
-                        uint4 v = lds128(src + (uint32_t)(r * D + c * 16));
-                        // rows behind the sequence's last key may hold
-                        // anything, and 0 * NaN is NaN
-                        if (r >= left)
-                            v = make_uint4(0, 0, 0, 0);
-                        uint4 lo, hi;
-                        e4m3_widen16<T>(v, lo, hi);
-                        const uint32_t a0 = dst + (uint32_t)(r * 128 + (((2 * (c & 3)) ^ (r & 7)) << 4));
-                        const uint32_t a1 = dst + (uint32_t)(r * 128 + (((2 * (c & 3) + 1) ^ (r & 7)) << 4));
-                        sts128(swap ? a1 : a0, swap ? hi : lo);
-                        sts128(swap ? a0 : a1, swap ? lo : hi);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(FULL(s));
-                        mbar_arrive(REMPTY(rs));
-                    }
-                }
+            for (int k = 0; k < C::CT * CPR / 128; ++k) {
+                const int r = r0 + k * (128 / CPR);
+                uint4 v = lds128(src + (uint32_t)(r * D + c * 16));
+                // rows behind the sequence's last key may hold anything, and
+                // 0 * NaN is NaN
+                if (r >= left)
+                    v = make_uint4(0, 0, 0, 0);
+                uint4 lo, hi;
+                e4m3_widen16(v, lo, hi);
+                const uint32_t a0 = dst + (uint32_t)(r * 128 + (((2 * (c & 3)) ^ (r & 7)) << 4));
+                const uint32_t a1 = dst + (uint32_t)(r * 128 + (((2 * (c & 3) + 1) ^ (r & 7)) << 4));
+                sts128(swap ? a1 : a0, swap ? hi : lo);
+                sts128(swap ? a0 : a1, swap ? lo : hi);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (cta.lane == 0) {
+                mbar_arrive(cta.full(s));
+                mbar_arrive(cta.r_empty(rs));
             }
         }
-    } else if (w == C::Q_WARP) {
-        // ------------------------------------------------------------ Q
-        // A sub-tile's rows: tps tokens of Gs heads each, plane by plane.
-        // Rows behind the sequence's are other sequences' (or zeros): they
-        // are computed and not written out.
-        int n[2] = {0, 0};
-        ExtSeg g;
-        while (!dead && next_seg(g)) {
-            if (lane == 0) {
-                for (int x = 0; x < 2 && !dead; ++x) {
-                    if (g.blk[x] <= g.blk0)
-                        continue;
-                    if (n[x] > 0 &&
-                        !mbar_wait_bounded_sleep_thread(QEMPTY(x), (uint32_t)((n[x] - 1) & 1), C::SLEEP_NS)) {
-                        dead = true;
-                        break;
-                    }
-                    mbar_arrive_expect_tx(QFULL(x), (uint32_t)(C::PLANES * p.tps * p.Gs * 128));
-                    for (int pl = 0; pl < C::PLANES; ++pl)
-                        tma_load_4d(qbuf + (uint32_t)(x * C::Q_BYTES + pl * C::PLANE), &p.tmq, 0,
-                                    g.h * p.G + g.slice * p.Gs, g.row0 + x * p.tps, pl, QFULL(x));
-                    ++n[x];
-                }
+    }
+}
+
+// ---------------------------------------------------------------- MMA issue
+// The whole warp runs it; the instructions are predicated on one lane.
+template <typename T, int D, bool F8>
+__device__ __forceinline__ void ext_mma(const ExtendParams &p, ExtCta<T, D, F8> &cta, uint32_t tmem)
+{
+    using C = ExtCfg<T, D, F8>;
+    constexpr int ST = C::STAGES;
+    constexpr int BF = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
+    constexpr uint32_t ID_S = idesc_f16(BF, 0, 0, C::M, C::CT);   // Q K-major, K K-major
+    constexpr uint32_t ID_O = idesc_f16(BF, 0, 1, C::M, D);       // P (TMEM) K-major, V MN-major
+    // Descriptors: a base, plus offsets in its units of 16 bytes (an address
+    // fits the field, so no carry leaves it).
+    const uint64_t qdesc = smem_desc_sw128(cta.qbuf, 16, 1024), kdesc = smem_desc_sw128(cta.ring, 16, 1024);
+    const uint64_t vdesc = smem_desc_sw128(cta.ring, (uint32_t)C::PLANE, 1024);
+    const uint32_t one = elect_one();
+    int np[2] = {0, 0};     // P taken from each engine
+    int nq[2] = {0, 0};     // Q of each sub-tile taken
+    // the ring is used in the order it is filled
+    struct Cursor {
+        int slot, phase;
+        __device__ __forceinline__ void step()
+        {
+            if (++slot == ST) {
+                slot = 0;
+                phase ^= 1;
             }
-            dead = __any_sync(FULL_MASK, dead);
         }
-        if (lane == 0) {
-            for (int x = 0; x < 2; ++x)
-                if (n[x] > 0)
-                    mbar_wait_bounded_sleep_thread(QFULL(x), (uint32_t)((n[x] - 1) & 1), C::SLEEP_NS);
-        }
-        __syncwarp();
-    } else if (w == C::MMA_WARP) {
-        // ------------------------------------------------------------ MMA issue
-        constexpr int BF = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
-        constexpr uint32_t ID_S = idesc_f16(BF, 0, 0, C::M, C::CT);   // Q K-major, K K-major
-        constexpr uint32_t ID_O = idesc_f16(BF, 0, 1, C::M, D);       // P (TMEM) K-major, V MN-major
-        long long n = 0;              // blocks taken from the ring
-        int ns[2] = {0, 0};           // P of each sub-tile taken
-        int nq[2] = {0, 0};           // Q of each sub-tile taken
-        auto wait = [&](uint32_t bar, int phase) {
-            if (!dead && !mbar_wait_bounded_soon(bar, (uint32_t)(phase & 1), C::SLEEP_NS))
-                dead = true;
-            return !dead;
-        };
-        // Descriptors: a base, plus offsets in its units of 16 bytes (an
-        // address fits the field, so no carry leaves it).
-        const uint64_t qdesc = smem_desc_sw128(qbuf, 16, 1024), kdesc = smem_desc_sw128(ring, 16, 1024);
-        const uint64_t vdesc = smem_desc_sw128(ring, (uint32_t)C::PLANE, 1024);
-        const uint32_t one = elect_one();
-        auto issue_s = [&](int x, int st) {
-            const uint64_t a = qdesc + (uint64_t)(x * (C::Q_BYTES >> 4)), b = kdesc + (uint64_t)(st * (C::BLOCK_BYTES >> 4));
+    } cur = {0, 0};
+    auto landed = [&](const Cursor &c) { return cta.wait(cta.full(c.slot), c.phase); };
+    // S of engine x, from Q of sub-tile q and K in stage st
+    auto issue_s = [&](int x, int q, int st) {
+        const uint64_t a = qdesc + (uint64_t)(q * (C::Q_BYTES >> 4)), b = kdesc + (uint64_t)(st * (C::BLOCK_BYTES >> 4));
+        tc_fence_after();
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-                // 16 elements = 32 bytes of each 128-byte row of plane ks / 4
-                const uint64_t o = (uint64_t)(((ks >> 2) * C::PLANE + (ks & 3) * 32) >> 4);
-                tc_mma_ss_if(one, tmem + (uint32_t)C::tm_s(x), a + o, b + o, ID_S, ks > 0 ? 1u : 0u);
-            }
-            tc_commit_if(one, SFULL(x));
-        };
-        // the keys of one half of P
-        auto issue_pv = [&](int x, int st, int half, bool first) {
-            const uint64_t b = vdesc + (uint64_t)(st * (C::BLOCK_BYTES >> 4));
+        for (int ks = 0; ks < D / 16; ++ks) {
+            // 16 elements = 32 bytes of each 128-byte row of plane ks / 4
+            const uint64_t o = (uint64_t)(((ks >> 2) * C::PLANE + (ks & 3) * 32) >> 4);
+            tc_mma_ss_if(one, tmem + (uint32_t)C::tm_s(x), a + o, b + o, ID_S, ks > 0 ? 1u : 0u);
+        }
+        tc_commit_if(one, cta.s_full(x));
+    };
+    // P.V of engine x, part by part as P arrives, V in stage st
+    auto issue_pv = [&](int x, int st, bool first) {
+        const uint64_t b = vdesc + (uint64_t)(st * (C::BLOCK_BYTES >> 4));
 #pragma unroll
-            for (int i = 0; i < C::CT / 32; ++i) {
-                const int ks = half * (C::CT / 32) + i;
+        for (int part = 0; part < 2; ++part) {
+            if (!cta.wait(cta.p_full(x, part), np[x]))
+                return;
+            tc_fence_after();
+#pragma unroll
+            for (int ks = part ? C::PART / 16 : 0; ks < (part ? C::CT : C::PART) / 16; ++ks)
                 tc_mma_ts_if(one, tmem + (uint32_t)C::tm_o(x), tmem + (uint32_t)(C::tm_p(x) + ks * 8),
                              b + (uint64_t)(ks * (2048 >> 4)), ID_O, (!first || ks > 0) ? 1u : 0u);
-            }
-        };
-        ExtSeg g;
-        while (!dead && next_seg(g)) {
-            const int end = ext_end(g);
-            if (end <= g.blk0)
-                continue;
-            // S of the first block
-            {
-                const int s = (int)(n % ST);
-                if (!wait(FULL(s), (int)((n / ST) & 1)))
-                    break;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (g.blk[x] <= g.blk0)
-                        continue;
-                    if (!wait(QFULL(x), nq[x]))
-                        break;
-                    ++nq[x];
-                    tc_fence_after();
-                    issue_s(x, s);
-                    if (g.blk[x] == g.blk0 + 1)
-                        tc_commit_if(one, QEMPTY(x));
-                }
-                if (dead)
-                    break;
-                tc_commit_if(one, EMPTY(s));
-                ++n;
-            }
-#pragma unroll 1
-            for (int j = g.blk0; j < end && !dead; ++j) {
-                const int vs = (int)(n % ST);
-                const int vph = (int)((n / ST) & 1);
-                ++n;
-                const int ks = (int)(n % ST);
-                const int kph = (int)((n / ST) & 1);
-                const bool more = j + 1 < end;
-                if (!wait(FULL(vs), vph))
-                    break;
-                const int left = g.m - j * C::CT;
-                if (!F8 && left < C::CT) {
-                    // V's rows behind the sequence's last key may hold
-                    // anything, and 0 * NaN is NaN: zeros instead
-                    const uint32_t vb = ring + (uint32_t)(vs * C::BLOCK_BYTES);
-                    for (int i = lane; i < (C::CT - left) * C::PLANES * 8; i += 32) {
-                        const int pl = i / ((C::CT - left) * 8), o = i % ((C::CT - left) * 8);
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                         vb + (uint32_t)(pl * C::PLANE + left * 128 + o * 16)),
-                                     "r"(0u)
-                                     : "memory");
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                bool kready = false;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (j < g.blk[x]) {
-                        if (!wait(PFULL(x, 0), ns[x]))
-                            break;
-                        tc_fence_after();
-                        issue_pv(x, vs, 0, j == g.blk0);
-                        if (!wait(PFULL(x, 1), ns[x]))
-                            break;
-                        ++ns[x];
-                        tc_fence_after();
-                        issue_pv(x, vs, 1, false);
-                        if (j + 1 == g.blk[x])
-                            tc_commit_if(one, OFULL(x));
-                    }
-                    if (x == 1)
-                        tc_commit_if(one, EMPTY(vs));
-                    if (j + 1 < g.blk[x]) {
-                        if (!kready && !wait(FULL(ks), kph))
-                            break;
-                        kready = true;
-                        tc_fence_after();
-                        issue_s(x, ks);
-                        if (j + 2 == g.blk[x])
-                            tc_commit_if(one, QEMPTY(x));
-                    }
-                }
-                if (dead)
-                    break;
-                if (more) {
-                    tc_commit_if(one, EMPTY(ks));
-                    ++n;
-                }
-            }
         }
-        // every MMA issued here has completed before TMEM is freed
-        __syncwarp();
-        tc_commit_if(one, FIN);
-        if (!mbar_wait_bounded_soon(FIN, 0, C::SLEEP_NS))
-            dead = true;
-    }
-    } else {
-        regs_inc<C::REGS_SOFTMAX>();
-        // ------------------------------------------------------------ softmax
-        const int x = w >> 2;              // sub-tile
-        const int row = tid & 127;         // its row = TMEM lane
-        const uint32_t tl = tmem + ((uint32_t)((w & 3) * 32) << 16);
-        const int rtok = row / p.Gs, rg = row % p.Gs;
-        const int tok = x * p.tps + rtok;  // token within the tile
-        int ns = 0, no = 0;
-        ExtSeg g;
-        while (!dead && next_seg(g)) {
-            const int gv = min(p.Gs, p.G - g.slice * p.Gs);
-            const bool live = rtok < p.tps && tok < g.ntok && rg < gv;
-            // keys this row sees; a row that is not written takes those of
-            // the last one, so that its warp masks no block for its sake
-            const int lim = p.causal ? min(g.m, g.lim + min(tok, g.ntok - 1)) : g.m;
-            float sc = p.scale_log2;
-            float vscale = 1.f;
-            if (F8) {
-                sc *= __ldg(p.k_scale + (long long)g.b * p.Hkv + g.h);
-                vscale = __ldg(p.v_scale + (long long)g.b * p.Hkv + g.h);
-            }
-            float mref = -INFINITY, l = 0.f;
-            const int end = g.blk[x];
-            // blocks below this one hide nothing from any row of the warp
-            const int whole = __reduce_min_sync(FULL_MASK, max(lim, 0)) / C::CT;
-#pragma unroll 1
-            for (int j = g.blk0; j < end; ++j) {
-                if (!mbar_wait_bounded_soon(SFULL(x), (uint32_t)(ns & 1), C::SLEEP_NS)) {
-                    dead = true;
-                    break;
-                }
-                ++ns;
-                tc_fence_after();
-                float s[4][32];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    tmem_ld32(tl + (uint32_t)(C::tm_s(x) + 32 * i), s[i]);
-                tmem_wait_ld();
-                float sx = sc;
-                if (F8 && !(sc > 0.f)) {   // a K scale that is not positive
-#pragma unroll
-                    for (int i = 0; i < 128; ++i)
-                        s[i >> 5][i & 31] *= sc;
-                    sx = 1.f;
-                }
-                if (j >= whole) {
-                    const int see = lim - j * C::CT;
-#pragma unroll
-                    for (int i = 0; i < 128; ++i)
-                        s[i >> 5][i & 31] = i < see ? s[i >> 5][i & 31] : -INFINITY;
-                }
-                // four chains of three-input maxima
-                float mx[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    mx[i] = fmaxf(s[i][0], s[i][1]);
-#pragma unroll
-                for (int e = 2; e < 32; e += 2)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        mx[i] = fmaxf(mx[i], fmaxf(s[i][e], s[i][e + 1]));
-                const float mc = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sx;
-                const bool grow = mc > mref + C::TAU;
-                float a = 1.f;
-                if (grow) {
-                    a = ex2(mref - mc);   // 0 on the row's first keys
-                    l *= a;
-                    mref = mc;
-                }
-                // the tcgen05 loads and stores are warp-wide, so the whole
-                // warp runs them when any of its rows grew (a = 1 for others)
-                if (j > g.blk0 && __any_sync(FULL_MASK, grow)) {
-#pragma unroll 1
-                    for (int q = 0; q < D / 16; ++q) {
-                        float o[16];
-                        tmem_ld16(tl + (uint32_t)(C::tm_o(x) + 16 * q), o);
-                        tmem_wait_ld();
-                        uint32_t u[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            u[e] = __float_as_uint(o[e] * a);
-                        tmem_st16u(tl + (uint32_t)(C::tm_o(x) + 16 * q), u);
-                    }
-                }
-                const float nm = mref == -INFINITY ? 0.f : C::SHIFT - mref;
-                const uint64_t sc2 = pack2(sx, sx), nm2 = pack2(nm, nm);
-                uint64_t ls[4] = {0, 0, 0, 0};   // pairs of zeros
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t ph[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float x0, x1;
-                        unpack2(fma2(pack2(s[i][2 * e], s[i][2 * e + 1]), sc2, nm2), x0, x1);
-                        const float p0 = ex2(x0), p1 = ex2(x1);
-                        ls[e & 3] = add2(ls[e & 3], pack2(p0, p1));
-                        ph[e] = Mma<T>::pack(p0, p1);
-                    }
-                    tmem_st16u(tl + (uint32_t)(C::tm_p(x) + 16 * i), ph);
-                    if (i & 1) {
-                        // half of P: its product with V may start
-                        tmem_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(PFULL(x, i >> 1));
-                    }
-                }
-                float la, lb;
-                unpack2(add2(add2(ls[0], ls[1]), add2(ls[2], ls[3])), la, lb);
-                l += la + lb;
-            }
-            if (dead)
+        ++np[x];
+    };
+    ExtSeg g;
+    while (cta.next(g)) {
+        const int nb = ext_blocks(g);
+        if (nb == 0)
+            continue;
+        const bool twin = g.twin != 0;
+        // engine x's blocks: its own sub-tile's, or every other one
+        const int len[2] = {twin ? nb : g.blk[0] - g.blk0, twin ? nb : g.blk[1] - g.blk0};
+        const int ahead = twin ? 2 : 1;   // S runs so many blocks ahead of P.V
+        auto has = [&](int x, int i) { return i < len[x] && (!twin || (i & 1) == x); };
+        // S of block i; Q is free behind the last
+        auto s_of = [&](int x, int i, int st) {
+            const int q = twin ? 0 : x;
+            issue_s(x, q, st);
+            if (i == len[x] - 1)
+                tc_commit_if(one, cta.q_empty(q));
+        };
+        for (int i = 0; i < ahead && !cta.dead; ++i) {
+            if (!landed(cur))
                 break;
-
-            // ---- the segment's result ----
-            const bool some = end > g.blk0;
-            if (some) {
-                if (!mbar_wait_bounded_soon(OFULL(x), (uint32_t)(no & 1), C::SLEEP_NS)) {
-                    dead = true;
-                    break;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                if (!has(x, i))
+                    continue;
+                const int q = twin ? 0 : x;
+                if (i == 0) {
+                    if (!cta.wait(F8 ? cta.q_wide(q) : cta.q_full(q), nq[q]))
+                        break;
+                    ++nq[q];
                 }
-                ++no;
-                tc_fence_after();
+                s_of(x, i, cur.slot);
             }
-            const bool any = !(l <= 0.f);   // NaN counts: it is the result then
-            const float inv = any ? vscale / l : 0.f;
-            const long long qrow = (long long)(g.row0 + tok) * p.Hq + g.h * p.G + g.slice * p.Gs + rg;
-            const long long prow = ((long long)g.slot * 2 + x) * C::M + row;
-            // an empty row is 0 whatever its accumulator holds
-#pragma unroll
-            for (int q = 0; q < D / 32; ++q) {
-                float o[32];
-                if (some) {
-                    tmem_ld32(tl + (uint32_t)(C::tm_o(x) + 32 * q), o);
-                    tmem_wait_ld();
+            if (!cta.dead)
+                tc_commit_if(one, cta.empty(cur.slot));
+            cur.step();
+        }
+        int i = 0;
+        // Both engines have this block and the two behind it: straight
+        // through.  A stage is given back as soon as its last MMA is issued
+        // (both at the end cost 5%: the ring is just deep enough).
+        const int plain = twin ? 0 : min(len[0], len[1]) - 2;
+#pragma unroll 1
+        for (; i < plain && !cta.dead; ++i) {
+            const Cursor vc = cur;
+            cur.step();
+            if (!landed(vc))
+                break;
+            issue_pv(0, vc.slot, i == 0);
+            if (!landed(cur))
+                break;
+            issue_s(0, 0, cur.slot);
+            issue_pv(1, vc.slot, i == 0);
+            tc_commit_if(one, cta.empty(vc.slot));
+            issue_s(1, 1, cur.slot);
+            tc_commit_if(one, cta.empty(cur.slot));
+            cur.step();
+        }
+#pragma unroll 1
+        for (; i < nb && !cta.dead; ++i) {
+            const int k = i + ahead;
+            const bool more = k < nb;
+            const Cursor vc = cur;
+            cur.step();
+            if (!landed(vc))
+                break;
+            const int left = g.m - (g.blk0 + i) * C::CT;
+            if (!F8 && left < C::CT) {
+                // V's rows behind the sequence's last key may hold anything,
+                // and 0 * NaN is NaN: zeros instead
+                const uint32_t vb = cta.ring + (uint32_t)(vc.slot * C::BLOCK_BYTES);
+                for (int e = cta.lane; e < (C::CT - left) * C::PLANES * 8; e += 32) {
+                    const int pl = e / ((C::CT - left) * 8), o = e % ((C::CT - left) * 8);
+                    sts128(vb + (uint32_t)(pl * C::PLANE + left * 128 + o * 16), make_uint4(0, 0, 0, 0));
                 }
-                if (!some || !any) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        o[e] = 0.f;
-                }
-                if (live && g.slot >= 0)
-                    store_out32(p.part_o, prow * D + 32 * q, 0, o, 1.f);
-                else if (live)
-                    store_out32(p.out, qrow * D + 32 * q, p.out_dtype, o, inv);
+                fence_proxy_async_smem();
                 __syncwarp();
             }
-            tc_fence_before();   // the next segment's P.V overwrites O behind this warp's next P
-            if (live) {
-                if (g.slot >= 0)
-                    p.part_ml[prow] = make_float2(any ? mref - C::SHIFT : -INFINITY, l);
-                else if (p.lse)
-                    p.lse[qrow] = any ? (mref - C::SHIFT + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            const int last = has(1, i) ? 1 : 0;   // the engine that is done with V last
+            bool kready = false;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                if (has(x, i)) {
+                    issue_pv(x, vc.slot, i < ahead);
+                    if (!has(x, k))
+                        tc_commit_if(one, cta.o_full(x));
+                    if (x == last)
+                        tc_commit_if(one, cta.empty(vc.slot));
+                }
+                if (has(x, k)) {
+                    if (!kready && !landed(cur))
+                        break;
+                    kready = true;
+                    s_of(x, k, cur.slot);
+                }
+            }
+            if (more) {
+                tc_commit_if(one, cta.empty(cur.slot));
+                cur.step();
             }
         }
     }
+    // every MMA issued here has completed before TMEM is freed
+    __syncwarp();
+    tc_commit_if(one, cta.fin());
+    if (!mbar_wait_bounded_soon(cta.fin(), 0, C::SLEEP_NS))
+        cta.dead = true;
+}
 
-    if (dead && lane == 0)
+// ---------------------------------------------------------------- softmax
+template <typename T, int D, bool F8>
+__device__ __forceinline__ void ext_softmax(const ExtendParams &p, ExtCta<T, D, F8> &cta, uint32_t tmem)
+{
+    using C = ExtCfg<T, D, F8>;
+    const int w = threadIdx.x >> 5;
+    const int x = w >> 2;                      // engine
+    const int row = (int)(threadIdx.x & 127);  // row of the sub-tile = TMEM lane
+    const uint32_t tl = tmem + ((uint32_t)((w & 3) * 32) << 16);
+    const int rtok = row / p.Gs, rg = row % p.Gs;
+    int ns = 0, no = 0, meets = 0;
+    int nq[2] = {0, 0};
+    ExtSeg g;
+    while (cta.next(g)) {
+        const bool twin = g.twin != 0;
+        const int sub = twin ? 0 : x;          // whose rows
+        const int tok = sub * p.tps + rtok;    // token within the tile
+        const int gv = min(p.Gs, p.G - g.slice * p.Gs);
+        const bool live = rtok < p.tps && tok < g.ntok && rg < gv;
+        // keys this row sees; a row that is not written takes those of the
+        // last one, so that its warp masks no block for its sake
+        const int lim = p.causal ? min(g.m, g.lim + min(tok, g.ntok - 1)) : g.m;
+        float sc = p.scale_log2;
+        float vscale = 1.f;
+        if (F8) {
+            sc *= __ldg(p.k_scale + (long long)g.b * p.Hkv + g.h);
+            vscale = __ldg(p.v_scale + (long long)g.b * p.Hkv + g.h);
+            // engine 1 may need either Q: it sees every phase of both, since
+            // a wait tells a phase only from the one before it
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                if (y > x || g.blk[y] <= g.blk0)
+                    continue;
+                if (!cta.wait(cta.q_wide(y), nq[y]))
+                    break;
+                if (y == sub) {
+                    const int sh = cta.qexp[((nq[y] & 1) * 2 + y) * C::M + row];
+                    sc *= __uint_as_float((uint32_t)(127 - sh) << 23);
+                }
+                ++nq[y];
+            }
+        }
+        float mref = -INFINITY, l = 0.f;
+        const int begin = g.blk0 + (twin ? x : 0), end = g.blk[sub], step = twin ? 2 : 1;
+        // blocks below this one hide nothing from any row of the warp
+        const int whole = __reduce_min_sync(FULL_MASK, max(lim, 0)) / C::CT;
+#pragma unroll 1
+        for (int j = begin; j < end; j += step) {
+            if (!cta.wait(cta.s_full(x), ns))
+                break;
+            ++ns;
+            tc_fence_after();
+            float s[4][32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                tmem_ld32(tl + (uint32_t)(C::tm_s(x) + 32 * i), s[i]);
+            tmem_wait_ld();
+            float sx = sc;
+            if (F8 && !(sc > 0.f)) {   // a K scale that is not positive
+#pragma unroll
+                for (int i = 0; i < 128; ++i)
+                    s[i >> 5][i & 31] *= sc;
+                sx = 1.f;
+            }
+            if (j >= whole) {
+                const int see = lim - j * C::CT;
+#pragma unroll
+                for (int i = 0; i < 128; ++i)
+                    s[i >> 5][i & 31] = i < see ? s[i >> 5][i & 31] : -INFINITY;
+            }
+            // four chains of three-input maxima
+            float mx[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                mx[i] = fmaxf(s[i][0], s[i][1]);
+#pragma unroll
+            for (int e = 2; e < 32; e += 2)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    mx[i] = fmaxf(mx[i], fmaxf(s[i][e], s[i][e + 1]));
+            const float mc = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sx;
+            const bool grow = mc > mref + C::TAU;
+            float a = 1.f;
+            if (grow) {
+                a = ex2(mref - mc);   // 0 on the row's first keys
+                l *= a;
+                mref = mc;
+            }
+            // the tcgen05 loads and stores are warp-wide, so the whole warp
+            // runs them when any of its rows grew (a = 1 for others)
+            if (j > begin && __any_sync(FULL_MASK, grow)) {
+#pragma unroll 1
+                for (int q = 0; q < D / 16; ++q) {
+                    float o[16];
+                    tmem_ld16(tl + (uint32_t)(C::tm_o(x) + 16 * q), o);
+                    tmem_wait_ld();
+                    uint32_t u[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        u[e] = __float_as_uint(o[e] * a);
+                    tmem_st16u(tl + (uint32_t)(C::tm_o(x) + 16 * q), u);
+                }
+            }
+            const float nm = mref == -INFINITY ? 0.f : C::SHIFT - mref;
+            const uint64_t sc2 = pack2(sx, sx), nm2 = pack2(nm, nm);
+            uint64_t ls[4] = {0, 0, 0, 0};   // pairs of zeros
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t ph[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float x0, x1;
+                    unpack2(fma2(pack2(s[i][2 * e], s[i][2 * e + 1]), sc2, nm2), x0, x1);
+                    const float p0 = ex2(x0), p1 = ex2(x1);
+                    ls[e & 3] = add2(ls[e & 3], pack2(p0, p1));
+                    ph[e] = Mma<T>::pack(p0, p1);
+                }
+                tmem_st16u(tl + (uint32_t)(C::tm_p(x) + 16 * i), ph);
+                if (i == C::PART / 32 - 1 || i == 3) {
+                    // a part of P: its product with V may start
+                    tmem_wait_st();
+                    tc_fence_before();
+                    cta.arrive(cta.p_full(x, i == 3));
+                }
+            }
+            float la, lb;
+            unpack2(add2(add2(ls[0], ls[1]), add2(ls[2], ls[3])), la, lb);
+            l += la + lb;
+        }
+        // ---- the segment's result ----
+        const bool some = end > begin;
+        if (some && !cta.dead && cta.wait(cta.o_full(x), no)) {
+            ++no;
+            tc_fence_after();
+        }
+        if (cta.dead)
+            break;
+        const long long qrow = (long long)(g.row0 + tok) * p.Hq + g.h * p.G + g.slice * p.Gs + rg;
+        const long long prow = ((long long)g.slot * 2 + sub) * C::M + row;
+        float M = mref, L = l;             // of the row; f[y]: the factor of engine y's O
+        float f[2] = {1.f, 1.f};
+        int c0 = 0, c1 = D;                // columns this engine writes
+        bool from[2] = {x == 0 && some, x == 1 && some};
+        if (twin) {
+            // both engines hold the same rows: they swap (reference, sum),
+            // and each joins and writes half of the columns
+            cta.xch[x * C::M + row] = make_float2(mref, l);
+            tc_fence_before();
+            cta.arrive(cta.meet());
+            if (!cta.wait(cta.meet(), meets++))
+                break;
+            tc_fence_after();
+            const float2 a0 = cta.xch[row], a1 = cta.xch[C::M + row];
+            M = fmaxf(a0.x, a1.x);
+            f[0] = a0.x == -INFINITY ? 0.f : ex2(a0.x - M);
+            f[1] = a1.x == -INFINITY ? 0.f : ex2(a1.x - M);
+            L = f[0] * a0.y + f[1] * a1.y;
+            c0 = x * (D / 2);
+            c1 = c0 + D / 2;
+            from[0] = from[1] = true;      // a twin segment has two blocks or more
+        }
+        const bool any = !(L <= 0.f);      // NaN counts: it is the result then
+        if (g.slot < 0) {
+            const float inv = any ? vscale / L : 0.f;
+            f[0] *= inv;
+            f[1] *= inv;
+        }
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) {
+            if (32 * q < c0 || 32 * q >= c1)
+                continue;
+            float o[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                o[e] = 0.f;
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                if (!from[y])
+                    continue;
+                float v[32];
+                tmem_ld32(tl + (uint32_t)(C::tm_o(y) + 32 * q), v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    o[e] = any ? fmaf(v[e], f[y], o[e]) : 0.f;   // an empty row is 0 whatever O holds
+            }
+            if (live && g.slot >= 0)
+                store_out32(p.part_o, prow * D + 32 * q, 0, o);
+            else if (live)
+                store_out32(p.out, qrow * D + 32 * q, p.out_dtype, o);
+            __syncwarp();
+        }
+        tc_fence_before();   // the next segment's P.V overwrites O behind this warp's next P
+        if (live && (!twin || x == 0)) {
+            if (g.slot >= 0)
+                p.part_ml[prow] = make_float2(any ? M - C::SHIFT : -INFINITY, L);
+            else if (p.lse)
+                p.lse[qrow] = any ? (M - C::SHIFT + log2f(L)) * 0.6931471805599453f : -INFINITY;
+        }
+        if (twin) {
+            // neither engine writes its next P before both have read both O
+            cta.arrive(cta.meet());
+            if (!cta.wait(cta.meet(), meets++))
+                break;
+        }
+    }
+}
+
+template <typename T, int D, bool F8>
+__global__ void __launch_bounds__(ExtCfg<T, D, F8>::THREADS, 1) extend_kernel(const __grid_constant__ ExtendParams p)
+{
+    using C = ExtCfg<T, D, F8>;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the merge waits for this grid's end
+    extern __shared__ __align__(1024) unsigned char smem[];           // the swizzle's atoms are 1024 bytes
+    const int w = threadIdx.x >> 5;
+    ExtCta<T, D, F8> cta;
+    cta.lane = threadIdx.x & 31;
+    cta.ring = smem_addr(smem);
+    cta.raw = cta.ring + C::STAGES * C::BLOCK_BYTES;
+    cta.qbuf = cta.raw + C::RAWS * C::RAW_BYTES;
+    unsigned char *rest = smem + (cta.qbuf + 2 * C::Q_BYTES - cta.ring);
+    cta.bar0 = smem_addr(rest);
+    rest += C::NBAR * 8;
+    cta.xch = reinterpret_cast<float2 *>(rest);
+    rest += C::XCH_BYTES;
+    cta.segs = reinterpret_cast<volatile ExtSeg *>(rest);
+    static_assert(sizeof(ExtSeg) == 56, "segment slots");
+    rest += C::SEGS * 56;
+    uint32_t *misc = reinterpret_cast<uint32_t *>(rest);
+    cta.qexp = reinterpret_cast<signed char *>(rest + 16);
+    if (threadIdx.x == 0) {
+        cta.init();
+        prefetch_tmap(&p.tmq);
+        prefetch_tmap(&p.tmk);
+        prefetch_tmap(&p.tmv);
+    }
+    if (w == C::MMA_WARP) {
+        tmem_alloc(smem_addr(misc), C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    fence_mbar_init();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = misc[0];
+
+    // a warpgroup changes its share of the registers as a whole
+    if (w < 8) {
+        regs_inc<C::REGS_SOFTMAX>();
+        ext_softmax<T, D, F8>(p, cta, tmem);
+    } else {
+        regs_dec<C::REGS_OTHER>();
+        if (w == C::SCHED_WARP) {
+            if (cta.lane == 0)
+                ext_schedule<T, D, F8>(p, cta);
+            __syncwarp();
+        } else if (w == C::KV_WARP) {
+            ext_load_kv<T, D, F8>(p, cta);
+        } else if (w == C::Q_WARP) {
+            ext_load_q<T, D, F8>(p, cta);
+        } else if (w == C::MMA_WARP) {
+            ext_mma<T, D, F8>(p, cta, tmem);
+        } else if (F8) {
+            ext_widen<T, D, F8>(p, cta);
+        }
+    }
+
+    if (cta.dead && cta.lane == 0)
         atomicOr(p.status, STATUS_TIMEOUT);
     tc_fence_before();
     __syncthreads();

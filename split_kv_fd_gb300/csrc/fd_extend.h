@@ -85,8 +85,7 @@ inline int ext_slots(int grid) { return 2 * (grid + 1); }
 cudaError_t launch_extend_plan(const ExtendParams &p, cudaStream_t s);
 cudaError_t launch_extend_bf16(const ExtendParams &p, cudaStream_t s);
 cudaError_t launch_extend_f16(const ExtendParams &p, cudaStream_t s);
-cudaError_t launch_extend_bf16_e4m3(const ExtendParams &p, cudaStream_t s);
-cudaError_t launch_extend_f16_e4m3(const ExtendParams &p, cudaStream_t s);
+cudaError_t launch_extend_e4m3(const ExtendParams &p, cudaStream_t s);
 cudaError_t launch_extend_merge(const ExtendParams &p, cudaStream_t s);
 
 }  // namespace fd

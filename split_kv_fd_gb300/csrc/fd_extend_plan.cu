@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(PT, 1) extend_plan_kernel(const ExtendParams p
 //     M = max m_i,  out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.
 // Every CTA reads the cuts, lists the split items and their rows, and takes
 // its share of all those rows.
-constexpr int MT = 128;         // threads
+constexpr int MT = 256;         // threads
 constexpr int MAX_CUTS = 1024;
 
 template <int D> __global__ void __launch_bounds__(MT) extend_merge_kernel(const ExtendParams p)

@@ -174,8 +174,9 @@ fd_status run_extend(ExtendParams &p, float scale, void *workspace, size_t works
         return FD_ERR_CUDA;
     cudaError_t e = launch_extend_plan(p, cs);
     if (e == cudaSuccess)
-        e = p.dtype == FD_BF16 ? (p.f8 ? launch_extend_bf16_e4m3(p, cs) : launch_extend_bf16(p, cs))
-                               : (p.f8 ? launch_extend_f16_e4m3(p, cs) : launch_extend_f16(p, cs));
+        e = p.f8                 ? launch_extend_e4m3(p, cs)
+            : p.dtype == FD_BF16 ? launch_extend_bf16(p, cs)
+                                 : launch_extend_f16(p, cs);
     if (e == cudaSuccess)
         e = launch_extend_merge(p, cs);
     return e == cudaSuccess ? FD_OK : FD_ERR_CUDA;
