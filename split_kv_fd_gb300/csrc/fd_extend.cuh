@@ -28,7 +28,7 @@
 // soon as the softmax had read this one, both engines fell into step on the
 // special-function units: 373 us against 325 for 8192 tokens of 32 heads.)
 //
-// Warp roles (384 threads, 640 for E4M3 K/V, one CTA per SM):
+// Warp roles (384 threads, 512 for E4M3 K/V, one CTA per SM):
 //  - warps 0-3, 4-7: softmax and results of engines 0 and 1;
 //  - warp 8: K and V by tensor-map TMA into one ring;
 //  - warp 9: allocates TMEM, issues every MMA, engine 0's and engine 1's by
@@ -37,7 +37,7 @@
 //    heads);
 //  - warp 10: Q by TMA, as soon as a sub-tile's last S is done;
 //  - warp 11: walks the CTA's share of the plan, segments into a small ring;
-//  - E4M3 only, warps 12-19: widen the blocks that warp 8 copied as they are
+//  - E4M3 only, warps 12-15: widen the blocks that warp 8 copied as they are
 //    to f16 (exact: E4M3 has 4 significant bits and exponents from -9 to 8)
 //    for the same products.  A bf16 Q becomes f16 too, each row brought to
 //    a maximum in [2^8, 2^9) by a power of two that its scores undo: exact
@@ -62,21 +62,19 @@ template <typename T, int D, bool F8> struct ExtCfg {
     static constexpr int BLOCK_BYTES = PLANES * PLANE;   // K or V of one block
     static constexpr int Q_BYTES = PLANES * PLANE;       // one sub-tile
     // 16-bit K and V: 160 KB of copies in flight.  E4M3: the copies land in
-    // a ring of raw blocks, and two 16-bit stages suffice.
-#ifndef FD_EXT_F8_STAGES
-#define FD_EXT_F8_STAGES 3
-#endif
-    static constexpr int STAGES = (F8 ? FD_EXT_F8_STAGES : 5) * (128 / D);
+    // a ring of raw blocks, as many bytes as the 16-bit stages leave (two
+    // or four 16-bit stages are slower at long or at few queries).
+    static constexpr int STAGES = (F8 ? 3 : 5) * (128 / D);
     static constexpr int RAW_BYTES = CT * D;             // an E4M3 block
-    static constexpr int RAWS = F8 ? 2 * (5 - FD_EXT_F8_STAGES) * (128 / D) : 0;
+    static constexpr int RAWS = F8 ? 4 * (128 / D) : 0;
     static constexpr int SEGS = 3;                       // segments the scheduler runs ahead
     static constexpr int KV_WARP = 8, MMA_WARP = 9, Q_WARP = 10, SCHED_WARP = 11, CVT_WARP = 12;
-    static constexpr int CVT_WARPS = 8;
-    static constexpr int THREADS = F8 ? 640 : 384;
+    static constexpr int CVT_WARPS = 4;
+    static constexpr int THREADS = F8 ? 384 + 32 * CVT_WARPS : 384;
     // registers a thread: the softmax warpgroups hold a row of S each; the
-    // shares add up to the launch's (168 x 384 and 96 x 640)
-    static constexpr int REGS_SOFTMAX = F8 ? 168 : 208, REGS_OTHER = F8 ? 48 : 88;
-    static_assert(2 * REGS_SOFTMAX + (THREADS / 128 - 2) * REGS_OTHER == (F8 ? 5 * 96 : 3 * 168), "register shares");
+    // shares fit the launch's (168 x 384 and 128 x 512)
+    static constexpr int REGS_SOFTMAX = F8 ? 184 : 208, REGS_OTHER = F8 ? 72 : 88;
+    static_assert(2 * REGS_SOFTMAX + (THREADS / 128 - 2) * REGS_OTHER <= (F8 ? 4 * 128 : 3 * 168), "register shares");
     // TMEM columns: S and O of both engines, P in the first half of its S
     static constexpr int TM_O = 2 * CT;
     __host__ __device__ static constexpr int tm_s(int x) { return x * CT; }
@@ -114,12 +112,13 @@ struct ExtSeg {
     int row0, ntok;      // the tile's first row of q and out, its tokens
     int h, slice, b;
     int m, lim, k0;
-    int blk0, blk[2];    // blocks [blk0, blk[x]) of sub-tile x
+    int blk0, end0, end1;   // blocks [blk0, end x) of sub-tile x
     int twin;            // one sub-tile, its blocks dealt to both engines
     int slot;            // partial result, or -1: the whole item
+    __device__ __forceinline__ int end(int x) const { return x ? end1 : end0; }
 };
 
-__device__ __forceinline__ int ext_blocks(const ExtSeg &g) { return max(g.blk[0], g.blk[1]) - g.blk0; }
+__device__ __forceinline__ int ext_blocks(const ExtSeg &g) { return max(g.end0, g.end1) - g.blk0; }
 
 // The order of a segment's n blocks in the ring: K(0), V(0), K(1), V(1), ...,
 // or with K one block ahead (S of the next block is wanted before P.V of
@@ -245,7 +244,7 @@ template <typename T, int D, bool F8> struct ExtCta {
     __device__ __forceinline__ void init()
     {
         for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(full(s), F8 ? 4 : 1);   // the producer's arrival plus the copy's bytes, or the widening warps
+            mbar_init(full(s), F8 ? C::CVT_WARPS : 1);   // the producer's arrival plus the copy's bytes, or the widening warps
             mbar_init(empty(s), 1);           // commit behind the block's last MMA
         }
         for (int x = 0; x < 2; ++x) {
@@ -255,7 +254,7 @@ template <typename T, int D, bool F8> struct ExtCta {
             mbar_init(o_full(x), 1);          // commit behind the segment's last P.V
             mbar_init(q_full(x), 1);
             mbar_init(q_empty(x), 1);         // commit behind the segment's last S
-            mbar_init(q_wide(x), 4);          // a group of the widening warps
+            mbar_init(q_wide(x), C::CVT_WARPS);   // the widening warps
         }
         mbar_init(meet(), 8);                 // the softmax warps of both engines
         mbar_init(fin(), 1);
@@ -265,7 +264,7 @@ template <typename T, int D, bool F8> struct ExtCta {
         }
         for (int s = 0; s < C::RAWS; ++s) {
             mbar_init(r_full(s), 1);
-            mbar_init(r_empty(s), 4);
+            mbar_init(r_empty(s), C::CVT_WARPS);
         }
     }
 
@@ -301,8 +300,8 @@ template <typename T, int D, bool F8> struct ExtCta {
         g.lim = x.lim;
         g.k0 = x.k0;
         g.blk0 = x.blk0;
-        g.blk[0] = x.blk[0];
-        g.blk[1] = x.blk[1];
+        g.end0 = x.end0;
+        g.end1 = x.end1;
         g.twin = x.twin;
         g.slot = x.slot;
         arrive(g_empty(s));
@@ -347,7 +346,7 @@ __device__ __forceinline__ void ext_schedule(const ExtendParams &p, ExtCta<T, D,
             const int n = min(t.ntok - x * p.tps, p.tps);   // the sub-tile's tokens
             const int see = n <= 0 ? 0 : p.causal ? min(t.m, t.lim + x * p.tps + n - 1) : t.m;
             const int end = see > 0 ? (see + C::CT - 1) / C::CT : 0;
-            g.blk[x] = max(blk0, min(blk1, end));
+            (x ? g.end1 : g.end0) = max(blk0, min(blk1, end));
         }
         g.twin = t.ntok <= p.tps && blk1 - blk0 > 1;
         g.slot = slot;
@@ -388,7 +387,8 @@ __device__ __forceinline__ void ext_load_kv(const ExtendParams &p, ExtCta<T, D, 
     const int R = p.paged ? p.box_rows : C::CT;
     const int ng = C::CT / R;   // row groups (at most 8)
     const int grp = cta.lane % ng, plane = cta.lane / ng;
-    const bool mine = plane < (F8 ? 1 : C::PLANES);
+    // (one box holds all planes where a block is one row group)
+    const bool mine = plane < (F8 || ng == 1 ? 1 : C::PLANES);
     int n = 0;                  // blocks issued
     ExtSeg g;
     while (cta.next(g)) {
@@ -431,7 +431,7 @@ __device__ __forceinline__ void ext_load_kv(const ExtendParams &p, ExtCta<T, D, 
             }
             const At at = i == ki ? k : before;
             const uint32_t bytes =
-                (uint32_t)__popc(__ballot_sync(FULL_MASK, at.x >= 0)) * (uint32_t)(R * (F8 ? D : 128));
+                (uint32_t)__popc(__ballot_sync(FULL_MASK, at.x >= 0)) * (uint32_t)(R * (F8 ? D : ng == 1 ? 128 * C::PLANES : 128));
             const int s = n % NS;
             const uint32_t full = F8 ? cta.r_full(s) : cta.full(s);
             if (n >= NS && !cta.wait(F8 ? cta.r_empty(s) : cta.empty(s), n / NS - 1))
@@ -466,7 +466,7 @@ __device__ __forceinline__ void ext_load_q(const ExtendParams &p, ExtCta<T, D, F
     while (cta.next(g)) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            if (g.blk[x] <= g.blk0)
+            if (g.end(x) <= g.blk0)
                 continue;
             if (n[x] > 0 && !cta.wait(cta.q_empty(x), n[x] - 1))
                 break;
@@ -491,16 +491,19 @@ __device__ __forceinline__ void ext_widen(const ExtendParams &p, ExtCta<T, D, F8
     using C = ExtCfg<T, D, F8>;
     constexpr int NR = F8 ? C::RAWS : 1, ST = C::STAGES;
     // A thread widens 16 values of a row at a time into the swizzled planes
-    // that the MMAs read.  Eight lanes read 128 bytes in a row; at d = 128
-    // the upper four write the other plane, their two halves in the other
-    // order, so that the eight 16-byte writes of a phase fall in different
-    // banks.
-    constexpr int CPR = D / 16;   // 16-value pieces of a row
-    // Two groups of four warps take the blocks by turns, and the Q of one
-    // sub-tile each.
-    const int group = ((int)threadIdx.x - C::CVT_WARP * 32) / 128, ct = (int)(threadIdx.x & 127);
-    const int c = ct % CPR, r0 = ct / CPR;
-    const bool swap = (c >> 2) != 0;
+    // that the MMAs read; the raw rows are swizzled too (by the copy: 128
+    // bytes at d = 128, 64 at d = 64).  Eight lanes take the same piece of
+    // eight rows in a row, which the swizzles put into eight different
+    // banks on both sides, and a thread's rows are a multiple of 8 apart, so
+    // its offsets are constants.
+    constexpr int CPR = D / 16;             // 16-value pieces of a row
+    constexpr int BATCH = C::CT * CPR / 128;
+    const int ct = (int)threadIdx.x - C::CVT_WARP * 32;
+    const int r8 = ct & 7, c = (ct >> 3) % CPR;
+    const int r0 = r8 + 8 * ((ct >> 3) / CPR);
+    const uint32_t src0 = (uint32_t)(r0 * D + ((D == 128 ? c ^ r8 : c ^ (r8 >> 1)) << 4));
+    const uint32_t dst0 = (uint32_t)((c >> 2) * C::PLANE + r0 * 128 + (((2 * (c & 3)) ^ r8) << 4));
+    const uint32_t dst1 = dst0 ^ 16u;
     int n = 0, nq[2] = {0, 0};
     ExtSeg g;
     while (cta.next(g)) {
@@ -508,7 +511,7 @@ __device__ __forceinline__ void ext_widen(const ExtendParams &p, ExtCta<T, D, F8
         // Q of the segment, a thread a row, in place
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            if (g.blk[x] <= g.blk0 || x != group)
+            if (g.end(x) <= g.blk0)
                 continue;
             if (!cta.wait(cta.q_full(x), nq[x]))
                 break;
@@ -545,28 +548,31 @@ __device__ __forceinline__ void ext_widen(const ExtendParams &p, ExtCta<T, D, F8
         for (int t = 0; t < 2 * nb && !cta.dead; ++t, ++n) {
             int i;
             order.item(t, i);
-            if ((n & 1) != group)
-                continue;
             const int left = g.m - (g.blk0 + i) * C::CT;
             const int rs = n % NR, s = n % ST;
             if (!cta.wait(cta.r_full(rs), n / NR) || (n >= ST && !cta.wait(cta.empty(s), n / ST - 1)))
                 break;
-            const uint32_t src = cta.raw + (uint32_t)(rs * C::RAW_BYTES);
-            const uint32_t dst = cta.ring + (uint32_t)(s * C::BLOCK_BYTES + (c >> 2) * C::PLANE);
-#pragma unroll 4
-            for (int k = 0; k < C::CT * CPR / 128; ++k) {
-                const int r = r0 + k * (128 / CPR);
-                uint4 v = lds128(src + (uint32_t)(r * D + c * 16));
+            const uint32_t src = cta.raw + (uint32_t)(rs * C::RAW_BYTES) + src0;
+            const uint32_t dst = cta.ring + (uint32_t)(s * C::BLOCK_BYTES);
+            constexpr int STEP = 128 / CPR;   // rows between a thread's pieces
+            uint4 v[BATCH];
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k)
+                v[k] = lds128(src + (uint32_t)(k * STEP * D));
+            if (left < C::CT) {
                 // rows behind the sequence's last key may hold anything, and
                 // 0 * NaN is NaN
-                if (r >= left)
-                    v = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k)
+                    if (r0 + k * STEP >= left)
+                        v[k] = make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
                 uint4 lo, hi;
-                e4m3_widen16(v, lo, hi);
-                const uint32_t a0 = dst + (uint32_t)(r * 128 + (((2 * (c & 3)) ^ (r & 7)) << 4));
-                const uint32_t a1 = dst + (uint32_t)(r * 128 + (((2 * (c & 3) + 1) ^ (r & 7)) << 4));
-                sts128(swap ? a1 : a0, swap ? hi : lo);
-                sts128(swap ? a0 : a1, swap ? lo : hi);
+                e4m3_widen16(v[k], lo, hi);
+                sts128(dst + dst0 + (uint32_t)(k * STEP * 128), lo);
+                sts128(dst + dst1 + (uint32_t)(k * STEP * 128), hi);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -593,8 +599,8 @@ __device__ __forceinline__ void ext_mma(const ExtendParams &p, ExtCta<T, D, F8> 
     const uint64_t qdesc = smem_desc_sw128(cta.qbuf, 16, 1024), kdesc = smem_desc_sw128(cta.ring, 16, 1024);
     const uint64_t vdesc = smem_desc_sw128(cta.ring, (uint32_t)C::PLANE, 1024);
     const uint32_t one = elect_one();
-    int np[2] = {0, 0};     // P taken from each engine
-    int nq[2] = {0, 0};     // Q of each sub-tile taken
+    int np0 = 0, np1 = 0;   // P taken from each engine
+    int nq0 = 0, nq1 = 0;   // Q of each sub-tile taken
     // the ring is used in the order it is filled
     struct Cursor {
         int slot, phase;
@@ -620,11 +626,11 @@ __device__ __forceinline__ void ext_mma(const ExtendParams &p, ExtCta<T, D, F8> 
         tc_commit_if(one, cta.s_full(x));
     };
     // P.V of engine x, part by part as P arrives, V in stage st
-    auto issue_pv = [&](int x, int st, bool first) {
+    auto issue_pv = [&](int x, int st, bool first, int &np) {
         const uint64_t b = vdesc + (uint64_t)(st * (C::BLOCK_BYTES >> 4));
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
-            if (!cta.wait(cta.p_full(x, part), np[x]))
+            if (!cta.wait(cta.p_full(x, part), np))
                 return;
             tc_fence_after();
 #pragma unroll
@@ -632,7 +638,7 @@ __device__ __forceinline__ void ext_mma(const ExtendParams &p, ExtCta<T, D, F8> 
                 tc_mma_ts_if(one, tmem + (uint32_t)C::tm_o(x), tmem + (uint32_t)(C::tm_p(x) + ks * 8),
                              b + (uint64_t)(ks * (2048 >> 4)), ID_O, (!first || ks > 0) ? 1u : 0u);
         }
-        ++np[x];
+        ++np;
     };
     ExtSeg g;
     while (cta.next(g)) {
@@ -641,95 +647,110 @@ __device__ __forceinline__ void ext_mma(const ExtendParams &p, ExtCta<T, D, F8> 
             continue;
         const bool twin = g.twin != 0;
         // engine x's blocks: its own sub-tile's, or every other one
-        const int len[2] = {twin ? nb : g.blk[0] - g.blk0, twin ? nb : g.blk[1] - g.blk0};
         const int ahead = twin ? 2 : 1;   // S runs so many blocks ahead of P.V
-        auto has = [&](int x, int i) { return i < len[x] && (!twin || (i & 1) == x); };
-        // S of block i; Q is free behind the last
-        auto s_of = [&](int x, int i, int st) {
-            const int q = twin ? 0 : x;
-            issue_s(x, q, st);
-            if (i == len[x] - 1)
-                tc_commit_if(one, cta.q_empty(q));
-        };
-        for (int i = 0; i < ahead && !cta.dead; ++i) {
-            if (!landed(cur))
-                break;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                if (!has(x, i))
-                    continue;
-                const int q = twin ? 0 : x;
-                if (i == 0) {
-                    if (!cta.wait(F8 ? cta.q_wide(q) : cta.q_full(q), nq[q]))
-                        break;
-                    ++nq[q];
-                }
-                s_of(x, i, cur.slot);
-            }
-            if (!cta.dead)
-                tc_commit_if(one, cta.empty(cur.slot));
-            cur.step();
-        }
-        int i = 0;
+        const int len0 = twin ? nb : g.end0 - g.blk0, len1 = twin ? nb : g.end1 - g.blk0;
+        auto has = [&](int x, int i) { return i >= 0 && i < (x ? len1 : len0) && (!twin || (i & 1) == x); };
         // Both engines have this block and the two behind it: straight
         // through.  A stage is given back as soon as its last MMA is issued
-        // (both at the end cost 5%: the ring is just deep enough).
-        const int plain = twin ? 0 : min(len[0], len[1]) - 2;
+        // (both at the end cost 5%: the ring is just deep enough).  The
+        // general loop below has one copy of each product for the rest: code
+        // that runs once a call comes from L2 line by line.
+        const int plain = twin ? 0 : min(len0, len1) - 2;
 #pragma unroll 1
-        for (; i < plain && !cta.dead; ++i) {
-            const Cursor vc = cur;
-            cur.step();
-            if (!landed(vc))
-                break;
-            issue_pv(0, vc.slot, i == 0);
-            if (!landed(cur))
-                break;
-            issue_s(0, 0, cur.slot);
-            issue_pv(1, vc.slot, i == 0);
-            tc_commit_if(one, cta.empty(vc.slot));
-            issue_s(1, 1, cur.slot);
-            tc_commit_if(one, cta.empty(cur.slot));
-            cur.step();
-        }
+        for (int i = -ahead; i < nb && !cta.dead; ++i) {
+            if (i == 0 && plain > 1) {
 #pragma unroll 1
-        for (; i < nb && !cta.dead; ++i) {
+                for (; i < plain && !cta.dead; ++i) {
+                    const Cursor vc = cur;
+                    cur.step();
+                    if (!landed(vc))
+                        break;
+                    issue_pv(0, vc.slot, i == 0, np0);
+                    if (!landed(cur))
+                        break;
+                    issue_s(0, 0, cur.slot);
+                    issue_pv(1, vc.slot, i == 0, np1);
+                    tc_commit_if(one, cta.empty(vc.slot));
+                    issue_s(1, 1, cur.slot);
+                    tc_commit_if(one, cta.empty(cur.slot));
+                    cur.step();
+                }
+                if (cta.dead)
+                    break;
+            }
+            if (i == 0 && twin) {
+                // the engines' blocks by turns, all but the last two
+#pragma unroll 1
+                for (; i + 2 < nb; ++i) {
+                    const int x = i & 1;
+                    const Cursor vc = cur;
+                    cur.step();
+                    if (!landed(vc))
+                        break;
+                    int np = x ? np1 : np0;
+                    issue_pv(x, vc.slot, i < 2, np);
+                    (x ? np1 : np0) = np;
+                    tc_commit_if(one, cta.empty(vc.slot));
+                    if (!landed(cur))
+                        break;
+                    issue_s(x, 0, cur.slot);
+                    tc_commit_if(one, cta.empty(cur.slot));
+                    if (i + 3 == nb)
+                        tc_commit_if(one, cta.q_empty(0));
+                    cur.step();
+                }
+                if (cta.dead)
+                    break;
+            }
             const int k = i + ahead;
             const bool more = k < nb;
-            const Cursor vc = cur;
-            cur.step();
-            if (!landed(vc))
-                break;
-            const int left = g.m - (g.blk0 + i) * C::CT;
-            if (!F8 && left < C::CT) {
-                // V's rows behind the sequence's last key may hold anything,
-                // and 0 * NaN is NaN: zeros instead
-                const uint32_t vb = cta.ring + (uint32_t)(vc.slot * C::BLOCK_BYTES);
-                for (int e = cta.lane; e < (C::CT - left) * C::PLANES * 8; e += 32) {
-                    const int pl = e / ((C::CT - left) * 8), o = e % ((C::CT - left) * 8);
-                    sts128(vb + (uint32_t)(pl * C::PLANE + left * 128 + o * 16), make_uint4(0, 0, 0, 0));
+            Cursor vc = cur;
+            if (i >= 0) {
+                cur.step();
+                if (!landed(vc))
+                    break;
+                const int left = g.m - (g.blk0 + i) * C::CT;
+                if (!F8 && left < C::CT) {
+                    // V's rows behind the sequence's last key may hold
+                    // anything, and 0 * NaN is NaN: zeros instead
+                    const uint32_t vb = cta.ring + (uint32_t)(vc.slot * C::BLOCK_BYTES);
+                    for (int e = cta.lane; e < (C::CT - left) * C::PLANES * 8; e += 32) {
+                        const int pl = e / ((C::CT - left) * 8), o = e % ((C::CT - left) * 8);
+                        sts128(vb + (uint32_t)(pl * C::PLANE + left * 128 + o * 16), make_uint4(0, 0, 0, 0));
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
             }
             const int last = has(1, i) ? 1 : 0;   // the engine that is done with V last
             bool kready = false;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
+#pragma unroll 1
+            for (int x = 0; x < 2 && !cta.dead; ++x) {
                 if (has(x, i)) {
-                    issue_pv(x, vc.slot, i < ahead);
+                    int np = x ? np1 : np0;
+                    issue_pv(x, vc.slot, i < ahead, np);
+                    (x ? np1 : np0) = np;
                     if (!has(x, k))
                         tc_commit_if(one, cta.o_full(x));
                     if (x == last)
                         tc_commit_if(one, cta.empty(vc.slot));
                 }
                 if (has(x, k)) {
+                    const int q = twin ? 0 : x;
+                    if (k == 0) {
+                        int nq = q ? nq1 : nq0;
+                        cta.wait(F8 ? cta.q_wide(q) : cta.q_full(q), nq);
+                        (q ? nq1 : nq0) = nq + 1;
+                    }
                     if (!kready && !landed(cur))
                         break;
                     kready = true;
-                    s_of(x, k, cur.slot);
+                    issue_s(x, q, cur.slot);
+                    if (k == (x && !twin ? len1 : len0) - 1)
+                        tc_commit_if(one, cta.q_empty(q));   // the last S that reads this Q
                 }
             }
-            if (more) {
+            if (more && !cta.dead) {
                 tc_commit_if(one, cta.empty(cur.slot));
                 cur.step();
             }
@@ -773,7 +794,7 @@ __device__ __forceinline__ void ext_softmax(const ExtendParams &p, ExtCta<T, D, 
             // a wait tells a phase only from the one before it
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-                if (y > x || g.blk[y] <= g.blk0)
+                if (y > x || g.end(y) <= g.blk0)
                     continue;
                 if (!cta.wait(cta.q_wide(y), nq[y]))
                     break;
@@ -785,7 +806,7 @@ __device__ __forceinline__ void ext_softmax(const ExtendParams &p, ExtCta<T, D, 
             }
         }
         float mref = -INFINITY, l = 0.f;
-        const int begin = g.blk0 + (twin ? x : 0), end = g.blk[sub], step = twin ? 2 : 1;
+        const int begin = g.blk0 + (twin ? x : 0), end = g.end(sub), step = twin ? 2 : 1;
         // blocks below this one hide nothing from any row of the warp
         const int whole = __reduce_min_sync(FULL_MASK, max(lim, 0)) / C::CT;
 #pragma unroll 1
@@ -881,10 +902,10 @@ __device__ __forceinline__ void ext_softmax(const ExtendParams &p, ExtCta<T, D, 
             break;
         const long long qrow = (long long)(g.row0 + tok) * p.Hq + g.h * p.G + g.slice * p.Gs + rg;
         const long long prow = ((long long)g.slot * 2 + sub) * C::M + row;
-        float M = mref, L = l;             // of the row; f[y]: the factor of engine y's O
-        float f[2] = {1.f, 1.f};
+        float M = mref, L = l;             // of the row; f0, f1: the factors of both O
+        float f0 = 1.f, f1 = 0.f;
+        int ta = C::tm_o(x), tb = ta;      // columns of this engine's O, and of a second one to add
         int c0 = 0, c1 = D;                // columns this engine writes
-        bool from[2] = {x == 0 && some, x == 1 && some};
         if (twin) {
             // both engines hold the same rows: they swap (reference, sum),
             // and each joins and writes half of the columns
@@ -896,42 +917,48 @@ __device__ __forceinline__ void ext_softmax(const ExtendParams &p, ExtCta<T, D, 
             tc_fence_after();
             const float2 a0 = cta.xch[row], a1 = cta.xch[C::M + row];
             M = fmaxf(a0.x, a1.x);
-            f[0] = a0.x == -INFINITY ? 0.f : ex2(a0.x - M);
-            f[1] = a1.x == -INFINITY ? 0.f : ex2(a1.x - M);
-            L = f[0] * a0.y + f[1] * a1.y;
+            f0 = a0.x == -INFINITY ? 0.f : ex2(a0.x - M);
+            f1 = a1.x == -INFINITY ? 0.f : ex2(a1.x - M);
+            L = f0 * a0.y + f1 * a1.y;
             c0 = x * (D / 2);
             c1 = c0 + D / 2;
-            from[0] = from[1] = true;      // a twin segment has two blocks or more
+            ta = C::tm_o(0);
+            tb = C::tm_o(1);
         }
         const bool any = !(L <= 0.f);      // NaN counts: it is the result then
         if (g.slot < 0) {
             const float inv = any ? vscale / L : 0.f;
-            f[0] *= inv;
-            f[1] *= inv;
+            f0 *= inv;
+            f1 *= inv;
         }
-#pragma unroll
-        for (int q = 0; q < D / 32; ++q) {
-            if (32 * q < c0 || 32 * q >= c1)
-                continue;
+        void *dst = g.slot >= 0 ? (void *)p.part_o : p.out;
+        const long long at = (g.slot >= 0 ? prow : qrow) * D;
+        const int kind = g.slot >= 0 ? 0 : p.out_dtype;
+#pragma unroll 1
+        for (int c = c0; c < c1; c += 32) {
             float o[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-                o[e] = 0.f;
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                if (!from[y])
-                    continue;
-                float v[32];
-                tmem_ld32(tl + (uint32_t)(C::tm_o(y) + 32 * q), v);
+            if (some || twin) {
+                tmem_ld32(tl + (uint32_t)(ta + c), o);
                 tmem_wait_ld();
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
-                    o[e] = any ? fmaf(v[e], f[y], o[e]) : 0.f;   // an empty row is 0 whatever O holds
+                    o[e] *= f0;
             }
-            if (live && g.slot >= 0)
-                store_out32(p.part_o, prow * D + 32 * q, 0, o);
-            else if (live)
-                store_out32(p.out, qrow * D + 32 * q, p.out_dtype, o);
+            if (twin) {
+                float v[32];
+                tmem_ld32(tl + (uint32_t)(tb + c), v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    o[e] = fmaf(v[e], f1, o[e]);
+            }
+            if (!any) {   // an empty row is 0 whatever O holds
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    o[e] = 0.f;
+            }
+            if (live)
+                store_out32(dst, at + c, kind, o);
             __syncwarp();
         }
         tc_fence_before();   // the next segment's P.V overwrites O behind this warp's next P

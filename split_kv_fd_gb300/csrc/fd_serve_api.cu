@@ -46,16 +46,16 @@ fd_status check_extend_pointers(const ExtendParams &p)
 }
 
 // A map of 16-bit elements [64, n1, n2, d/64 planes] with boxes [64, box1,
-// box2, 1] and the 128-byte swizzle; strides in bytes.
+// box2, planes] and the 128-byte swizzle; strides in bytes.
 bool map_16bit(CUtensorMap *m, const void *base, int dtype, int d, long long n1, long long s1, long long n2,
-               long long s2, int box1, int box2)
+               long long s2, int box1, int box2, int planes)
 {
     EncodeTiledFn fn = encode_tiled();
     if (!fn)
         return false;
     const cuuint64_t dims[4] = {64, (cuuint64_t)n1, (cuuint64_t)n2, (cuuint64_t)(d / 64)};
     const cuuint64_t strides[3] = {(cuuint64_t)s1, (cuuint64_t)s2, 128};
-    const cuuint32_t box[4] = {64, (cuuint32_t)box1, (cuuint32_t)box2, 1};
+    const cuuint32_t box[4] = {64, (cuuint32_t)box1, (cuuint32_t)box2, (cuuint32_t)planes};
     const cuuint32_t es[4] = {1, 1, 1, 1};
     return fn(m, dtype == FD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
               const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -63,7 +63,8 @@ bool map_16bit(CUtensorMap *m, const void *base, int dtype, int d, long long n1,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A map of bytes [d, n1, n2] with boxes [d, box1, 1]: E4M3 blocks as they are.
+// A map of bytes [d, n1, n2] with boxes [d, box1, 1]: E4M3 blocks as they
+// are, rows swizzled over their own length.
 bool map_8bit(CUtensorMap *m, const void *base, int d, long long n1, long long n2, int box1)
 {
     EncodeTiledFn fn = encode_tiled();
@@ -74,7 +75,8 @@ bool map_8bit(CUtensorMap *m, const void *base, int d, long long n1, long long n
     const cuuint32_t box[3] = {(cuuint32_t)d, (cuuint32_t)box1, 1};
     const cuuint32_t es[3] = {1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -151,7 +153,7 @@ fd_status run_extend(ExtendParams &p, float scale, void *workspace, size_t works
     p.part_o = reinterpret_cast<float *>(ws + l.part_o);
 
     const long long row = (long long)p.d * 2;
-    bool ok = map_16bit(&p.tmq, p.q, p.dtype, p.d, p.Hq, row, p.total_q, p.q_stride * 2, p.Gs, p.tps);
+    bool ok = map_16bit(&p.tmq, p.q, p.dtype, p.d, p.Hq, row, p.total_q, p.q_stride * 2, p.Gs, p.tps, 1);
     if (p.paged) {
         p.box_rows = EXT_MIN_PAGE;   // the largest power of two up to a block that divides the page
         while (p.box_rows < EXT_CT && p.page_size % (2 * p.box_rows) == 0)
@@ -163,9 +165,9 @@ fd_status run_extend(ExtendParams &p, float scale, void *workspace, size_t works
             const void *x = i ? p.v : p.k;
             ok = ok && (p.f8      ? map_8bit(m, x, p.d, p.page_size, p.num_pages * p.Hkv, p.box_rows)
                         : p.paged ? map_16bit(m, x, p.dtype, p.d, p.page_size, row, p.num_pages * p.Hkv,
-                                              row * p.page_size, p.box_rows, 1)
+                                              row * p.page_size, p.box_rows, 1, p.box_rows == EXT_CT ? p.d / 64 : 1)
                                   : map_16bit(m, x, p.dtype, p.d, p.total_k, (i ? p.v_stride : p.k_stride) * 2,
-                                              p.Hkv, row, EXT_CT, 1));
+                                              p.Hkv, row, EXT_CT, 1, p.d / 64));
         }
     } else {
         p.tmk = p.tmv = p.tmq;   // no key anywhere: never used
