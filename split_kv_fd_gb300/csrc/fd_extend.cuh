@@ -389,68 +389,81 @@ __device__ __forceinline__ void ext_load_kv(const ExtendParams &p, ExtCta<T, D, 
     const int grp = cta.lane % ng, plane = cta.lane / ng;
     // (one box holds all planes where a block is one row group)
     const bool mine = plane < (F8 || ng == 1 ? 1 : C::PLANES);
-    int n = 0;                  // blocks issued
+    const uint32_t box = (uint32_t)(R * (F8 ? D : ng == 1 ? 128 * C::PLANES : 128));
+    const uint32_t at = (uint32_t)(F8 ? grp * R * D : plane * C::PLANE + grp * R * 128);   // in the stage
+    // a block's rows, in pages and rows of a page (no division in the loop:
+    // this warp's time an item bounds how fast a cache can stream)
+    const int ps = p.paged ? p.page_size : 1;
+    const int pstep = C::CT / ps, rstep = C::CT % ps;
+    int slot = 0, lap = 0;      // the ring: next stage, times round
     ExtSeg g;
     while (cta.next(g)) {
         const int nb = ext_blocks(g);
-        // where this lane's rows of a block are: row in its page (or of
-        // all), page and head (or head); x < 0: behind the sequence's keys
-        struct At {
-            int x, y;
-        };
-        auto page_of = [&](int i) {
-            const int tok = (g.blk0 + i) * C::CT + grp * R;
-            return (p.paged && mine && i < nb && tok < g.m)
-                       ? __ldg(p.table + (long long)g.b * p.max_pages + tok / p.page_size)
-                       : 0;
-        };
         const ExtOrder order = {g.twin != 0, nb};
-        int page = page_of(0);   // the table is read a block ahead
-        int ki = 0;              // k: where K(ki) is, before: K(ki - 1)
-        At k = {-1, 0}, before = {-1, 0};
+        int tok = g.blk0 * C::CT + grp * R;   // this lane's first row of the next K
+        int pidx = tok / ps, row = tok % ps;
+        const int32_t *table = p.table + (long long)g.b * p.max_pages;
+        auto page_at = [&]() { return (p.paged && mine && tok < g.m) ? __ldg(table + pidx) : 0; };
+        int page = page_at();   // read a block ahead
+        // where this lane's rows of K(ki) and of K(ki - 1) are: row in the
+        // page (or of all), page and head (or head); x < 0: behind the
+        // sequence's keys
+        int ki = 0, kx = -1, ky = 0, bx = -1, by = 0;
         for (int t = 0; t < 2 * nb && !cta.dead; ++t) {
             int i;
             const bool isv = order.item(t, i);
             if (!isv) {
-                before = k;
+                bx = kx;
+                by = ky;
                 ki = i;
-                const int tok = (g.blk0 + i) * C::CT + grp * R;
-                k = {-1, 0};
+                kx = -1;
                 if (mine && tok < g.m) {
                     if (!p.paged) {
-                        k = {g.k0 + tok, g.h};
+                        kx = g.k0 + tok;
+                        ky = g.h;
                     } else {
                         if (page < 0 || page >= p.num_pages) {
                             atomicOr(p.status, STATUS_BAD_PAGE);
                             page = 0;
                         }
-                        k = {tok % p.page_size, page * p.Hkv + g.h};
+                        kx = row;
+                        ky = page * p.Hkv + g.h;
                     }
                 }
-                page = page_of(i + 1);
+                tok += C::CT;
+                pidx += pstep;
+                row += rstep;
+                if (row >= ps) {
+                    row -= ps;
+                    ++pidx;
+                }
+                page = i + 1 < nb ? page_at() : 0;
             }
-            const At at = i == ki ? k : before;
-            const uint32_t bytes =
-                (uint32_t)__popc(__ballot_sync(FULL_MASK, at.x >= 0)) * (uint32_t)(R * (F8 ? D : ng == 1 ? 128 * C::PLANES : 128));
-            const int s = n % NS;
-            const uint32_t full = F8 ? cta.r_full(s) : cta.full(s);
-            if (n >= NS && !cta.wait(F8 ? cta.r_empty(s) : cta.empty(s), n / NS - 1))
+            const int x = i == ki ? kx : bx, y = i == ki ? ky : by;
+            const uint32_t bytes = (uint32_t)__popc(__ballot_sync(FULL_MASK, x >= 0)) * box;
+            const uint32_t full = F8 ? cta.r_full(slot) : cta.full(slot);
+            if (lap > 0 && !cta.wait(F8 ? cta.r_empty(slot) : cta.empty(slot), lap - 1))
                 break;
             if (cta.lane == 0)
                 mbar_arrive_expect_tx(full, bytes);
             __syncwarp();
             const CUtensorMap *tm = isv ? &p.tmv : &p.tmk;
-            if (F8 && at.x >= 0)
-                tma_load_3d(cta.raw + (uint32_t)(s * C::RAW_BYTES + grp * R * D), tm, 0, at.x, at.y, full);
-            else if (at.x >= 0)
-                tma_load_4d(cta.ring + (uint32_t)(s * C::BLOCK_BYTES + plane * C::PLANE + grp * R * 128), tm, 0, at.x,
-                            at.y, plane, full);
-            ++n;
+            if (F8 && x >= 0)
+                tma_load_3d(cta.raw + (uint32_t)(slot * C::RAW_BYTES) + at, tm, 0, x, y, full);
+            else if (x >= 0)
+                tma_load_4d(cta.ring + (uint32_t)(slot * C::BLOCK_BYTES) + at, tm, 0, x, y, plane, full);
+            if (++slot == NS) {
+                slot = 0;
+                ++lap;
+            }
         }
     }
     // no copy may be in flight when the CTA ends: the last fill of each stage
-    for (int i = n > NS ? n - NS : 0; i < n; ++i)
-        mbar_wait_bounded_soon(F8 ? cta.r_full(i % NS) : cta.full(i % NS), (uint32_t)((i / NS) & 1), C::SLEEP_NS);
+    for (int i = 0; i < NS; ++i) {
+        const int n = i < slot ? lap : lap - 1;   // its last lap
+        if (n >= 0)
+            mbar_wait_bounded_soon(F8 ? cta.r_full(i) : cta.full(i), (uint32_t)(n & 1), C::SLEEP_NS);
+    }
 }
 
 // ---------------------------------------------------------------- Q
@@ -504,7 +517,8 @@ __device__ __forceinline__ void ext_widen(const ExtendParams &p, ExtCta<T, D, F8
     const uint32_t src0 = (uint32_t)(r0 * D + ((D == 128 ? c ^ r8 : c ^ (r8 >> 1)) << 4));
     const uint32_t dst0 = (uint32_t)((c >> 2) * C::PLANE + r0 * 128 + (((2 * (c & 3)) ^ r8) << 4));
     const uint32_t dst1 = dst0 ^ 16u;
-    int n = 0, nq[2] = {0, 0};
+    int rs = 0, rlap = 0, s = 0, lap = 0;   // both rings: next stage, times round
+    int nq[2] = {0, 0};
     ExtSeg g;
     while (cta.next(g)) {
         const int nb = ext_blocks(g);
@@ -545,12 +559,11 @@ __device__ __forceinline__ void ext_widen(const ExtendParams &p, ExtCta<T, D, F8
             ++nq[x];
         }
         const ExtOrder order = {g.twin != 0, nb};
-        for (int t = 0; t < 2 * nb && !cta.dead; ++t, ++n) {
+        for (int t = 0; t < 2 * nb && !cta.dead; ++t) {
             int i;
             order.item(t, i);
             const int left = g.m - (g.blk0 + i) * C::CT;
-            const int rs = n % NR, s = n % ST;
-            if (!cta.wait(cta.r_full(rs), n / NR) || (n >= ST && !cta.wait(cta.empty(s), n / ST - 1)))
+            if (!cta.wait(cta.r_full(rs), rlap) || (lap > 0 && !cta.wait(cta.empty(s), lap - 1)))
                 break;
             const uint32_t src = cta.raw + (uint32_t)(rs * C::RAW_BYTES) + src0;
             const uint32_t dst = cta.ring + (uint32_t)(s * C::BLOCK_BYTES);
@@ -579,6 +592,14 @@ __device__ __forceinline__ void ext_widen(const ExtendParams &p, ExtCta<T, D, F8
             if (cta.lane == 0) {
                 mbar_arrive(cta.full(s));
                 mbar_arrive(cta.r_empty(rs));
+            }
+            if (++rs == NR) {
+                rs = 0;
+                ++rlap;
+            }
+            if (++s == ST) {
+                s = 0;
+                ++lap;
             }
         }
     }
