@@ -36,9 +36,20 @@ struct ExtCut {
     int item, off, blk, pad;
 };
 
+// An item that was cut: the cuts inside it are [c0, c1).
+struct ExtSplit {
+    int c0, c1;
+    int rows;    // rows of the split items before it
+    int row0, ntok, b;   // its tile
+    int vh;      // virtual head
+    int pad;
+};
+
 struct ExtPlanHeader {
     int n_items;   // tiles * virtual heads
     int waves;     // whole items each CTA takes: item w * grid + c (odd w: from the far end)
+    int n_splits;
+    int split_rows;   // rows of all split items
 };
 
 struct ExtendParams {
@@ -75,6 +86,7 @@ struct ExtendParams {
     ExtTile *tiles;          // [max_tiles] by descending cost
     long long *cost_sum;     // [max_tiles + 1] costs before, over the virtual heads
     ExtCut *cuts;            // [grid + 1]
+    ExtSplit *splits;        // [grid]
     float *part_o;           // [slots][2 * EXT_M][d] sums of weights times V
     float2 *part_ml;         // [slots][2 * EXT_M] (reference max, sum of weights)
 };

@@ -118,9 +118,12 @@ __global__ void __launch_bounds__(PT, 1) extend_plan_kernel(const ExtendParams p
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ long long sums[32];
     __shared__ int maxs[32];
-    __shared__ int hist[BUCKETS * PW];   // bucket-major, then warp
-    __shared__ int near_start[NEAR], near_blk[NEAR];
+    __shared__ int near_blk[NEAR];
     __shared__ long long near_sum[NEAR + 1];
+    __shared__ ExtCut near_cut[PT];                         // at the end; before that
+    int *hist = reinterpret_cast<int *>(near_cut);          // bucket-major, then warp
+    int *near_start = hist + BUCKETS * PW;
+    static_assert((BUCKETS * PW + NEAR) * sizeof(int) <= sizeof near_cut, "both in the cuts' place");
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int Hv = p.Hkv * p.NG;
     const int tt = 2 * p.tps;
@@ -275,87 +278,78 @@ __global__ void __launch_bounds__(PT, 1) extend_plan_kernel(const ExtendParams p
             c.blk = max(0, c.off - EXT_START);
         }
         p.cuts[tid] = c;
+        near_cut[tid] = c;
+    }
+    __syncthreads();
+
+    // the items with cuts inside, for the merge: a thread at each first cut
+    const bool is = tid > 0 && tid < G && near_cut[tid].blk > 0 &&
+                    !(near_cut[tid - 1].item == near_cut[tid].item && near_cut[tid - 1].blk > 0);
+    ExtSplit sp = {};
+    int rows = 0;
+    if (is) {
+        const int item = near_cut[tid].item;
+        const ExtTile t = p.tiles[item / Hv];
+        sp.c0 = tid;
+        sp.c1 = tid + 1;
+        while (sp.c1 < G && near_cut[sp.c1].item == item && near_cut[sp.c1].blk > 0)
+            ++sp.c1;
+        sp.row0 = t.row0;
+        sp.ntok = t.ntok;
+        sp.b = t.b;
+        sp.vh = item % Hv;
+        rows = t.ntok * p.Gs;
+    }
+    // counts below 2^20, rows below 2^40: one scan for both
+    const long long both = scan_block(((long long)rows << 20) | (is ? 1 : 0), sums, total);
+    if (is) {
+        sp.rows = (int)(both >> 20) - rows;
+        p.splits[(int)(both & ((1 << 20) - 1)) - 1] = sp;
     }
     if (tid == 0) {
-        p.header->n_items = (int)items;
-        p.header->waves = waves;
+        ExtPlanHeader hd;
+        hd.n_items = (int)items;
+        hd.waves = waves;
+        hd.n_splits = (int)(total & ((1 << 20) - 1));
+        hd.split_rows = (int)(total >> 20);
+        *p.header = hd;
     }
 }
 
 // The merge of the split items, a warp a row, the pieces in the order of the
 // cuts:
 //     M = max m_i,  out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.
-// Every CTA reads the cuts, lists the split items and their rows, and takes
-// its share of all those rows.
+// Every CTA reads the list of the split items and takes its share of their
+// rows.
 constexpr int MT = 256;         // threads
-constexpr int MAX_CUTS = 1024;
+constexpr int MAX_CUTS = 1023;
 
 template <int D> __global__ void __launch_bounds__(MT) extend_merge_kernel(const ExtendParams p)
 {
-    __shared__ ExtCut cuts[MAX_CUTS + 1];
-    __shared__ int first[MAX_CUTS];      // the first cut of each split item
-    __shared__ int rows[MAX_CUTS + 1];   // rows before it
-    __shared__ int warp_n[MT / 32], warp_r[MT / 32];
+    __shared__ ExtSplit splits[MAX_CUTS];
+    __shared__ int cut_blk[MAX_CUTS + 1];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-    const int Hv = p.Hkv * p.NG;
-    for (int c = tid; c <= p.grid; c += MT)
-        cuts[c] = p.cuts[c];
-    __syncthreads();
-    // cuts inside an item: 1 .. grid - 1 with blocks before them
-    int n = 0, total = 0;
-    for (int base = 1; base < p.grid; base += MT) {
-        const int c = base + tid;
-        const bool is = c < p.grid && cuts[c].blk > 0 && !(cuts[c - 1].item == cuts[c].item && cuts[c - 1].blk > 0);
-        int r = 0;
-        if (is)
-            r = min(p.tiles[cuts[c].item / Hv].ntok, 2 * p.tps) * p.Gs;
-        const unsigned vote = __ballot_sync(FULL_MASK, is);
-        int sum = r;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(FULL_MASK, sum, o);
-            if (lane >= o)
-                sum += y;
-        }
-        if (lane == 31) {
-            warp_n[w] = __popc(vote);
-            warp_r[w] = sum;
-        }
-        __syncthreads();
-        int bn = n, br = total;
-        for (int i = 0; i < MT / 32; ++i) {
-            if (i < w) {
-                bn += warp_n[i];
-                br += warp_r[i];
-            }
-            n += warp_n[i];
-            total += warp_r[i];
-        }
-        if (is) {
-            const int at = bn + __popc(vote & ((1u << lane) - 1));
-            first[at] = c;
-            rows[at] = br + sum - r;
-        }
-        __syncthreads();
+    const int tid = threadIdx.x, lane = tid & 31;
+    const ExtPlanHeader hd = *p.header;
+    for (int i = tid; i < p.grid; i += MT) {
+        splits[i] = p.splits[i];   // (those behind the last are not used)
+        cut_blk[i] = p.cuts[i].blk;
     }
-
+    __syncthreads();
     constexpr int E = D / 32;
-    for (int x = blockIdx.x * (MT / 32) + w; x < total; x += gridDim.x * (MT / 32)) {
-        int lo = 0, hi = n - 1;   // the last item with rows <= x
+    for (int x = blockIdx.x * (MT / 32) + (tid >> 5); x < hd.split_rows; x += gridDim.x * (MT / 32)) {
+        int lo = 0, hi = hd.n_splits - 1;   // the last item with rows <= x
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (rows[mid] <= x)
+            if (splits[mid].rows <= x)
                 lo = mid;
             else
                 hi = mid - 1;
         }
-        const int c0 = first[lo];
-        const ExtCut cut = cuts[c0];
-        const ExtTile t = p.tiles[cut.item / Hv];
-        const int vh = cut.item % Hv, h = vh / p.NG, s = vh % p.NG;
+        const ExtSplit t = splits[lo];
+        const int h = t.vh / p.NG, s = t.vh % p.NG;
         const int gv = min(p.Gs, p.G - s * p.Gs), hq0 = h * p.G + s * p.Gs;
-        const int tok = (x - rows[lo]) / p.Gs, g = (x - rows[lo]) % p.Gs;
+        const int tok = (x - t.rows) / p.Gs, g = (x - t.rows) % p.Gs;
         if (g >= gv)
             continue;
         const int r = tok / p.tps * EXT_M + tok % p.tps * p.Gs + g;   // its row of the partials
@@ -365,15 +359,14 @@ template <int D> __global__ void __launch_bounds__(MT) extend_merge_kernel(const
             o[e] = 0.f;
         // the piece left of the first cut, then the one right of each cut
         // inside the item (none where two cuts coincide)
-        for (int i = c0 - 1; i == c0 - 1 || (i < p.grid && cuts[i].item == cut.item); i += 4) {
+        for (int i = t.c0 - 1; i < t.c1; i += 4) {
             float2 ml[4];
             float v[4][E];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const int k = i + u;
-                const bool some = k < c0 || (k < p.grid && cuts[k].item == cut.item &&
-                                             (cuts[k + 1].item != cut.item || cuts[k + 1].blk > cuts[k].blk));
-                const long long row = (long long)(some ? (k < c0 ? 2 * c0 : 2 * k + 1) : 2 * c0) * 2 * EXT_M + r;
+                const bool some = k < t.c0 || (k < t.c1 && (k + 1 == t.c1 || cut_blk[k + 1] > cut_blk[k]));
+                const long long row = (long long)(some && k >= t.c0 ? 2 * k + 1 : 2 * t.c0) * 2 * EXT_M + r;
                 ml[u] = __ldcg(p.part_ml + row);
                 const float *src = p.part_o + row * D + lane * E;
                 if (E == 4) {
@@ -405,7 +398,18 @@ template <int D> __global__ void __launch_bounds__(MT) extend_merge_kernel(const
         const float inv = any ? vs / L : 0.f;
 #pragma unroll
         for (int e = 0; e < E; ++e)
-            store_out(p.out, qrow * D + lane * E + e, p.out_dtype, any ? o[e] * inv : 0.f);
+            o[e] = any ? o[e] * inv : 0.f;
+        if (p.out_dtype == 0) {
+#pragma unroll
+            for (int e = 0; e < E; e += 2)
+                *reinterpret_cast<float2 *>(static_cast<float *>(p.out) + qrow * D + lane * E + e) =
+                    make_float2(o[e], o[e + 1]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; e += 2)
+                *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + qrow * D + lane * E + e) =
+                    p.out_dtype == 1 ? Mma<__half>::pack(o[e], o[e + 1]) : Mma<__nv_bfloat16>::pack(o[e], o[e + 1]);
+        }
         if (p.lse && lane == 0)
             p.lse[qrow] = any ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
     }

@@ -14,36 +14,47 @@
 namespace fd {
 namespace {
 
-constexpr int RT = 1024;   // threads of the one CTA that keeps the books
+constexpr int RT = 1024;     // threads of a CTA
+constexpr int CLUSTER = 8;   // CTAs that write slots and positions
+constexpr int RW = RT / 32;
 
-// Inclusive sum over the block, and the block's total.
-__device__ __forceinline__ long long block_scan(long long x, long long *warp_sums, long long &total)
-{
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(FULL_MASK, x, o);
-        if (lane >= o)
-            x += y;
-    }
-    __syncthreads();   // the sums of the previous call have been read
-    if (lane == 31)
-        warp_sums[w] = x;
-    __syncthreads();
-    if (w == 0) {
-        long long s = warp_sums[lane];
+// Inclusive sums of N values over the block, and their totals.
+template <int N> struct Scan {
+    long long warp[N][RW];
+    __device__ __forceinline__ void run(long long (&x)[N], long long (&total)[N])
+    {
+        const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(FULL_MASK, s, o);
-            if (lane >= o)
-                s += y;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const long long y = __shfl_up_sync(FULL_MASK, x[i], o);
+                if (lane >= o)
+                    x[i] += y;
+            }
         }
-        warp_sums[lane] = s;
+        __syncthreads();   // the sums of the previous call have been read
+        if (lane == 31) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                warp[i][w] = x[i];
+        }
+        __syncthreads();
+        // every warp sums the warps before it, and all of them
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const long long s = warp[i][lane];
+            long long before = lane < w ? s : 0, all = s;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) {
+                before += __shfl_xor_sync(FULL_MASK, before, o);
+                all += __shfl_xor_sync(FULL_MASK, all, o);
+            }
+            x[i] += before;
+            total[i] = all;
+        }
     }
-    __syncthreads();
-    total = warp_sums[31];
-    return x + (w ? warp_sums[w - 1] : 0);
-}
+};
 
 struct Change {
     int oldn, newn, po, pn;
@@ -62,24 +73,60 @@ __device__ __forceinline__ Change change_of(const ResizeParams &p, int b)
     return c;
 }
 
-__global__ void __launch_bounds__(RT, 1) resize_kernel(const ResizeParams p)
+// The pages of a chunk of sequences: thread b's are x[b] .. x[b + 1] - 1 of
+// the chunk's, its first one page `page0[b]` of its sequence.
+struct Flat {
+    int x[RT + 1];
+    int page0[RT];
+    // the thread whose pages i is among
+    __device__ __forceinline__ int owner(int i) const
+    {
+        int lo = 0, hi = RT - 1;   // the last with x <= i
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (x[mid] <= i)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        return lo;
+    }
+};
+
+__device__ __forceinline__ void keep_books(const ResizeParams &p)
 {
-    __shared__ long long sums[32];
+    __shared__ Scan<3> scan3;
+    __shared__ Scan<2> scan2;
+    __shared__ Flat flat;
     const int tid = threadIdx.x;
     const long long count0 = min(max(*p.free_count, 0), p.num_pages);
     unsigned bad = 0;
+    const bool once = p.B <= RT;   // one chunk: its changes and sums stay in registers
 
     // how many pages come back
     long long back = 0;
-    for (int b0 = 0; b0 < p.B; b0 += RT) {
+    Change c = {};
+    long long sum[3] = {0, 0, 0}, total[3], own[3] = {0, 0, 0};   // released, needed, new tokens
+    auto load = [&](int b0) {
         const int b = b0 + tid;
-        long long r = 0, total;
+        c = {};
+        own[0] = own[1] = own[2] = 0;
         if (b < p.B) {
-            const Change c = change_of(p, b);
-            r = max(0, c.po - c.pn);
+            c = change_of(p, b);
+            own[0] = max(0, c.po - c.pn);
+            if (c.fits) {
+                own[1] = max(0, c.pn - c.po);
+                own[2] = max(0, c.newn - c.oldn);
+            }
         }
-        block_scan(r, sums, total);
-        back += total;
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+            sum[i] = own[i];
+        scan3.run(sum, total);
+    };
+    for (int b0 = 0; b0 < p.B; b0 += RT) {
+        load(b0);
+        back += total[0];
     }
     const long long top = count0 + back;
 
@@ -87,60 +134,58 @@ __global__ void __launch_bounds__(RT, 1) resize_kernel(const ResizeParams p)
     // out of later calls by the range checks of whoever reads the table
     long long done = 0;
     for (int b0 = 0; back > 0 && b0 < p.B; b0 += RT) {
-        const int b = b0 + tid;
-        long long r = 0, total;
-        Change c = {};
-        if (b < p.B) {
-            c = change_of(p, b);
-            r = max(0, c.po - c.pn);
-        }
-        const long long first = done + block_scan(r, sums, total) - r;
-        for (int j = 0; j < r; ++j) {
-            const long long at = top - 1 - (first + j);
-            const int page = p.table[(long long)b * p.max_pages + c.pn + j];
+        if (!once)
+            load(b0);
+        __syncthreads();   // the pages before have been written
+        flat.x[tid] = (int)(sum[0] - own[0]);
+        flat.page0[tid] = c.pn;
+        __syncthreads();
+        for (int i = tid; i < total[0]; i += RT) {
+            const int o = flat.owner(i), b = b0 + o;
+            const long long at = top - 1 - (done + i);
+            const int page = p.table[(long long)b * p.max_pages + flat.page0[o] + (i - flat.x[o])];
             if (page < 0 || page >= p.num_pages || at >= p.num_pages)
                 bad |= STATUS_BAD_PAGE;
             if (at < p.num_pages)
                 p.free_pages[at] = page;
         }
-        done += total;
+        done += total[0];
     }
     __syncthreads();   // what is taken below may have come back above
 
     // growth, in order of b, as far as the pages (and the slots) last
     long long pages = 0, tokens = 0, grown = 0, taken = 0;
     for (int b0 = 0; b0 < p.B; b0 += RT) {
+        if (!once)
+            load(b0);
         const int b = b0 + tid;
-        long long need = 0, more = 0, total;
-        Change c = {};
-        if (b < p.B) {
-            c = change_of(p, b);
-            if (c.fits) {
-                need = max(0, c.pn - c.po);
-                more = max(0, c.newn - c.oldn);
-            }
-        }
-        const long long cp = pages + block_scan(need, sums, total);
-        pages += total;
-        const long long ct = tokens + block_scan(more, sums, total);
-        tokens += total;
-        const bool given = b < p.B && c.fits && (need == 0 || cp <= min(top, (long long)p.num_pages)) &&
-                           (more == 0 || !p.slots || ct <= p.max_tokens);
-        const long long mine = given ? need : 0;
-        const long long first = taken + block_scan(mine, sums, total) - mine;
-        taken += total;
-        for (int j = 0; j < mine; ++j) {
-            const long long at = top - 1 - (first + j);
-            p.table[(long long)b * p.max_pages + c.po + j] = at < p.num_pages ? p.free_pages[at] : -1;
-        }
-        const long long g = given ? more : 0;
-        const long long cu = grown + block_scan(g, sums, total);
-        grown += total;
+        const bool given = b < p.B && c.fits &&
+                           (own[1] == 0 || pages + sum[1] <= min(top, (long long)p.num_pages)) &&
+                           (own[2] == 0 || tokens + sum[2] <= p.max_tokens);
+        pages += total[1];
+        tokens += total[2];
+        const long long mine = given ? own[1] : 0, g = given ? own[2] : 0;
+        long long two[2] = {mine, g}, all[2];
+        scan2.run(two, all);
         if (b < p.B) {
             p.seqlens[b] = given ? c.newn : c.oldn;
             if (p.cu)
-                p.cu[b + 1] = (int)cu;
+                p.cu[b + 1] = (int)(grown + two[1]);
         }
+        if (all[0] > 0) {
+            __syncthreads();   // the pages before have been written
+            flat.x[tid] = (int)(two[0] - mine);
+            flat.page0[tid] = c.po;
+            __syncthreads();
+            for (int i = tid; i < all[0]; i += RT) {
+                const int o = flat.owner(i);
+                const long long at = top - 1 - (taken + i);
+                p.table[(long long)(b0 + o) * p.max_pages + flat.page0[o] + (i - flat.x[o])] =
+                    at < p.num_pages ? p.free_pages[at] : -1;
+            }
+        }
+        taken += all[0];
+        grown += all[1];
     }
     if (tid == 0) {
         if (p.cu)
@@ -151,43 +196,60 @@ __global__ void __launch_bounds__(RT, 1) resize_kernel(const ResizeParams p)
         atomicOr(p.status, bad);
 }
 
-// A thread a token: its sequence by bisection of the offsets, then its
-// position and its page.
-__global__ void slots_kernel(const ResizeParams p)
+// The cluster's first CTA keeps the books; then all of them write a slot and
+// a position a thread: the token's sequence by bisection of the offsets,
+// its position and its page from what the first CTA wrote.
+__global__ void __launch_bounds__(RT, 1) resize_kernel(const ResizeParams p)
 {
-    const int i = blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= p.max_tokens)
+    if (blockIdx.x == 0)
+        keep_books(p);
+    if (!p.slots && !p.positions)
         return;
-    int slot = -1, pos = 0;
-    if (i < p.cu[p.B]) {
-        int lo = 0, hi = p.B - 1;   // the last b with cu[b] <= i
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (p.cu[mid] <= i)
-                lo = mid;
-            else
-                hi = mid - 1;
+    // the first CTA's writes, to the others
+    __threadfence();
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+    const int grown = p.cu[p.B];
+    for (int i = blockIdx.x * RT + threadIdx.x; i < p.max_tokens; i += gridDim.x * RT) {
+        int slot = -1, pos = 0;
+        if (i < grown) {
+            int lo = 0, hi = p.B - 1;   // the last b with cu[b] <= i
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (p.cu[mid] <= i)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            pos = p.seqlens[lo] - (p.cu[lo + 1] - i);
+            const int page = p.table[(long long)lo * p.max_pages + pos / p.page_size];
+            slot = page < 0 ? -1 : (int)((long long)page * p.page_size + pos % p.page_size);
         }
-        pos = p.seqlens[lo] - (p.cu[lo + 1] - i);
-        const int page = p.table[(long long)lo * p.max_pages + pos / p.page_size];
-        slot = page < 0 ? -1 : (int)((long long)page * p.page_size + pos % p.page_size);
+        if (p.slots)
+            p.slots[i] = slot;
+        if (p.positions)
+            p.positions[i] = pos;
     }
-    if (p.slots)
-        p.slots[i] = slot;
-    if (p.positions)
-        p.positions[i] = pos;
 }
 
 }  // namespace
 
 cudaError_t launch_resize(const ResizeParams &p, cudaStream_t s)
 {
-    resize_kernel<<<1, RT, 0, s>>>(p);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || p.max_tokens == 0 || (!p.slots && !p.positions))
-        return e;
-    slots_kernel<<<(p.max_tokens + 255) / 256, 256, 0, s>>>(p);
-    return cudaGetLastError();
+    // one CTA where one can write the slots in a pass (or there are none)
+    const bool tokens = p.slots || p.positions;
+    const int ctas = tokens && p.max_tokens > RT ? CLUSTER : 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(RT);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = ctas;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, resize_kernel, p);
 }
 
 }  // namespace fd

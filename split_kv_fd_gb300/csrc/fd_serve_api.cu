@@ -84,7 +84,7 @@ bool map_8bit(CUtensorMap *m, const void *base, int d, long long n1, long long n
 struct ExtLayout {
     int G, NG, Gs, tps, grid;
     long long max_tiles;
-    size_t header, tile_start, tile_blk, tiles, cost_sum, cuts, part_ml, part_o, total;
+    size_t header, tile_start, tile_blk, tiles, cost_sum, cuts, splits, part_ml, part_o, total;
 };
 
 bool ext_layout(int B, int total_q, int Hq, int Hkv, int d, ExtLayout &l)
@@ -113,6 +113,7 @@ bool ext_layout(int B, int total_q, int Hq, int Hkv, int d, ExtLayout &l)
     l.tiles = take((size_t)l.max_tiles * sizeof(ExtTile));
     l.cost_sum = take((size_t)(l.max_tiles + 1) * sizeof(long long));
     l.cuts = take((size_t)(l.grid + 1) * sizeof(ExtCut));
+    l.splits = take((size_t)l.grid * sizeof(ExtSplit));
     l.part_ml = take((size_t)slots * 2 * EXT_M * sizeof(float2));
     l.part_o = take((size_t)slots * 2 * EXT_M * d * sizeof(float));
     l.total = at;
@@ -149,6 +150,7 @@ fd_status run_extend(ExtendParams &p, float scale, void *workspace, size_t works
     p.tiles = reinterpret_cast<ExtTile *>(ws + l.tiles);
     p.cost_sum = reinterpret_cast<long long *>(ws + l.cost_sum);
     p.cuts = reinterpret_cast<ExtCut *>(ws + l.cuts);
+    p.splits = reinterpret_cast<ExtSplit *>(ws + l.splits);
     p.part_ml = reinterpret_cast<float2 *>(ws + l.part_ml);
     p.part_o = reinterpret_cast<float *>(ws + l.part_o);
 
