@@ -15,6 +15,8 @@ namespace fd {
 constexpr int EXT_M = 128;
 // Keys per block.
 constexpr int EXT_CT = 128;
+// CTAs of the main kernel at most: the plan deals with a thread for each.
+constexpr int EXT_MAX_GRID = 255;
 // Boxes of a paged K/V block: at most EXT_CT / 16 row groups.
 constexpr int EXT_MIN_PAGE = 16;
 

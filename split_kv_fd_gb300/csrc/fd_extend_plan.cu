@@ -17,11 +17,12 @@
 namespace fd {
 namespace {
 
-constexpr int PT = 1024;        // threads of the planning CTA
+constexpr int PT = 512;         // threads of the planning CTA
 constexpr int PW = PT / 32;
+static_assert(EXT_MAX_GRID < PT, "a thread a cut");
 constexpr int BUCKETS = 64;     // of the sort by cost
-constexpr int EXT_START = 2;    // cost of an item beside its blocks, in blocks
-constexpr int EXT_MIN_CUT = 3;  // a share of the cut items is at least this cost
+constexpr int EXT_START = 3;    // cost of an item beside its blocks, in blocks
+constexpr int EXT_MIN_CUT = EXT_START + 1;   // a share of the cut items is a block at least
 constexpr int NEAR = 2048;      // up to so many sequences, or tiles, the tables below are in shared memory
 
 __device__ __forceinline__ long long scan_block(long long x, long long *warp_sums, long long &total)
@@ -38,17 +39,18 @@ __device__ __forceinline__ long long scan_block(long long x, long long *warp_sum
         warp_sums[w] = x;
     __syncthreads();
     if (w == 0) {
-        long long s = warp_sums[lane];
+        long long s = lane < PW ? warp_sums[lane] : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long y = __shfl_up_sync(FULL_MASK, s, o);
             if (lane >= o)
                 s += y;
         }
-        warp_sums[lane] = s;
+        if (lane < PW)
+            warp_sums[lane] = s;
     }
     __syncthreads();
-    total = warp_sums[31];
+    total = warp_sums[PW - 1];
     return x + (w ? warp_sums[w - 1] : 0);
 }
 
@@ -59,7 +61,7 @@ __device__ __forceinline__ int max_block(int x, int *warp_max)
     if ((threadIdx.x & 31) == 0)
         warp_max[threadIdx.x >> 5] = x;
     __syncthreads();
-    return __reduce_max_sync(FULL_MASK, warp_max[threadIdx.x & 31]);
+    return __reduce_max_sync(FULL_MASK, warp_max[min(threadIdx.x & 31, PW - 1u)]);
 }
 
 // Sequence b's rows of q, clamped; true if the offsets had to be.
@@ -116,14 +118,13 @@ __device__ __forceinline__ ExtTile tile_at(const ExtendParams &p, const int *til
 __global__ void __launch_bounds__(PT, 1) extend_plan_kernel(const ExtendParams p)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    __shared__ long long sums[32];
-    __shared__ int maxs[32];
+    __shared__ long long sums[PW];
+    __shared__ int maxs[PW];
     __shared__ int near_blk[NEAR];
     __shared__ long long near_sum[NEAR + 1];
-    __shared__ ExtCut near_cut[PT];                         // at the end; before that
-    int *hist = reinterpret_cast<int *>(near_cut);          // bucket-major, then warp
-    int *near_start = hist + BUCKETS * PW;
-    static_assert((BUCKETS * PW + NEAR) * sizeof(int) <= sizeof near_cut, "both in the cuts' place");
+    __shared__ int near_start[NEAR];
+    __shared__ int hist[BUCKETS * PW];   // bucket-major, then warp
+    __shared__ ExtCut near_cut[PT];
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int Hv = p.Hkv * p.NG;
     const int tt = 2 * p.tps;
@@ -322,12 +323,11 @@ __global__ void __launch_bounds__(PT, 1) extend_plan_kernel(const ExtendParams p
 // Every CTA reads the list of the split items and takes its share of their
 // rows.
 constexpr int MT = 256;         // threads
-constexpr int MAX_CUTS = 1023;
 
 template <int D> __global__ void __launch_bounds__(MT) extend_merge_kernel(const ExtendParams p)
 {
-    __shared__ ExtSplit splits[MAX_CUTS];
-    __shared__ int cut_blk[MAX_CUTS + 1];
+    __shared__ ExtSplit splits[EXT_MAX_GRID];
+    __shared__ int cut_blk[EXT_MAX_GRID];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31;
     const ExtPlanHeader hd = *p.header;

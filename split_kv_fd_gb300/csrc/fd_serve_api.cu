@@ -94,7 +94,7 @@ bool ext_layout(int B, int total_q, int Hq, int Hkv, int d, ExtLayout &l)
     const int sms = sm_count();
     if (sms <= 0)
         return false;
-    l.grid = sms < 1023 ? sms : 1023;   // the plan deals in one CTA of 1024 threads
+    l.grid = sms < EXT_MAX_GRID ? sms : EXT_MAX_GRID;
     l.G = Hq > 0 ? Hq / Hkv : 1;
     l.NG = (l.G + EXT_M - 1) / EXT_M;
     l.Gs = (l.G + l.NG - 1) / l.NG;
