@@ -661,6 +661,19 @@ __device__ __forceinline__ void ext_mma(const ExtendParams &p, ExtCta<T, D, F8> 
         }
         ++np;
     };
+    // The same for a sequence's last block: of the 16-key steps only the
+    // first `steps` hold keys
+    auto issue_pv_tail = [&](int x, int st, bool first, int &np, int steps) {
+        const uint64_t b = vdesc + (uint64_t)(st * (C::BLOCK_BYTES >> 4));
+        if (!cta.wait(cta.p_full(x, 0), np) || !cta.wait(cta.p_full(x, 1), np))
+            return;
+        tc_fence_after();
+#pragma unroll 1
+        for (int ks = 0; ks < steps; ++ks)
+            tc_mma_ts_if(one, tmem + (uint32_t)C::tm_o(x), tmem + (uint32_t)(C::tm_p(x) + ks * 8),
+                         b + (uint64_t)(ks * (2048 >> 4)), ID_O, (!first || ks > 0) ? 1u : 0u);
+        ++np;
+    };
     ExtSeg g;
     while (cta.next(g)) {
         const int nb = ext_blocks(g);
@@ -726,21 +739,26 @@ __device__ __forceinline__ void ext_mma(const ExtendParams &p, ExtCta<T, D, F8> 
             const int k = i + ahead;
             const bool more = k < nb;
             Cursor vc = cur;
+            int steps = C::CT / 16;
             if (i >= 0) {
                 cur.step();
                 if (!landed(vc))
                     break;
                 const int left = g.m - (g.blk0 + i) * C::CT;
-                if (!F8 && left < C::CT) {
-                    // V's rows behind the sequence's last key may hold
-                    // anything, and 0 * NaN is NaN: zeros instead
-                    const uint32_t vb = cta.ring + (uint32_t)(vc.slot * C::BLOCK_BYTES);
-                    for (int e = cta.lane; e < (C::CT - left) * C::PLANES * 8; e += 32) {
-                        const int pl = e / ((C::CT - left) * 8), o = e % ((C::CT - left) * 8);
-                        sts128(vb + (uint32_t)(pl * C::PLANE + left * 128 + o * 16), make_uint4(0, 0, 0, 0));
+                if (left < C::CT) {
+                    steps = (left + 15) / 16;
+                    if (!F8) {
+                        // V's rows behind the sequence's last key may hold
+                        // anything, and 0 * NaN is NaN: zeros instead, in the
+                        // last step that is computed
+                        const uint32_t vb = cta.ring + (uint32_t)(vc.slot * C::BLOCK_BYTES + left * 128);
+                        for (int e = cta.lane; e < (steps * 16 - left) * 8; e += 32)
+#pragma unroll
+                            for (int pl = 0; pl < C::PLANES; ++pl)
+                                sts128(vb + (uint32_t)(pl * C::PLANE + e * 16), make_uint4(0, 0, 0, 0));
+                        fence_proxy_async_smem();
+                        __syncwarp();
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
                 }
             }
             const int last = has(1, i) ? 1 : 0;   // the engine that is done with V last
@@ -749,7 +767,10 @@ __device__ __forceinline__ void ext_mma(const ExtendParams &p, ExtCta<T, D, F8> 
             for (int x = 0; x < 2 && !cta.dead; ++x) {
                 if (has(x, i)) {
                     int np = x ? np1 : np0;
-                    issue_pv(x, vc.slot, i < ahead, np);
+                    if (steps == C::CT / 16)
+                        issue_pv(x, vc.slot, i < ahead, np);
+                    else
+                        issue_pv_tail(x, vc.slot, i < ahead, np, steps);
                     (x ? np1 : np0) = np;
                     if (!has(x, k))
                         tc_commit_if(one, cta.o_full(x));
