@@ -213,8 +213,8 @@ template <typename T, int D, bool F8> struct ExtCta {
     using C = ExtCfg<T, D, F8>;
     uint32_t ring, raw, qbuf, bar0;
     volatile ExtSeg *segs;
-    float2 *xch;            // [2][M]
-    signed char *qexp;      // [2 in flight][2][M]
+    volatile float *xch;    // [2][M] pairs
+    volatile signed char *qexp;   // [2 in flight][2][M]
     int lane;
     int sg = 0;             // segments taken so far
     bool dead = false;
@@ -814,7 +814,7 @@ __device__ __forceinline__ void ext_softmax(const ExtendParams &p, ExtCta<T, D, 
     const uint32_t tl = tmem + ((uint32_t)((w & 3) * 32) << 16);
     const int rtok = row / p.Gs, rg = row % p.Gs;
     int ns = 0, no = 0, meets = 0;
-    int nq[2] = {0, 0};
+    int nq0 = 0, nq1 = 0;   // E4M3: loads of each sub-tile's Q
     ExtSeg g;
     while (cta.next(g)) {
         const bool twin = g.twin != 0;
@@ -830,20 +830,13 @@ __device__ __forceinline__ void ext_softmax(const ExtendParams &p, ExtCta<T, D, 
         if (F8) {
             sc *= __ldg(p.k_scale + (long long)g.b * p.Hkv + g.h);
             vscale = __ldg(p.v_scale + (long long)g.b * p.Hkv + g.h);
-            // engine 1 may need either Q: it sees every phase of both, since
-            // a wait tells a phase only from the one before it
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                if (y > x || g.end(y) <= g.blk0)
-                    continue;
-                if (!cta.wait(cta.q_wide(y), nq[y]))
-                    break;
-                if (y == sub) {
-                    const int sh = cta.qexp[((nq[y] & 1) * 2 + y) * C::M + row];
-                    sc *= __uint_as_float((uint32_t)(127 - sh) << 23);
-                }
-                ++nq[y];
-            }
+        }
+        // the exponents of this segment's Q: of its sub-tile's n-th load
+        int qn = 0;
+        if (F8) {
+            qn = (sub ? nq1 : nq0) & 1;
+            nq0 += g.end0 > g.blk0;
+            nq1 += g.end1 > g.blk0;
         }
         float mref = -INFINITY, l = 0.f;
         const int begin = g.blk0 + (twin ? x : 0), end = g.end(sub), step = twin ? 2 : 1;
@@ -855,6 +848,13 @@ __device__ __forceinline__ void ext_softmax(const ExtendParams &p, ExtCta<T, D, 
                 break;
             ++ns;
             tc_fence_after();
+            if (F8 && j == begin) {
+                // S was issued behind the wait for Q's widening, which wrote
+                // them (waiting for that again here could miss a phase: an
+                // engine without blocks falls behind by several segments)
+                const int sh = cta.qexp[(qn * 2 + sub) * C::M + row];
+                sc *= __uint_as_float((uint32_t)(127 - sh) << 23);
+            }
             float s[4][32];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -956,13 +956,15 @@ __device__ __forceinline__ void ext_softmax(const ExtendParams &p, ExtCta<T, D, 
         if (twin) {
             // both engines hold the same rows: they swap (reference, sum),
             // and each joins and writes half of the columns
-            cta.xch[x * C::M + row] = make_float2(mref, l);
+            cta.xch[2 * (x * C::M + row)] = mref;
+            cta.xch[2 * (x * C::M + row) + 1] = l;
             tc_fence_before();
             cta.arrive(cta.meet());
             if (!cta.wait(cta.meet(), meets++))
                 break;
             tc_fence_after();
-            const float2 a0 = cta.xch[row], a1 = cta.xch[C::M + row];
+            const float2 a0 = make_float2(cta.xch[2 * row], cta.xch[2 * row + 1]);
+            const float2 a1 = make_float2(cta.xch[2 * (C::M + row)], cta.xch[2 * (C::M + row) + 1]);
             M = fmaxf(a0.x, a1.x);
             f0 = a0.x == -INFINITY ? 0.f : ex2(a0.x - M);
             f1 = a1.x == -INFINITY ? 0.f : ex2(a1.x - M);
@@ -1039,13 +1041,13 @@ __global__ void __launch_bounds__(ExtCfg<T, D, F8>::THREADS, 1) extend_kernel(co
     unsigned char *rest = smem + (cta.qbuf + 2 * C::Q_BYTES - cta.ring);
     cta.bar0 = smem_addr(rest);
     rest += C::NBAR * 8;
-    cta.xch = reinterpret_cast<float2 *>(rest);
+    cta.xch = reinterpret_cast<volatile float *>(rest);
     rest += C::XCH_BYTES;
     cta.segs = reinterpret_cast<volatile ExtSeg *>(rest);
     static_assert(sizeof(ExtSeg) == 56, "segment slots");
     rest += C::SEGS * 56;
     uint32_t *misc = reinterpret_cast<uint32_t *>(rest);
-    cta.qexp = reinterpret_cast<signed char *>(rest + 16);
+    cta.qexp = reinterpret_cast<volatile signed char *>(rest + 16);
     if (threadIdx.x == 0) {
         cta.init();
         prefetch_tmap(&p.tmq);

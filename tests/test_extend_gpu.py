@@ -253,3 +253,14 @@ def test_page_pool_past_32_bits():
     out, lse = fd.extend_paged(q, kp, vp, table, pack_offsets([5]).cuda(), torch.tensor([n], dtype=torch.int32, device="cuda"),
                                out_dtype=torch.float32)
     check(out, lse, attend(q, k, v), torch.bfloat16, n)
+
+
+def test_e4m3_many_segments_of_one_subtile():
+    """Many short items a CTA next to long ones: an engine without blocks of
+    its own runs through segments that the other one works on."""
+    g = torch.Generator().manual_seed(5)
+    new = torch.randint(1, 40, (300,), generator=g).tolist()
+    new[::17] = [200 + i for i in range(len(new[::17]))]
+    lens = [n + int(x) for n, x in zip(new, torch.randint(0, 700, (300,), generator=g))]
+    _run8(new, lens, 8, 2, 64, 32, seed=9)
+    _run8(new[:120], lens[:120], 8, 2, 128, 16, "f16", seed=10)
