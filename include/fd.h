@@ -456,7 +456,8 @@ fd_status fd_decode_noalloc(const void *q, const void *k, const void *v, const i
  * what is free, and one that has new tokens when those of all up to it
  * exceed max_tokens (with slots or positions only).  Compare seqlens with
  * target to see which were given.  The result does not depend on the order
- * of threads.  A released entry that names no page, or a stack that would
+ * of threads.  A page belongs to one sequence (one that several tables name
+ * would be given back several times).  A released entry that names no page, or a stack that would
  * pass num_pages, is reported as FD_ERR_BAD_PAGE by fd_device_status.
  * page_size*max_pages and page_size*num_pages must be below 2^31.
  */
@@ -554,7 +555,11 @@ fd_status fd_extend_paged(const void *q, const void *k_pages, const void *v_page
 
 /*
  * fd_extend_paged over E4M3 pages with the scales of fd_decode_gqa_paged_fp8
- * (k_scale, v_scale [B*Hkv] float32); q_dtype f16 or bf16.
+ * (k_scale, v_scale [B*Hkv] float32); q_dtype f16 or bf16.  Both products
+ * are of float16 operands (an E4M3 value is one exactly): the weights are
+ * rounded to float16, and a bf16 query row is scaled by a power of two to a
+ * largest magnitude of 2^8, which keeps its values down to 2^-22 of that
+ * exact.
  */
 fd_status fd_extend_paged_fp8(const void *q, fd_dtype q_dtype, const void *k_pages, const void *v_pages,
                               const float *k_scale, const float *v_scale, const int32_t *block_table,

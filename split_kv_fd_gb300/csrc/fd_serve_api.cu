@@ -154,6 +154,12 @@ fd_status run_extend(ExtendParams &p, float scale, void *workspace, size_t works
     p.part_ml = reinterpret_cast<float2 *>(ws + l.part_ml);
     p.part_o = reinterpret_cast<float *>(ws + l.part_o);
 
+    // a single row's stride may be anything
+    if (p.total_q == 1)
+        p.q_stride = (long long)p.Hq * p.d;
+    if (p.total_k == 1)
+        p.k_stride = p.v_stride = (long long)p.Hkv * p.d;
+
     const long long row = (long long)p.d * 2;
     bool ok = map_16bit(&p.tmq, p.q, p.dtype, p.d, p.Hq, row, p.total_q, p.q_stride * 2, p.Gs, p.tps, 1);
     if (p.paged) {

@@ -564,13 +564,17 @@ def _address(t):
     return None if t is None else t.data_ptr()
 
 
-def _keep(dev, stream, *ts):
-    """Tensors allocated here under the current stream but used on ``stream``
-    are not reused before that stream is done with them."""
-    if stream is not None and stream != torch.cuda.current_stream(dev):
-        for t in ts:
-            if t is not None:
-                t.record_stream(stream)
+def _empty(stream, *args, **kw):
+    """torch.empty for a call on ``stream``: memory of that stream's, since
+    the current one may still work on what it gave back last; and kept until
+    the current one, which will read the result, is done with it."""
+    if stream is None:
+        return torch.empty(*args, **kw)
+    reader = torch.cuda.current_stream(kw["device"])
+    with torch.cuda.stream(stream):
+        t = torch.empty(*args, **kw)
+    t.record_stream(reader)
+    return t
 
 
 def _rows(t, name):
@@ -625,20 +629,18 @@ def resize_pages(seqlens, target, block_table, free_pages, free_count, page_size
     _int32(block_table, (B, width), "block_table")
     _int32(free_pages, (pool,), "free_pages")
     _int32(free_count, (1,), "free_count")
-    own = None
     if slots is not None or positions is not None:
         room = (positions if slots is None else slots).numel()
         for t, n in ((slots, "slots"), (positions, "positions")):
             if t is not None:
                 _int32(t, (room,), n)
         if cu_new is None:
-            own = cu_new = torch.empty(B + 1, dtype=torch.int32, device=seqlens.device)
-    if cu_new is not None and own is None:
+            cu_new = _empty(stream, B + 1, dtype=torch.int32, device=seqlens.device)
+    if cu_new is not None:
         _int32(cu_new, (B + 1,), "cu_new")
     _call("fd_resize_pages", dev, stream, seqlens.data_ptr(), target.data_ptr(), B, block_table.data_ptr(), width,
           free_pages.data_ptr(), free_count.data_ptr(), pool, page_size, _address(slots), _address(positions), room,
           _address(cu_new))
-    _keep(dev, stream, own)
     return cu_new
 
 
@@ -705,15 +707,13 @@ def _extend_bytes(dev, *sizes):
         return max(workspace_size_extend(*sizes), 256)
 
 
-def _extend_out(dev, q, B, Hkv, out_dtype, out, lse, return_lse, workspace):
+def _extend_out(dev, q, B, Hkv, out_dtype, out, lse, return_lse, workspace, stream):
     """out, lse and the workspace of the attention calls of several new
-    tokens, checked or allocated (the workspace for this one call), and
-    those that were allocated."""
+    tokens, checked or allocated (the workspace for this one call)."""
     shape = T, Hq, d = q.shape
-    where, mine = q.device, []
+    where = q.device
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype or q.dtype, device=where)
-        mine.append(out)
+        out = _empty(stream, shape, dtype=out_dtype or q.dtype, device=where)
     elif out.shape != shape or out.get_device() != dev or not out.is_contiguous():
         raise ValueError("out must be contiguous [T, Hq, d] on q's device")
     if out.dtype not in DTYPE_CODE:
@@ -722,14 +722,12 @@ def _extend_out(dev, q, B, Hkv, out_dtype, out, lse, return_lse, workspace):
         if lse.dtype != torch.float32 or lse.shape != (T, Hq) or lse.get_device() != dev or not lse.is_contiguous():
             raise ValueError("lse must be contiguous float32 [T, Hq] on q's device")
     elif return_lse:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=where)
-        mine.append(lse)
+        lse = _empty(stream, (T, Hq), dtype=torch.float32, device=where)
     if workspace is None:
-        workspace = torch.empty(_extend_bytes(dev, B, T, Hq, Hkv, d), dtype=torch.uint8, device=where)
-        mine.append(workspace)
+        workspace = _empty(stream, _extend_bytes(dev, B, T, Hq, Hkv, d), dtype=torch.uint8, device=where)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous and on q's device")
-    return out, lse, workspace, mine
+    return out, lse, workspace
 
 
 def _tail(d, scale, out, lse, workspace):
@@ -763,11 +761,10 @@ def prefill(q, k, v, cu_seqlens_q, cu_seqlens_k=None, causal=True, scale=None, o
     B = cu_seqlens_q.numel() - 1
     _int32(cu_seqlens_q, (B + 1,), "cu_seqlens_q")
     _int32(cu_k, (B + 1,), "cu_seqlens_k")
-    out, lse, workspace, mine = _extend_out(dev, q, B, Hkv, out_dtype, out, lse, return_lse, workspace)
+    out, lse, workspace = _extend_out(dev, q, B, Hkv, out_dtype, out, lse, return_lse, workspace, stream)
     _call("fd_prefill", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens_q.data_ptr(),
           cu_k.data_ptr(), B, T, Tk, Hq, Hkv, d, q_stride, k_stride, v_stride, DTYPE_CODE[q.dtype], bool(causal),
           *_tail(d, scale, out, lse, workspace))
-    _keep(dev, stream, *mine)
     return out, lse
 
 
@@ -807,11 +804,10 @@ def extend_paged(q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens, scale=
     args = _extend_args(q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens)
     if k_pages.dtype != q.dtype:
         raise ValueError("the pages must have q's dtype")
-    out, lse, workspace, mine = _extend_out(dev, q, args[0], args[3], out_dtype, out, lse, return_lse, workspace)
+    out, lse, workspace = _extend_out(dev, q, args[0], args[3], out_dtype, out, lse, return_lse, workspace, stream)
     _call("fd_extend_paged", dev, stream, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
           block_table.data_ptr(), cu_seqlens_q.data_ptr(), seqlens.data_ptr(), *args, DTYPE_CODE[q.dtype],
           *_tail(args[4], scale, out, lse, workspace))
-    _keep(dev, stream, *mine)
     return out, lse
 
 
@@ -825,11 +821,10 @@ def extend_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, cu_seql
     if k_pages.dtype not in (torch.float8_e4m3fn, torch.uint8):
         raise ValueError("pages must be float8_e4m3fn (or uint8 E4M3 bytes)")
     _scales(k_scale, v_scale, (args[0], args[3]))
-    out, lse, workspace, mine = _extend_out(dev, q, args[0], args[3], out_dtype, out, lse, return_lse, workspace)
+    out, lse, workspace = _extend_out(dev, q, args[0], args[3], out_dtype, out, lse, return_lse, workspace, stream)
     _call("fd_extend_paged_fp8", dev, stream, q.data_ptr(), DTYPE_CODE[q.dtype], k_pages.data_ptr(),
           v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), cu_seqlens_q.data_ptr(),
           seqlens.data_ptr(), *args, *_tail(args[4], scale, out, lse, workspace))
-    _keep(dev, stream, *mine)
     return out, lse
 
 

@@ -264,3 +264,12 @@ def test_e4m3_many_segments_of_one_subtile():
     lens = [n + int(x) for n, x in zip(new, torch.randint(0, 700, (300,), generator=g))]
     _run8(new, lens, 8, 2, 64, 32, seed=9)
     _run8(new[:120], lens[:120], 8, 2, 128, 16, "f16", seed=10)
+
+
+def test_past_the_planning_tables():
+    """More sequences, and more tiles, than the plan keeps in shared memory."""
+    g = torch.Generator().manual_seed(6)
+    new = torch.randint(0, 4, (2500,), generator=g).tolist()
+    lens = [n + int(x) for n, x in zip(new, torch.randint(0, 200, (2500,), generator=g))]
+    _run(new, lens, 2, 1, 64, 16, seed=11)
+    _run([4200], [4300], 128, 1, 64, 64, seed=12)

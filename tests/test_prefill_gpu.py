@@ -234,6 +234,40 @@ def test_two_streams_at_once():
         assert torch.equal(o, want[0]) and torch.equal(z, want[1])
 
 
+def test_memory_of_the_stream_that_works():
+    """What a call on another stream allocates is not what the current
+    stream has given back but still writes to."""
+    q, k, v = (_packed([500], h, 128, "bf16", h) for h in (8, 2, 2))
+    cu = pack_offsets([500]).cuda()
+    want = fd.prefill(q, k, v, cu)
+    busy = torch.randn(8192, 8192, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    late = [torch.empty_like(t) for t in want]
+    for _ in range(6):
+        busy = busy @ busy
+    for t in late:
+        t.fill_(7)
+    del late, t
+    out, lse = fd.prefill(q, k, v, cu, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_a_single_row_has_no_stride():
+    q, k, v = (_packed([1], h, 128, "bf16", h) for h in (4, 2, 2))
+    cu = pack_offsets([1]).cuda()
+    want, _ = fd.prefill(q, k, v, cu)
+    out = torch.empty_like(want)
+    ws = torch.empty(fd.workspace_size_extend(1, 1, 4, 2, 128), dtype=torch.uint8, device="cuda")
+    for stride in (0, -64, 1 << 44):
+        out.fill_(5)
+        st = fd.load().fd_prefill(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu.data_ptr(), cu.data_ptr(), 1, 1, 1, 4, 2, 128,
+                                  stride, stride, stride, 2, 1, 0.1, out.data_ptr(), 2, None, ws.data_ptr(), ws.numel(),
+                                  torch.cuda.current_stream().cuda_stream)
+        assert st == 0 and torch.equal(out, want)   # one key: its value, whatever the scale
+
+
 def test_long_rows_past_32_bits():
     """Tokens so far apart that element offsets pass 2^31 (a wide view)."""
     H, d, T = 2, 64, 40
