@@ -2,6 +2,7 @@
 // checks, the choice of decomposition and grid, workspace carving, and the
 // launches.  Nothing here computes attention; every step runs in the kernels.
 #include "fd.h"
+#include "fd_extend.h"
 #include "fd_gqa.cuh"
 #include "fd_gqa_tc8.cuh"
 #include "fd_host.h"

@@ -24,7 +24,6 @@ constexpr unsigned WAIT_LIMIT_POLLS = 1u << 30;
 // Status word bits.
 constexpr unsigned STATUS_TIMEOUT = 1u;
 constexpr unsigned STATUS_BAD_PAGE = 2u;
-constexpr unsigned STATUS_BAD_OFFSETS = 4u;
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p)
 {
@@ -159,26 +158,6 @@ __device__ __forceinline__ bool mbar_wait_bounded_sleep_thread(uint32_t bar, uin
     return false;
 }
 
-// Bounded wait by a whole warp for a phase that is often complete already:
-// one try first, and the clock is read only when that fails (a read of
-// %globaltimer costs about as much as a short wait).
-__device__ __forceinline__ bool mbar_wait_bounded_soon(uint32_t bar, uint32_t parity, uint32_t hint_ns)
-{
-    bool ok = mbar_try_wait(bar, parity);
-    if (!ok) {
-        const unsigned long long t0 = global_ns();
-        for (unsigned i = 0; i < WAIT_LIMIT_POLLS; ++i) {
-            if (mbar_try_wait_hint(bar, parity, hint_ns)) {
-                ok = true;
-                break;
-            }
-            if (global_ns() - t0 > WAIT_LIMIT_NS)
-                break;
-        }
-    }
-    return __all_sync(FULL_MASK, ok);
-}
-
 // 1-D bulk copy global -> shared, completion counted on `bar` in bytes.
 // dst, src and bytes must be multiples of 16.
 __device__ __forceinline__ void bulk_g2s(uint32_t dst, const void *src, uint32_t bytes,
@@ -236,14 +215,6 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
 {
     uint64_t d;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-
-// Two independent round-to-nearest fp32 additions (PTX add.rn.f32x2).
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
 

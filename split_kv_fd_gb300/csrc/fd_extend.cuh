@@ -48,9 +48,8 @@
 // the CTA frees its TMEM.
 #pragma once
 
-#include "fd_device.cuh"
 #include "fd_extend.h"
-#include "fd_tc.cuh"
+#include "fd_extend_ops.cuh"
 
 namespace fd {
 

@@ -10,6 +10,9 @@
 
 namespace fd {
 
+// Status word bit, beside those of fd_device.cuh: offsets had to be clamped.
+constexpr unsigned STATUS_BAD_OFFSETS = 4u;
+
 // A tile's MMA rows are (token, query head of the slice) pairs, token major:
 // two sub-tiles of EXT_M rows, each of EXT_M / Gs tokens.
 constexpr int EXT_M = 128;
@@ -20,8 +23,10 @@ constexpr int EXT_MAX_GRID = 255;
 // Boxes of a paged K/V block: at most EXT_CT / 16 row groups.
 constexpr int EXT_MIN_PAGE = 16;
 
-// One tile of a sequence's new tokens, written by the plan.
-struct ExtTile {
+// One tile of a sequence's new tokens, written by the plan (as 16-byte words,
+// like the other records of the plan: a warp's tiles are scattered, and word
+// by word their stores took half of the plan's time).
+struct alignas(16) ExtTile {
     int row0;    // first token's row of q and out
     int ntok;    // tokens
     int b;       // sequence
@@ -34,12 +39,12 @@ struct ExtTile {
 
 // Where a CTA's share of the split tiles begins: an item (tile, virtual
 // head), the offset in it in cost units, and the block that offset lies in.
-struct ExtCut {
+struct alignas(16) ExtCut {
     int item, off, blk, pad;
 };
 
 // An item that was cut: the cuts inside it are [c0, c1).
-struct ExtSplit {
+struct alignas(16) ExtSplit {
     int c0, c1;
     int rows;    // rows of the split items before it
     int row0, ntok, b;   // its tile
@@ -47,7 +52,7 @@ struct ExtSplit {
     int pad;
 };
 
-struct ExtPlanHeader {
+struct alignas(16) ExtPlanHeader {
     int n_items;   // tiles * virtual heads
     int waves;     // whole items each CTA takes: item w * grid + c (odd w: from the far end)
     int n_splits;

@@ -25,6 +25,7 @@ constexpr int EXT_START = 3;    // cost of an item beside its blocks, in blocks
 constexpr int EXT_MIN_CUT = EXT_START + 1;   // a share of the cut items is a block at least
 constexpr int NEAR = 2048;      // up to so many sequences, or tiles, the tables below are in shared memory
 
+// Inclusive sums over the block, and their total.
 __device__ __forceinline__ long long scan_block(long long x, long long *warp_sums, long long &total)
 {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -38,20 +39,16 @@ __device__ __forceinline__ long long scan_block(long long x, long long *warp_sum
     if (lane == 31)
         warp_sums[w] = x;
     __syncthreads();
-    if (w == 0) {
-        long long s = lane < PW ? warp_sums[lane] : 0;
+    // every warp sums the warps before it, and all of them
+    const long long s = lane < PW ? warp_sums[lane] : 0;
+    long long before = lane < w ? s : 0, all = s;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(FULL_MASK, s, o);
-            if (lane >= o)
-                s += y;
-        }
-        if (lane < PW)
-            warp_sums[lane] = s;
+    for (int o = 16; o; o >>= 1) {
+        before += __shfl_xor_sync(FULL_MASK, before, o);
+        all += __shfl_xor_sync(FULL_MASK, all, o);
     }
-    __syncthreads();
-    total = warp_sums[PW - 1];
-    return x + (w ? warp_sums[w - 1] : 0);
+    total = all;
+    return x + before;
 }
 
 __device__ __forceinline__ int max_block(int x, int *warp_max)
@@ -164,9 +161,20 @@ __global__ void __launch_bounds__(PT, 1) extend_plan_kernel(const ExtendParams p
     __syncthreads();
     const int share = ((n + PW - 1) / PW + 31) & ~31;
     const int i0 = w * share, i1 = min(n, i0 + share);
+    ExtTile t = {};       // a thread's last one: its only one up to PT tiles
+    int key = BUCKETS;
+    auto take = [&](int i) {
+        if (i < i1) {
+            t = tile_at(p, start, i);
+            // blocks are fewer than 2^25
+            key = BUCKETS - 1 - (int)((unsigned)t.nblk * (unsigned)(BUCKETS - 1) / (unsigned)top);
+        } else {
+            key = BUCKETS;
+        }
+    };
     for (int i = i0; i < i1; i += 32) {
+        take(i + lane);
         const bool on = i + lane < i1;
-        const int key = on ? BUCKETS - 1 - (int)((long long)tile_at(p, start, i + lane).nblk * (BUCKETS - 1) / top) : BUCKETS;
         const unsigned same = __match_any_sync(FULL_MASK, key);
         if (on && lane == __ffs(same) - 1)
             hist[key * PW + w] += __popc(same);
@@ -183,13 +191,9 @@ __global__ void __launch_bounds__(PT, 1) extend_plan_kernel(const ExtendParams p
     static_assert(BUCKETS * PW == 2 * PT, "two counts a thread");
     __syncthreads();
     for (int i = i0; i < i1; i += 32) {
+        if (share > 32)
+            take(i + lane);
         const bool on = i + lane < i1;
-        ExtTile t = {};
-        int key = BUCKETS;
-        if (on) {
-            t = tile_at(p, start, i + lane);
-            key = BUCKETS - 1 - (int)((long long)t.nblk * (BUCKETS - 1) / top);
-        }
         const unsigned same = __match_any_sync(FULL_MASK, key);
         int at = 0;
         if (on)
@@ -227,20 +231,36 @@ __global__ void __launch_bounds__(PT, 1) extend_plan_kernel(const ExtendParams p
     int waves = (int)(items / G);
     if (n > 0 && blk[0] + EXT_START > even)
         waves = 0;
-    int load = 0;
-    auto cost_of = [&](int wave) {
-        const long long it = (long long)wave * G + ((wave & 1) ? G - 1 - tid : tid);
-        return blk[(int)it / Hv] + EXT_START;
-    };
-    if (tid < G) {
-#pragma unroll 4
-        for (int x = 0; x < waves; ++x)
-            load += cost_of(x);
-    }
-    while (waves > 0 && max_block(load, maxs) > even) {
-        --waves;
+    long long load = 0;
+    if (waves > 0) {
+        // the tiles of this CTA's items, an even and an odd wave at a time:
+        // items 2 G further on, without a division a step
+        const int dj = 2 * G / Hv, dh = 2 * G % Hv;
+        int fit = waves;   // waves that leave the CTA within the share
+        auto walk = [&](int upto, auto each) {
+            int ja = tid / Hv, ha = tid % Hv, jb = (2 * G - 1 - tid) / Hv, hb = (2 * G - 1 - tid) % Hv;
+            for (int x = 0; x < upto; x += 2) {
+                each(x, blk[ja] + EXT_START);
+                if (x + 1 < upto)
+                    each(x + 1, blk[jb] + EXT_START);
+                ja += dj, ha += dh, jb += dj, hb += dh;
+                if (ha >= Hv)
+                    ha -= Hv, ++ja;
+                if (hb >= Hv)
+                    hb -= Hv, ++jb;
+            }
+        };
+        if (tid < G) {
+            long long sofar = 0;
+            walk(waves, [&](int x, int cost) {
+                sofar += cost;
+                if (sofar > even)
+                    fit = min(fit, x);
+            });
+        }
+        waves = -max_block(-fit, maxs);
         if (tid < G)
-            load -= cost_of(waves);
+            walk(waves, [&](int, int cost) { load += cost; });
     }
 
     // what is left, cut so that every CTA reaches the even share
@@ -317,27 +337,29 @@ __global__ void __launch_bounds__(PT, 1) extend_plan_kernel(const ExtendParams p
     }
 }
 
-// The merge of the split items, a warp a row, the pieces in the order of the
-// cuts:
+// The merge of the split items, 16 lanes a row, the pieces in the order of
+// the cuts:
 //     M = max m_i,  out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.
 // Every CTA reads the list of the split items and takes its share of their
 // rows.
 constexpr int MT = 256;         // threads
+constexpr int ML = 16;          // lanes a row
+constexpr int U = 4;            // pieces in flight
 
 template <int D> __global__ void __launch_bounds__(MT) extend_merge_kernel(const ExtendParams p)
 {
     __shared__ ExtSplit splits[EXT_MAX_GRID];
     __shared__ int cut_blk[EXT_MAX_GRID];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int tid = threadIdx.x, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid % ML;
     const ExtPlanHeader hd = *p.header;
     for (int i = tid; i < p.grid; i += MT) {
         splits[i] = p.splits[i];   // (those behind the last are not used)
         cut_blk[i] = p.cuts[i].blk;
     }
     __syncthreads();
-    constexpr int E = D / 32;
-    for (int x = blockIdx.x * (MT / 32) + (tid >> 5); x < hd.split_rows; x += gridDim.x * (MT / 32)) {
+    constexpr int E = D / ML, V = E / 4;   // a lane's elements, in float4 that lie 64 apart
+    for (int x = blockIdx.x * (MT / ML) + tid / ML; x < hd.split_rows; x += gridDim.x * (MT / ML)) {
         int lo = 0, hi = hd.n_splits - 1;   // the last item with rows <= x
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -359,34 +381,33 @@ template <int D> __global__ void __launch_bounds__(MT) extend_merge_kernel(const
             o[e] = 0.f;
         // the piece left of the first cut, then the one right of each cut
         // inside the item (none where two cuts coincide)
-        for (int i = t.c0 - 1; i < t.c1; i += 4) {
-            float2 ml[4];
-            float v[4][E];
+        for (int i = t.c0 - 1; i < t.c1; i += U) {
+            float2 ml[U];
+            float4 v[U][V];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < U; ++u) {
                 const int k = i + u;
-                const bool some = k < t.c0 || (k < t.c1 && (k + 1 == t.c1 || cut_blk[k + 1] > cut_blk[k]));
-                const long long row = (long long)(some && k >= t.c0 ? 2 * k + 1 : 2 * t.c0) * 2 * EXT_M + r;
-                ml[u] = __ldcg(p.part_ml + row);
-                const float *src = p.part_o + row * D + lane * E;
-                if (E == 4) {
-                    const float4 y = __ldcg(reinterpret_cast<const float4 *>(src));
-                    v[u][0] = y.x, v[u][1] = y.y, v[u][E - 2] = y.z, v[u][E - 1] = y.w;
-                } else {
-                    const float2 y = __ldcg(reinterpret_cast<const float2 *>(src));
-                    v[u][0] = y.x, v[u][1] = y.y;
+                ml[u] = make_float2(-INFINITY, 0.f);
+                if (k < t.c0 || (k < t.c1 && (k + 1 == t.c1 || cut_blk[k + 1] > cut_blk[k]))) {
+                    const long long row = (long long)(k >= t.c0 ? 2 * k + 1 : 2 * t.c0) * 2 * EXT_M + r;
+                    ml[u] = __ldcg(p.part_ml + row);
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        v[u][e] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + row * D) + lane + ML * e);
                 }
-                if (!some)
-                    ml[u].y = 0.f;
             }
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < U; ++u) {
                 if (!(ml[u].y <= 0.f)) {
                     const float mn = fmaxf(M, ml[u].x);
                     const float a = ex2(M - mn), b = ex2(ml[u].x - mn);
 #pragma unroll
-                    for (int e = 0; e < E; ++e)
-                        o[e] = fmaf(b, v[u][e], a * o[e]);
+                    for (int e = 0; e < V; ++e) {
+                        o[4 * e] = fmaf(b, v[u][e].x, a * o[4 * e]);
+                        o[4 * e + 1] = fmaf(b, v[u][e].y, a * o[4 * e + 1]);
+                        o[4 * e + 2] = fmaf(b, v[u][e].z, a * o[4 * e + 2]);
+                        o[4 * e + 3] = fmaf(b, v[u][e].w, a * o[4 * e + 3]);
+                    }
                     L = fmaf(L, a, b * ml[u].y);
                     M = mn;
                 }
@@ -399,16 +420,16 @@ template <int D> __global__ void __launch_bounds__(MT) extend_merge_kernel(const
 #pragma unroll
         for (int e = 0; e < E; ++e)
             o[e] = any ? o[e] * inv : 0.f;
-        if (p.out_dtype == 0) {
 #pragma unroll
-            for (int e = 0; e < E; e += 2)
-                *reinterpret_cast<float2 *>(static_cast<float *>(p.out) + qrow * D + lane * E + e) =
-                    make_float2(o[e], o[e + 1]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < E; e += 2)
-                *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + qrow * D + lane * E + e) =
-                    p.out_dtype == 1 ? Mma<__half>::pack(o[e], o[e + 1]) : Mma<__nv_bfloat16>::pack(o[e], o[e + 1]);
+        for (int e = 0; e < V; ++e) {
+            const long long at = qrow * D + 4 * (lane + ML * e);
+            const float *y = o + 4 * e;
+            if (p.out_dtype == 0)
+                *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) = make_float4(y[0], y[1], y[2], y[3]);
+            else
+                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at) =
+                    p.out_dtype == 1 ? make_uint2(Mma<__half>::pack(y[0], y[1]), Mma<__half>::pack(y[2], y[3]))
+                                     : make_uint2(Mma<__nv_bfloat16>::pack(y[0], y[1]), Mma<__nv_bfloat16>::pack(y[2], y[3]));
         }
         if (p.lse && lane == 0)
             p.lse[qrow] = any ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
