@@ -120,3 +120,53 @@ def test_prefill_is_the_first_chunk():
         ref = attend(q[rows], k[rows], v[rows])
         check(a[0][rows], a[1][rows], ref, torch.bfloat16, n)
         check(b[0][rows], b[1][rows], ref, torch.bfloat16, n)
+
+
+def test_a_captured_step():
+    """Bookkeeping, append and attention in one graph, replayed with new
+    targets and rows; a second graph uses the same workspace in turn."""
+    B, page, pool, Hq, Hkv, d, width, T = 5, 32, 60, 8, 2, 64, 12, 96
+    torch.manual_seed(4)
+    kp, vp = (torch.full((pool, Hkv, page, d), float("nan"), device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    table = torch.full((B, width), -1, dtype=torch.int32, device="cuda")
+    free, count, seq, target = torch.randperm(pool, device="cuda").to(torch.int32), _i32([pool]), _i32([0] * B), _i32([0] * B)
+    qkv = torch.zeros(T, Hq + 2 * Hkv, d, dtype=torch.bfloat16, device="cuda")
+    q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+    slots, pos = torch.zeros(T, dtype=torch.int32, device="cuda"), torch.zeros(T, dtype=torch.int32, device="cuda")
+    cu = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(fd.workspace_size_extend(B, T, Hq, Hkv, d), dtype=torch.uint8, device="cuda")
+    outs = [torch.zeros(T, Hq, d, device="cuda") for _ in range(2)]
+    lses = [torch.zeros(T, Hq, device="cuda") for _ in range(2)]
+
+    def step(i):
+        fd.resize_pages(seq, target, table, free, count, page, slots=slots, positions=pos, cu_new=cu)
+        fd.append_paged(k, v, slots, kp, vp)
+        fd.extend_paged(q, kp, vp, table, cu, seq, out=outs[i], lse=lses[i], workspace=ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(0)   # nothing grows: every target is 0
+    torch.cuda.current_stream().wait_stream(side)
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for i, g in enumerate(graphs):
+        with torch.cuda.graph(g):
+            step(i)
+    hist = [[torch.zeros(0, Hkv, d, dtype=torch.float64, device="cuda")] * 2 for _ in range(B)]
+    old = [0] * B
+    for i, want in enumerate([[40, 0, 1, 33, 20], [41, 1, 2, 34, 21], [41, 80, 2, 38, 0], [45, 81, 0, 39, 60], [50, 90, 9, 0, 90]]):
+        target.copy_(_i32(want))
+        qkv.normal_()
+        outs[i % 2].fill_(5)
+        graphs[i % 2].replay()
+        assert seq.tolist() == want
+        at = 0
+        for b in range(B):
+            n = max(0, want[b] - old[b])
+            rows = slice(at, at + n)
+            at += n
+            hist[b] = [torch.cat([h, x[rows].double()])[: want[b]] for h, x in zip(hist[b], (k, v))]
+            assert pos[rows].tolist() == list(range(old[b], old[b] + n))
+            check(outs[i % 2][rows], lses[i % 2][rows], attend(q[rows], *hist[b]), torch.bfloat16, want[b], f"request {b}")
+        assert bool((outs[i % 2][at:] == 5).all()) and bool((slots[at:] == -1).all())
+        old = want
