@@ -45,7 +45,24 @@
 //    the score's, the V scale of the result's.
 // Every hand-off is an mbarrier, and every wait is bounded: on expiry a role
 // records FD_ERR_DEVICE_TIMEOUT, stops, waits for the copies it issued, and
-// the CTA frees its TMEM.
+// the CTA frees its TMEM.  A role that waits by parity waits for every phase
+// of its barrier, or one that it cannot fall two behind of.
+//
+// What bounds it, and what it measured (one GB300, device times; cuBLAS and
+// a copy reach 1889 TFLOP/s and 6794 GB/s):
+//  - long prompts and chunks at d = 128: the tensor cores; 16001 tokens of
+//    64 heads on 8, bf16: 2258 us, 1857 TFLOP/s; f16 chunks of 2048 tokens
+//    over 16K-30K keys 1797.  In a loop the power cap holds it to 0.91-0.96 of
+//    the sustained cuBLAS rate;
+//  - d = 64: the chain of a block, S, maximum, 128 exponentials a row, P.V
+//    (2475 cycles a pair of blocks): 8192 tokens of 32 heads 286 us, 962;
+//  - few new tokens over a long 16-bit cache: memory; 32 sequences of 8
+//    tokens over 4K-32K keys, 64 heads on 8: 325 us, 6590 GB/s;
+//  - E4M3 caches: shared memory, 224 KB a block of 128 keys in some 2400
+//    cycles: 16 sequences of 5 tokens 139 us, 3545 GB/s;
+//  - short and packed prompts: the ends of items.  A CTA's last block, the
+//    drain of P.V and the result take some 9000 cycles beside the next
+//    item's start: 20K tokens in 9 prompts 398 us, 1378 TFLOP/s.
 #pragma once
 
 #include "fd_extend.h"
@@ -61,8 +78,8 @@ template <typename T, int D, bool F8> struct ExtCfg {
     static constexpr int BLOCK_BYTES = PLANES * PLANE;   // K or V of one block
     static constexpr int Q_BYTES = PLANES * PLANE;       // one sub-tile
     // 16-bit K and V: 160 KB of copies in flight.  E4M3: the copies land in
-    // a ring of raw blocks, as many bytes as the 16-bit stages leave (two
-    // or four 16-bit stages are slower at long or at few queries).
+    // a ring of raw blocks of 64 KB, all that three stages of widened ones
+    // leave (two or four stages are slower at long or at few queries).
     static constexpr int STAGES = (F8 ? 3 : 5) * (128 / D);
     static constexpr int RAW_BYTES = CT * D;             // an E4M3 block
     static constexpr int RAWS = F8 ? 4 * (128 / D) : 0;

@@ -29,6 +29,7 @@ struct AppendParams {
     const void *k, *v;       // [T, H, d], token strides in elements
     long long k_stride, v_stride;
     int T, H, d, dtype;
+    int step;                // tokens side by side in a CTA
     const int32_t *slots;    // [T]
     void *k_pages, *v_pages; // [num_pages, H, page_size, d]
     int page_size;

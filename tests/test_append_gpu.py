@@ -95,6 +95,55 @@ def test_e4m3_every_value_and_ties():
     assert torch.equal(got[~nan], want[~nan])
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [0.0, -0.0, 1e-45, 2.0 ** -127, 2.0 ** -126, 1.1e-38, 2.0 ** 125, 2.0 ** 126, 3e38, math.inf,
+                                   math.nan, -0.37, 1 / 448, 0.0123, 7.0])
+def test_e4m3_is_the_quotient_rounded(dtype, scale):
+    """The byte of x / scale for any scale, over all exponents of x."""
+    g = torch.Generator().manual_seed(8)
+    k = torch.randint(-2 ** 31, 2 ** 31, (512, 4, 64), generator=g).to(torch.int32).view(torch.float32)
+    k[256:] = torch.randn(256, 4, 64, generator=g) * 100 * (abs(scale) if 0 < abs(scale) < 1e30 else 1.0)
+    k = k.to(DT[dtype])
+    want = (k.float() / torch.tensor(scale, dtype=torch.float32)).clamp(-448, 448).to(torch.float8_e4m3fn).float()
+    sc = torch.full((1, 4), scale, device="cuda")
+    kp, vp = (torch.zeros(512 // 16, 4, 16, 64, dtype=torch.float8_e4m3fn, device="cuda") for _ in range(2))
+    slots = torch.arange(512, dtype=torch.int32, device="cuda")
+    fd.append_paged_fp8(k.cuda(), k.cuda(), sc, sc, torch.tensor([0, 512], dtype=torch.int32, device="cuda"), slots, kp, vp)
+    for pool in (kp, vp):
+        got = _gather(pool, slots).view(torch.float8_e4m3fn).float().cpu()
+        nan = torch.isnan(want)
+        assert bool(torch.isnan(got[nan]).all())
+        assert torch.equal(got[~nan], want[~nan]) and torch.equal(torch.signbit(got[~nan]), torch.signbit(want[~nan]))
+
+
+@pytest.mark.parametrize("H,d", [(1, 64), (3, 64), (5, 128), (9, 128), (40, 256)])
+@pytest.mark.parametrize("T", [1, 77, 2100, 9000])
+def test_tokens_side_by_side(H, d, T):
+    """Few heads share a CTA between tokens, many take several rounds."""
+    g = torch.Generator(device="cuda").manual_seed(H)
+    k, v = (torch.randn(T, H, d, device="cuda", generator=g) for _ in range(2))
+    P = -(-T // 16)
+    slots = torch.randperm(P * 16, device="cuda", generator=g)[:T].to(torch.int32)
+    slots[::7] = -1
+    on = slots >= 0
+    lens = [T // 2, 0, T - T // 2 - T // 3, T // 3]
+    sc = [torch.rand(4, H, device="cuda", generator=g) * 0.01 + 0.005 for _ in range(2)]
+    cu = torch.tensor([0] + torch.tensor(lens).cumsum(0).tolist(), dtype=torch.int32, device="cuda")
+    for dt in (torch.float32, torch.bfloat16, torch.float8_e4m3fn):
+        src = [x.to(torch.bfloat16) if dt == torch.float8_e4m3fn else x.to(dt) for x in (k, v)]
+        pools = [torch.zeros(P, H, 16, d, dtype=torch.uint8 if dt == torch.float8_e4m3fn else dt, device="cuda") for _ in range(2)]
+        if dt == torch.float8_e4m3fn:
+            fd.append_paged_fp8(*src, *sc, cu, slots, *pools)
+            row = torch.repeat_interleave(torch.arange(4, device="cuda"), torch.tensor(lens, device="cuda"))
+            src = [(x.float() / s[row][:, :, None]).clamp(-448, 448).to(dt).view(torch.uint8) for x, s in zip(src, sc)]
+        else:
+            fd.append_paged(*src, slots, *pools)
+        for x, pool in zip(src, pools):
+            assert torch.equal(_gather(pool, slots[on]), x[on])
+            pool.view(P, H, 16, d)[slots[on].long() // 16, :, slots[on].long() % 16] = 0
+            assert not bool(pool.view(torch.uint8).any())
+
+
 def test_rows_outside_the_sequences_are_skipped():
     """E4M3: rows before cu[0] and behind cu[B] belong to nobody."""
     k = torch.randn(10, 2, 64, device="cuda").to(torch.bfloat16)
