@@ -273,3 +273,22 @@ def test_past_the_planning_tables():
     lens = [n + int(x) for n, x in zip(new, torch.randint(0, 200, (2500,), generator=g))]
     _run(new, lens, 2, 1, 64, 16, seed=11)
     _run([4200], [4300], 128, 1, 64, 64, seed=12)
+
+
+@pytest.mark.parametrize("d,dtype", [(128, "bf16"), (64, "f16")])
+@pytest.mark.parametrize("seed", [0, 1, 2])
+def test_items_of_one_block(seed, d, dtype):
+    """Few tokens over at most a block of keys, which the engines take by
+    turns, between items of several blocks and of two sub-tiles, and some
+    without any key."""
+    g = torch.Generator().manual_seed(seed)
+    new = torch.randint(0, 9, (400,), generator=g).tolist()
+    lens = [n + int(x) for n, x in zip(new, torch.randint(0, 120, (400,), generator=g))]
+    for i in range(0, 400, 23):
+        new[i], lens[i] = 150 + i, 160 + 2 * i      # two sub-tiles
+    for i in range(1, 400, 19):
+        lens[i] = 129 + 3 * i                       # several blocks of one sub-tile
+    for i in range(2, 400, 31):
+        lens[i] = new[i] // 2                       # tokens without keys
+    _run(new, lens, 6, 2, d, 16, dtype, seed=seed + 20)
+    _run8(new[:200], lens[:200], 6, 2, d, 32, dtype, seed=seed + 30)
