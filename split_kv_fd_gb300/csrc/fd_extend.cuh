@@ -258,7 +258,8 @@ template <typename T, int D, bool F8> struct ExtCta {
     __device__ __forceinline__ void init()
     {
         for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(full(s), F8 ? C::CVT_WARPS : 1);   // the producer's arrival plus the copy's bytes, or the widening warps
+            // the producer's arrival plus the copy's bytes, or the widening warps
+            mbar_init(full(s), F8 ? C::CVT_WARPS : 1);
             mbar_init(empty(s), 1);           // commit behind the block's last MMA
         }
         for (int x = 0; x < 2; ++x) {

@@ -433,10 +433,12 @@ template <int D> __global__ void __launch_bounds__(MT) extend_merge_kernel(const
             const float *y = o + 4 * e;
             if (p.out_dtype == 0)
                 *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) = make_float4(y[0], y[1], y[2], y[3]);
+            else if (p.out_dtype == 1)
+                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at) =
+                    make_uint2(Mma<__half>::pack(y[0], y[1]), Mma<__half>::pack(y[2], y[3]));
             else
                 *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at) =
-                    p.out_dtype == 1 ? make_uint2(Mma<__half>::pack(y[0], y[1]), Mma<__half>::pack(y[2], y[3]))
-                                     : make_uint2(Mma<__nv_bfloat16>::pack(y[0], y[1]), Mma<__nv_bfloat16>::pack(y[2], y[3]));
+                    make_uint2(Mma<__nv_bfloat16>::pack(y[0], y[1]), Mma<__nv_bfloat16>::pack(y[2], y[3]));
         }
         if (p.lse && lane == 0)
             p.lse[qrow] = any ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
