@@ -457,8 +457,11 @@ fd_status fd_decode_noalloc(const void *q, const void *k, const void *v, const i
  * exceed max_tokens (with slots or positions only).  Compare seqlens with
  * target to see which were given.  The result does not depend on the order
  * of threads.  A page belongs to one sequence (one that several tables name
- * would be given back several times).  A released entry that names no page, or a stack that would
- * pass num_pages, is reported as FD_ERR_BAD_PAGE by fd_device_status.
+ * would be given back several times).  Ids that name no page (in a released
+ * entry, on the stack, in the page that a sequence grows in) are replaced by
+ * -1, and the slots of new tokens in such a page are -1; that, and a stack
+ * that would pass num_pages, is reported as FD_ERR_BAD_PAGE by
+ * fd_device_status.
  * page_size*max_pages and page_size*num_pages must be below 2^31.
  */
 fd_status fd_resize_pages(int32_t *seqlens, const int32_t *target, int B, int32_t *block_table, int max_pages,

@@ -79,6 +79,17 @@ __device__ __forceinline__ Change change_of(const ResizeParams &p, int b)
     return c;
 }
 
+// A page id, or -1 (reported) where it names no page of the pool: nothing
+// else may reach the stack, the table or a slot, whose product with
+// page_size could lie in another sequence's page.
+__device__ __forceinline__ int page_or_none(const ResizeParams &p, int page, unsigned &bad)
+{
+    if (page >= 0 && page < p.num_pages)
+        return page;
+    bad |= STATUS_BAD_PAGE;
+    return -1;
+}
+
 // The pages of a chunk of sequences: thread b's are x[b] .. x[b + 1] - 1 of
 // the chunk's, its first one page `page0[b]` of its sequence.
 struct Flat {
@@ -136,8 +147,8 @@ __device__ __forceinline__ void keep_books(const ResizeParams &p)
     }
     const long long top = count0 + back;
 
-    // onto the stack, the last of them first; a page that is none is kept
-    // out of later calls by the range checks of whoever reads the table
+    // onto the stack, the last of them first; one that is no page goes there
+    // as -1, and is none again for who takes it
     long long done = 0;
     for (int b0 = 0; back > 0 && b0 < p.B; b0 += RT) {
         if (!once)
@@ -149,11 +160,12 @@ __device__ __forceinline__ void keep_books(const ResizeParams &p)
         for (int i = tid; i < total[0]; i += RT) {
             const int o = flat.owner(i), b = b0 + o;
             const long long at = top - 1 - (done + i);
-            const int page = p.table[(long long)b * p.max_pages + flat.page0[o] + (i - flat.x[o])];
-            if (page < 0 || page >= p.num_pages || at >= p.num_pages)
-                bad |= STATUS_BAD_PAGE;
+            const int page =
+                page_or_none(p, p.table[(long long)b * p.max_pages + flat.page0[o] + (i - flat.x[o])], bad);
             if (at < p.num_pages)
                 p.free_pages[at] = page;
+            else
+                bad |= STATUS_BAD_PAGE;
         }
         done += total[0];
     }
@@ -187,7 +199,7 @@ __device__ __forceinline__ void keep_books(const ResizeParams &p)
                 const int o = flat.owner(i);
                 const long long at = top - 1 - (taken + i);
                 p.table[(long long)(b0 + o) * p.max_pages + flat.page0[o] + (i - flat.x[o])] =
-                    at < p.num_pages ? p.free_pages[at] : -1;
+                    page_or_none(p, at < p.num_pages ? p.free_pages[at] : -1, bad);
             }
         }
         taken += all[0];
@@ -215,6 +227,7 @@ __global__ void __launch_bounds__(RT, 1) resize_kernel(const ResizeParams p)
     __threadfence();
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
     const int grown = p.cu[p.B];
+    unsigned bad = 0;
     for (int i = blockIdx.x * RT + threadIdx.x; i < p.max_tokens; i += gridDim.x * RT) {
         int slot = -1, pos = 0;
         if (i < grown) {
@@ -227,14 +240,16 @@ __global__ void __launch_bounds__(RT, 1) resize_kernel(const ResizeParams p)
                     hi = mid - 1;
             }
             pos = p.seqlens[lo] - (p.cu[lo + 1] - i);
-            const int page = p.table[(long long)lo * p.max_pages + pos / p.page_size];
-            slot = page < 0 ? -1 : (int)((long long)page * p.page_size + pos % p.page_size);
+            const int page = page_or_none(p, p.table[(long long)lo * p.max_pages + pos / p.page_size], bad);
+            slot = page < 0 ? -1 : page * p.page_size + pos % p.page_size;
         }
         if (p.slots)
             p.slots[i] = slot;
         if (p.positions)
             p.positions[i] = pos;
     }
+    if (bad)
+        atomicOr(p.status, bad);
 }
 
 }  // namespace
