@@ -459,8 +459,9 @@ fd_status fd_decode_noalloc(const void *q, const void *k, const void *v, const i
  * of threads.  A page belongs to one sequence (one that several tables name
  * would be given back several times).  Ids that name no page (in a released
  * entry, on the stack, in the page that a sequence grows in) are replaced by
- * -1, and the slots of new tokens in such a page are -1; that, and a stack
- * that would pass num_pages, is reported as FD_ERR_BAD_PAGE by
+ * -1, and the slots of new tokens in such a page are -1; released pages that
+ * would raise the stack past num_pages are dropped, those of the first
+ * sequences before others'.  Both are reported as FD_ERR_BAD_PAGE by
  * fd_device_status.
  * page_size*max_pages and page_size*num_pages must be below 2^31.
  */

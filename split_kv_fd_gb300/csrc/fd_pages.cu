@@ -145,10 +145,13 @@ __device__ __forceinline__ void keep_books(const ResizeParams &p)
         load(b0);
         back += total[0];
     }
-    const long long top = count0 + back;
-
-    // onto the stack, the last of them first; one that is no page goes there
-    // as -1, and is none again for who takes it
+    // Onto the stack, the last of them first; one that is no page goes there
+    // as -1, and is none again for who takes it.  What would pass the stack's
+    // end (pages given back twice) is not stored, so that the stack is what
+    // lies below `top` in any case.
+    const long long raised = count0 + back, top = min(raised, (long long)p.num_pages);
+    if (raised > top)
+        bad |= STATUS_BAD_PAGE;
     long long done = 0;
     for (int b0 = 0; back > 0 && b0 < p.B; b0 += RT) {
         if (!once)
@@ -159,13 +162,11 @@ __device__ __forceinline__ void keep_books(const ResizeParams &p)
         __syncthreads();
         for (int i = tid; i < total[0]; i += RT) {
             const int o = flat.owner(i), b = b0 + o;
-            const long long at = top - 1 - (done + i);
+            const long long at = raised - 1 - (done + i);
             const int page =
                 page_or_none(p, p.table[(long long)b * p.max_pages + flat.page0[o] + (i - flat.x[o])], bad);
-            if (at < p.num_pages)
+            if (at < top)
                 p.free_pages[at] = page;
-            else
-                bad |= STATUS_BAD_PAGE;
         }
         done += total[0];
     }
@@ -178,7 +179,7 @@ __device__ __forceinline__ void keep_books(const ResizeParams &p)
             load(b0);
         const int b = b0 + tid;
         const bool given = b < p.B && c.fits &&
-                           (own[1] == 0 || pages + sum[1] <= min(top, (long long)p.num_pages)) &&
+                           (own[1] == 0 || pages + sum[1] <= top) &&
                            (own[2] == 0 || tokens + sum[2] <= p.max_tokens);
         pages += total[1];
         tokens += total[2];
@@ -199,7 +200,7 @@ __device__ __forceinline__ void keep_books(const ResizeParams &p)
                 const int o = flat.owner(i);
                 const long long at = top - 1 - (taken + i);
                 p.table[(long long)(b0 + o) * p.max_pages + flat.page0[o] + (i - flat.x[o])] =
-                    page_or_none(p, at < p.num_pages ? p.free_pages[at] : -1, bad);
+                    page_or_none(p, p.free_pages[at], bad);
             }
         }
         taken += all[0];
@@ -208,7 +209,7 @@ __device__ __forceinline__ void keep_books(const ResizeParams &p)
     if (tid == 0) {
         if (p.cu)
             p.cu[0] = 0;
-        *p.free_count = (int)min(top - taken, (long long)p.num_pages);
+        *p.free_count = (int)(top - taken);
     }
     if (bad)
         atomicOr(p.status, bad);

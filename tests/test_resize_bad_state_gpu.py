@@ -81,3 +81,31 @@ def test_no_other_sequences_rows_are_overwritten():
     fd.append_paged(rows, rows, slots, *pages)
     assert fd.device_status() == BAD_PAGE
     assert all(bool((p == 7).all()) for p in pages)
+
+
+@pytest.mark.parametrize("B", [3, 1500])
+@pytest.mark.parametrize("extra", [1, 2])
+def test_a_stack_that_would_overflow_still_serves(B, extra):
+    """More pages come back than the pool has room for: the stack keeps its
+    num_pages entries, and growth in the same call takes real ones."""
+    seq, table = _i32([0] * B), _i32([[-1, -1]] * B)
+    seq[0] = 16 * extra
+    table[0, :extra] = _i32([3, 2][:extra])         # pages that are free already
+    free, count = _i32([0, 1, 2, 3, 4, 5, 6, 7]), _i32([8])
+    target, slots = _i32([0] * B), torch.full((20,), -9, dtype=torch.int32, device="cuda")
+    target[B - 1] = 20
+    fd.resize_pages(seq, target, table, free, count, 16, slots=slots)
+    assert fd.device_status() == BAD_PAGE
+    assert seq.tolist() == [0] * (B - 1) + [20]
+    assert table[B - 1].tolist() == [7, 6] and int(count) == 6
+    assert slots.tolist() == [7 * 16 + i for i in range(16)] + [6 * 16 + i for i in range(4)]
+    assert free.tolist() == list(range(8))
+
+
+def test_an_overflow_drops_what_passes_the_end():
+    """One place is left for the three pages of two sequences: the last one's."""
+    seq, table = _i32([32, 16, 0]), _i32([[4, 5], [6, -1], [-1, -1]])
+    free, count = _i32([0, 1, 2, 3, 7, 1, 2, -1]), _i32([7])
+    fd.resize_pages(seq, _i32([0, 0, 0]), table, free, count, 16)
+    assert fd.device_status() == BAD_PAGE
+    assert int(count) == 8 and free.tolist() == [0, 1, 2, 3, 7, 1, 2, 6]
