@@ -463,7 +463,8 @@ fd_status fd_decode_noalloc(const void *q, const void *k, const void *v, const i
  * would raise the stack past num_pages are dropped, those of the first
  * sequences before others'.  Both are reported as FD_ERR_BAD_PAGE by
  * fd_device_status.
- * page_size*max_pages and page_size*num_pages must be below 2^31.
+ * page_size*max_pages and page_size*num_pages must be below 2^31, and B at
+ * most 2^30.
  */
 fd_status fd_resize_pages(int32_t *seqlens, const int32_t *target, int B, int32_t *block_table, int max_pages,
                           int32_t *free_pages, int32_t *free_count, int num_pages, int page_size, int32_t *slots,

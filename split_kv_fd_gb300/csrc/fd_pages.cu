@@ -91,12 +91,13 @@ __device__ __forceinline__ int page_or_none(const ResizeParams &p, int page, uns
 }
 
 // The pages of a chunk of sequences: thread b's are x[b] .. x[b + 1] - 1 of
-// the chunk's, its first one page `page0[b]` of its sequence.
+// the chunk's, its first one page `page0[b]` of its sequence.  (In 64 bits:
+// lengths that name the same pages many times can pass 2^31 pages.)
 struct Flat {
-    int x[RT + 1];
+    long long x[RT];
     int page0[RT];
     // the thread whose pages i is among
-    __device__ __forceinline__ int owner(int i) const
+    __device__ __forceinline__ int owner(long long i) const
     {
         int lo = 0, hi = RT - 1;   // the last with x <= i
         while (lo < hi) {
@@ -157,16 +158,13 @@ __device__ __forceinline__ void keep_books(const ResizeParams &p)
         if (!once)
             load(b0);
         __syncthreads();   // the pages before have been written
-        flat.x[tid] = (int)(sum[0] - own[0]);
+        flat.x[tid] = sum[0] - own[0];
         flat.page0[tid] = c.pn;
         __syncthreads();
-        for (int i = tid; i < total[0]; i += RT) {
+        for (long long i = max(0LL, raised - top - done) + tid; i < total[0]; i += RT) {
             const int o = flat.owner(i), b = b0 + o;
-            const long long at = raised - 1 - (done + i);
-            const int page =
+            p.free_pages[raised - 1 - (done + i)] =
                 page_or_none(p, p.table[(long long)b * p.max_pages + flat.page0[o] + (i - flat.x[o])], bad);
-            if (at < top)
-                p.free_pages[at] = page;
         }
         done += total[0];
     }
@@ -193,7 +191,7 @@ __device__ __forceinline__ void keep_books(const ResizeParams &p)
         }
         if (all[0] > 0) {
             __syncthreads();   // the pages before have been written
-            flat.x[tid] = (int)(two[0] - mine);
+            flat.x[tid] = two[0] - mine;
             flat.page0[tid] = c.po;
             __syncthreads();
             for (int i = tid; i < all[0]; i += RT) {
@@ -229,7 +227,9 @@ __global__ void __launch_bounds__(RT, 1) resize_kernel(const ResizeParams p)
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
     const int grown = p.cu[p.B];
     unsigned bad = 0;
-    for (int i = blockIdx.x * RT + threadIdx.x; i < p.max_tokens; i += gridDim.x * RT) {
+    // (unsigned: the step behind the last of 2^31 - 1 slots passes an int)
+    for (unsigned u = blockIdx.x * RT + threadIdx.x; u < (unsigned)p.max_tokens; u += gridDim.x * RT) {
+        const int i = (int)u;
         int slot = -1, pos = 0;
         if (i < grown) {
             int lo = 0, hi = p.B - 1;   // the last b with cu[b] <= i

@@ -18,6 +18,9 @@ namespace {
 
 cudaStream_t stream_of(void *s) { return static_cast<cudaStream_t>(s); }
 
+// The kernels step through sequences by whole CTAs, in 32 bits.
+constexpr int MAX_SEQUENCES = 1 << 30;
+
 bool is16(int t) { return t == FD_F16 || t == FD_BF16; }
 
 // `rows` token rows of H*d elements, `stride` elements apart.
@@ -323,7 +326,7 @@ fd_status fd_resize_pages(int32_t *seqlens, const int32_t *target, int B, int32_
                           int32_t *free_pages, int32_t *free_count, int num_pages, int page_size, int32_t *slots,
                           int32_t *positions, int max_tokens, int32_t *cu_new, void *stream)
 {
-    if (B < 0 || max_pages < 0 || num_pages < 0 || page_size < 1 || max_tokens < 0 ||
+    if (B < 0 || B > MAX_SEQUENCES || max_pages < 0 || num_pages < 0 || page_size < 1 || max_tokens < 0 ||
         (long long)page_size * max_pages > INT_MAX || (long long)page_size * num_pages > INT_MAX)
         return FD_ERR_INVALID_ARG;
     const bool tokens = slots || positions;

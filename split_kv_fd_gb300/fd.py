@@ -23,6 +23,8 @@ STATUS_NAMES = {0: "FD_OK", 1: "FD_ERR_INVALID_ARG", 2: "FD_ERR_UNSUPPORTED",
                 3: "FD_ERR_WORKSPACE", 4: "FD_ERR_CUDA", 5: "FD_ERR_DEVICE_TIMEOUT",
                 6: "FD_ERR_SCRATCH_TOO_SMALL", 7: "FD_ERR_BAD_PAGE", 8: "FD_ERR_BAD_OFFSETS"}
 
+INT_MAX = 2 ** 31 - 1
+
 DTYPE_CODE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
 # every symbol include/fd.h declares
@@ -598,6 +600,8 @@ def _rows(t, name):
 def _int32(t, shape, name):
     if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)}")
+    if t.numel() > INT_MAX and max(shape) > INT_MAX:   # the C call's sizes are ints, and ctypes cuts what passes them
+        raise ValueError(f"{name}: sizes must be below 2^31")
 
 
 def _whole(*ts):
@@ -624,6 +628,8 @@ def resize_pages(seqlens, target, block_table, free_pages, free_count, page_size
         raise ValueError("seqlens [B], block_table [B, max_pages], free_pages [num_pages]")
     B = seqlens.shape[0]
     width, pool, room = block_table.shape[1], free_pages.shape[0], 0
+    if abs(page_size) > INT_MAX:
+        raise ValueError("page_size must be below 2^31")
     _int32(seqlens, (B,), "seqlens")
     _int32(target, (B,), "target")
     _int32(block_table, (B, width), "block_table")

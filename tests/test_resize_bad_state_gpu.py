@@ -109,3 +109,17 @@ def test_an_overflow_drops_what_passes_the_end():
     fd.resize_pages(seq, _i32([0, 0, 0]), table, free, count, 16)
     assert fd.device_status() == BAD_PAGE
     assert int(count) == 8 and free.tolist() == [0, 1, 2, 3, 7, 1, 2, 6]
+
+
+def test_releases_past_32_bits():
+    """1024 sequences that claim 2^22 pages each, 2^32 in all: the counts are
+    kept in 64 bits, and the pool of 8 takes its 8."""
+    B, width = 1024, 1 << 22
+    seq = torch.full((B,), width, dtype=torch.int32, device="cuda")
+    table = torch.zeros(B, width, dtype=torch.int32, device="cuda")
+    table[B - 1, width - 8:] = _i32(list(range(8)))
+    free, count = _i32([-1] * 8), _i32([0])
+    fd.resize_pages(seq, _i32([0] * B), table, free, count, 1)
+    assert fd.device_status() == BAD_PAGE
+    assert not bool(seq.any()) and int(count) == 8
+    assert free.tolist() == [7, 6, 5, 4, 3, 2, 1, 0]
