@@ -429,6 +429,8 @@ fd_status fd_decode_noalloc(const void *q, const void *k, const void *v, const i
  * and fd_prefill attends over packed prompts without a cache.  The new
  * tokens of all sequences are packed one behind the other, sequence b's at
  * rows cu[b] .. cu[b+1]-1 of every packed tensor (cu [B+1] int32, device).
+ * A packed tensor's token stride is a multiple of 16 bytes and a token's row
+ * at least; of a tensor of one token it may be anything.
  * ---------------------------------------------------------------------- */
 
 /*

@@ -23,8 +23,13 @@ constexpr int MAX_SEQUENCES = 1 << 30;
 
 bool is16(int t) { return t == FD_F16 || t == FD_BF16; }
 
-// `rows` token rows of H*d elements, `stride` elements apart.
-bool stride_ok(long long stride, int rows, long long row) { return rows <= 1 || stride >= row; }
+// `rows` token rows of `row` elements, `stride` elements apart, each on a
+// 16-byte boundary (16 bytes are `of` elements).  A single row's stride may
+// be anything.
+bool stride_ok(long long stride, int rows, long long row, int of)
+{
+    return rows <= 1 || (stride >= row && stride % of == 0);
+}
 
 // What prefill and extend check alike.
 fd_status check_extend(const ExtendParams &p, float scale)
@@ -35,7 +40,7 @@ fd_status check_extend(const ExtendParams &p, float scale)
     if (!is16(p.dtype) || (p.d != 64 && p.d != 128) ||
         (p.out_dtype != FD_F32 && p.out_dtype != FD_F16 && p.out_dtype != FD_BF16))
         return FD_ERR_UNSUPPORTED;
-    if (!stride_ok(p.q_stride, p.total_q, (long long)p.Hq * p.d) || p.q_stride % 8 != 0)
+    if (!stride_ok(p.q_stride, p.total_q, (long long)p.Hq * p.d, 8))
         return FD_ERR_INVALID_ARG;
     return FD_OK;
 }
@@ -157,7 +162,7 @@ fd_status run_extend(ExtendParams &p, float scale, void *workspace, size_t works
     p.part_ml = reinterpret_cast<float2 *>(ws + l.part_ml);
     p.part_o = reinterpret_cast<float *>(ws + l.part_o);
 
-    // a single row's stride may be anything
+    // (a map's strides are checked whatever its extents)
     if (p.total_q == 1)
         p.q_stride = (long long)p.Hq * p.d;
     if (p.total_k == 1)
@@ -287,8 +292,7 @@ fd_status fd_prefill(const void *q, const void *k, const void *v, const int32_t 
     fd_status st = check_extend(p, scale);
     if (st != FD_OK)
         return st;
-    if (!stride_ok(k_stride, total_k, (long long)Hkv * d) || !stride_ok(v_stride, total_k, (long long)Hkv * d) ||
-        k_stride % 8 != 0 || v_stride % 8 != 0)
+    if (!stride_ok(k_stride, total_k, (long long)Hkv * d, 8) || !stride_ok(v_stride, total_k, (long long)Hkv * d, 8))
         return FD_ERR_INVALID_ARG;
     if (B == 0 || total_q == 0 || Hq == 0)
         return FD_OK;
@@ -360,14 +364,13 @@ namespace {
 
 fd_status append(AppendParams &p, long long num_pages, void *stream)
 {
-    const int es = p.dtype == FD_F32 ? 4 : 2;
+    const int of = p.dtype == FD_F32 ? 4 : 8;   // elements of 16 bytes
     if (p.T < 0 || p.H < 0 || p.page_size < 1 || num_pages < 0 || p.d < 1 ||
         num_pages > INT_MAX / p.page_size || (long long)p.H * p.d > INT_MAX)
         return FD_ERR_INVALID_ARG;
     if ((p.dtype != FD_F32 && !is16(p.dtype)) || (p.d != 64 && p.d != 128 && p.d != 256))
         return FD_ERR_UNSUPPORTED;
-    if (!stride_ok(p.k_stride, p.T, (long long)p.H * p.d) || !stride_ok(p.v_stride, p.T, (long long)p.H * p.d) ||
-        p.k_stride * es % 16 != 0 || p.v_stride * es % 16 != 0)
+    if (!stride_ok(p.k_stride, p.T, (long long)p.H * p.d, of) || !stride_ok(p.v_stride, p.T, (long long)p.H * p.d, of))
         return FD_ERR_INVALID_ARG;
     if (p.T == 0 || p.H == 0)
         return FD_OK;
