@@ -496,7 +496,8 @@ fd_status fd_append_paged(const void *k, const void *v, const int32_t *slots, in
  * saturated at +-448 (NaN stays NaN).
  *   k_scale, v_scale  [B*Hkv] float32 (those the attention calls take)
  *   cu_new            [B+1] int32: which rows are sequence b's; B >= 1; rows
- *                     outside [cu_new[0], cu_new[B]) are skipped
+ *                     outside [cu_new[0], cu_new[B]) are skipped; B at most
+ *                     2^30
  */
 fd_status fd_append_paged_fp8(const void *k, const void *v, const float *k_scale, const float *v_scale,
                               const int32_t *cu_new, const int32_t *slots, int B, int total, int Hkv, int d,
@@ -508,6 +509,8 @@ fd_status fd_append_paged_fp8(const void *k, const void *v, const float *k_scale
  * fd_extend_paged_fp8 need for these sizes on the current device.  It needs
  * no initialisation; calls that overlap on the GPU need workspaces of their
  * own.  Returns 0 for sizes that are not supported, or on a CUDA error.
+ * Supported are d of 64 and 128, and up to 2^30 tiles of 256 (token, query
+ * head) rows, about total_q*Hq/256 + B*Hkv.
  */
 size_t fd_workspace_size_extend(int B, int total_q, int Hq, int Hkv, int d);
 
@@ -551,8 +554,9 @@ fd_status fd_prefill(const void *q, const void *k, const void *v, const int32_t 
  *   cu_q              [B+1] int32, as in fd_prefill
  *   seqlens           [B] int32, the new tokens included; clamped to [0,
  *                     max_pages*page_size]
- * page_size must be a multiple of 16 and num_pages*Hkv below 2^31.  All
- * else as in fd_prefill.
+ * page_size must be a multiple of 16, num_pages*Hkv below 2^31 and
+ * page_size*max_pages at most 2^31 - 257 (as total_q and total_k of
+ * fd_prefill).  All else as in fd_prefill.
  */
 fd_status fd_extend_paged(const void *q, const void *k_pages, const void *v_pages, const int32_t *block_table,
                           const int32_t *cu_q, const int32_t *seqlens, int B, int total_q, int Hq, int Hkv, int d,

@@ -18,8 +18,10 @@ namespace {
 
 cudaStream_t stream_of(void *s) { return static_cast<cudaStream_t>(s); }
 
-// The kernels step through sequences by whole CTAs, in 32 bits.
+// The kernels step through sequences, tiles and keys by whole CTAs and
+// blocks, in 32 bits: a step behind the last one must still fit.
 constexpr int MAX_SEQUENCES = 1 << 30;
+constexpr int MAX_TOKENS = INT_MAX - 2 * EXT_CT;
 
 bool is16(int t) { return t == FD_F16 || t == FD_BF16; }
 
@@ -34,7 +36,7 @@ bool stride_ok(long long stride, int rows, long long row, int of)
 // What prefill and extend check alike.
 fd_status check_extend(const ExtendParams &p, float scale)
 {
-    if (p.B < 0 || p.total_q < 0 || p.Hkv <= 0 || p.Hq < 0 || p.Hq % p.Hkv != 0 ||
+    if (p.B < 0 || p.total_q < 0 || p.total_q > MAX_TOKENS || p.Hkv <= 0 || p.Hq < 0 || p.Hq % p.Hkv != 0 ||
         (long long)p.B * p.Hkv > INT_MAX || !(scale > 0.f) || isinf(scale))
         return FD_ERR_INVALID_ARG;
     if (!is16(p.dtype) || (p.d != 64 && p.d != 128) ||
@@ -125,7 +127,7 @@ bool ext_layout(int B, int total_q, int Hq, int Hkv, int d, ExtLayout &l)
     l.part_ml = take((size_t)slots * 2 * EXT_M * sizeof(float2));
     l.part_o = take((size_t)slots * 2 * EXT_M * d * sizeof(float));
     l.total = at;
-    return l.max_tiles * Hkv * l.NG <= INT_MAX;
+    return l.max_tiles * Hkv * l.NG <= MAX_SEQUENCES;
 }
 
 fd_status run_extend(ExtendParams &p, float scale, void *workspace, size_t workspace_bytes, void *stream)
@@ -137,7 +139,7 @@ fd_status run_extend(ExtendParams &p, float scale, void *workspace, size_t works
         return FD_ERR_CUDA;
     ExtLayout l;
     if (!ext_layout(p.B, p.total_q, p.Hq, p.Hkv, p.d, l))
-        return FD_ERR_UNSUPPORTED;   // more tiles than a 32-bit count
+        return FD_ERR_UNSUPPORTED;   // too many tiles
     if (!workspace || workspace_bytes < l.total || !aligned(workspace, 256))
         return FD_ERR_WORKSPACE;
     p.status = status_ptr();
@@ -233,7 +235,7 @@ fd_status extend_paged(const void *q, fd_dtype q_dtype, const void *k_pages, con
     p.out = out;
     p.out_dtype = out_dtype;
     p.lse = lse;
-    if (page_size < 1 || max_pages < 0 || num_pages < 0 || (long long)page_size * max_pages > INT_MAX)
+    if (page_size < 1 || max_pages < 0 || num_pages < 0 || (long long)page_size * max_pages > MAX_TOKENS)
         return FD_ERR_INVALID_ARG;
     fd_status st = check_extend(p, scale);
     if (st != FD_OK)
@@ -287,7 +289,7 @@ fd_status fd_prefill(const void *q, const void *k, const void *v, const int32_t 
     p.out = out;
     p.out_dtype = out_dtype;
     p.lse = lse;
-    if (total_k < 0)
+    if (total_k < 0 || total_k > MAX_TOKENS)
         return FD_ERR_INVALID_ARG;
     fd_status st = check_extend(p, scale);
     if (st != FD_OK)
@@ -376,7 +378,7 @@ fd_status append(AppendParams &p, long long num_pages, void *stream)
         return FD_OK;
     if (!p.k || !p.v || !p.slots || !p.k_pages || !p.v_pages || !aligned(p.k, 16) || !aligned(p.v, 16) ||
         !aligned(p.k_pages, 16) || !aligned(p.v_pages, 16) || !aligned(p.slots, 4) ||
-        (p.f8 && (p.B < 1 || !p.cu || !p.k_scale || !p.v_scale || !aligned(p.cu, 4) || !aligned(p.k_scale, 4) ||
+        (p.f8 && (p.B < 1 || p.B > MAX_SEQUENCES || !p.cu || !p.k_scale || !p.v_scale || !aligned(p.cu, 4) || !aligned(p.k_scale, 4) ||
                   !aligned(p.v_scale, 4))))
         return FD_ERR_INVALID_ARG;
     p.num_slots = num_pages * p.page_size;

@@ -57,3 +57,25 @@ def test_several_tokens_have_one(lib, stride):
     assert lib.fd_append_paged(X, X, X, 2, 2, 128, 256, stride, 2, X, X, 16, 9, None) == INVALID
     if stride != 260:   # 1040 bytes of float32 are on the boundary
         assert lib.fd_append_paged(X, X, X, 2, 2, 128, stride, 256, 0, X, X, 16, 9, None) == INVALID
+
+
+def test_keys_are_counted_in_32_bits(lib):
+    """A block of keys behind the last one must fit an int.  (Without a
+    workspace, so that no call that passes the checks is launched.)"""
+    def extend(page, width):
+        return lib.fd_extend_paged(X, X, X, X, X, X, 2, 4, 4, 2, 128, 512, page, width, 9, 2, 0.1, X, 2, None, None, 0, None)
+
+    def prefill(tq, tk):
+        return lib.fd_prefill(X, X, X, X, X, 2, tq, tk, 4, 2, 128, 512, 256, 256, 2, 1, 0.1, X, 2, None, None, 0, None)
+
+    top = (1 << 31) - 1 - 256
+    assert extend(16, (1 << 27) - 1) == INVALID and extend(128, (1 << 24) - 1) == INVALID
+    assert extend(16, top // 16) != INVALID
+    assert prefill(4, top + 1) == INVALID and prefill(top + 1, 4) == INVALID
+    assert prefill(4, top) != INVALID
+
+
+def test_sequences_are_counted_in_32_bits(lib):
+    assert lib.fd_append_paged_fp8(X, X, X, X, X, X, (1 << 30) + 1, 2, 2, 128, 256, 256, 2, X, X, 16, 9, None) == INVALID
+    assert lib.fd_workspace_size_extend((1 << 30) + 1, 1, 1, 1, 64) == 0
+    assert lib.fd_workspace_size_extend(1 << 20, 1, 1 << 11, 1 << 11, 64) == 0
