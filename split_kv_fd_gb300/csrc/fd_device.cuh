@@ -144,7 +144,8 @@ __device__ __forceinline__ bool mbar_wait_bounded_sleep(uint32_t bar, uint32_t p
 }
 
 // The same for one thread on its own (no warp vote).
-__device__ __forceinline__ bool mbar_wait_bounded_sleep_thread(uint32_t bar, uint32_t parity, uint32_t hint_ns)
+__device__ __forceinline__ bool mbar_wait_bounded_sleep_thread(uint32_t bar, uint32_t parity, uint32_t hint_ns,
+                                                               unsigned long long limit_ns = WAIT_LIMIT_NS)
 {
     if (mbar_try_wait_hint(bar, parity, hint_ns))
         return true;
@@ -152,7 +153,7 @@ __device__ __forceinline__ bool mbar_wait_bounded_sleep_thread(uint32_t bar, uin
     for (unsigned i = 0; i < WAIT_LIMIT_POLLS; ++i) {
         if (mbar_try_wait_hint(bar, parity, hint_ns))
             return true;
-        if (global_ns() - t0 > WAIT_LIMIT_NS)
+        if (global_ns() - t0 > limit_ns)
             break;
     }
     return false;

@@ -43,10 +43,10 @@
 //    a maximum in [2^8, 2^9) by a power of two that its scores undo: exact
 //    but for elements 2^22 times smaller than that.  The K scale is part of
 //    the score's, the V scale of the result's.
-// Every hand-off is an mbarrier, and every wait is bounded: on expiry a role
-// records FD_ERR_DEVICE_TIMEOUT, stops, waits for the copies it issued, and
-// the CTA frees its TMEM.  A role that waits by parity waits for every phase
-// of its barrier, or one that it cannot fall two behind of.
+// Every hand-off is an mbarrier, and every wait is bounded (ext_wait_ns): on
+// expiry a role records FD_ERR_DEVICE_TIMEOUT, stops, waits for the copies it
+// issued, and the CTA frees its TMEM.  A role that waits by parity waits for
+// every phase of its barrier, or one that it cannot fall two behind of.
 //
 // What bounds it, and what it measured (one GB300, device times; cuBLAS and
 // a copy reach 1889 TFLOP/s and 6794 GB/s):
@@ -227,6 +227,7 @@ template <int R> __device__ __forceinline__ void regs_dec() { asm volatile("setm
 // The CTA's shared memory, and a segment ring cursor per warp.
 template <typename T, int D, bool F8> struct ExtCta {
     using C = ExtCfg<T, D, F8>;
+    const ExtendParams &p;
     uint32_t ring, raw, qbuf, bar0;
     volatile ExtSeg *segs;
     volatile float *xch;    // [2][M] pairs
@@ -234,6 +235,8 @@ template <typename T, int D, bool F8> struct ExtCta {
     int lane;
     int sg = 0;             // segments taken so far
     bool dead = false;
+
+    __device__ __forceinline__ explicit ExtCta(const ExtendParams &params) : p(params) {}
 
     __device__ __forceinline__ uint32_t bar(int i) const { return bar0 + 8u * (uint32_t)i; }
     __device__ __forceinline__ uint32_t full(int s) const { return bar(s); }
@@ -286,7 +289,7 @@ template <typename T, int D, bool F8> struct ExtCta {
     // Wait of a whole warp for the n-th (from 0) completion of a barrier.
     __device__ __forceinline__ bool wait(uint32_t b, int n)
     {
-        if (!dead && !mbar_wait_bounded_soon(b, (uint32_t)(n & 1), C::SLEEP_NS))
+        if (!dead && !mbar_wait_bounded_soon(b, (uint32_t)(n & 1), C::SLEEP_NS, p.wait_ns))
             dead = true;
         return !dead;
     }
@@ -340,7 +343,8 @@ __device__ __forceinline__ void ext_schedule(const ExtendParams &p, ExtCta<T, D,
     auto push = [&](int it, const ExtTile &t, int blk0, int blk1, int slot) {
         const int s = sg % C::SEGS;
         if (sg >= C::SEGS &&
-            !mbar_wait_bounded_sleep_thread(cta.g_empty(s), (uint32_t)(((sg / C::SEGS) - 1) & 1), C::SLEEP_NS)) {
+            !mbar_wait_bounded_sleep_thread(cta.g_empty(s), (uint32_t)(((sg / C::SEGS) - 1) & 1), C::SLEEP_NS,
+                                            p.wait_ns)) {
             cta.dead = true;
             return;
         }
@@ -477,7 +481,7 @@ __device__ __forceinline__ void ext_load_kv(const ExtendParams &p, ExtCta<T, D, 
     for (int i = 0; i < NS; ++i) {
         const int n = i < slot ? lap : lap - 1;   // its last lap
         if (n >= 0)
-            mbar_wait_bounded_soon(F8 ? cta.r_full(i) : cta.full(i), (uint32_t)(n & 1), C::SLEEP_NS);
+            mbar_wait_bounded_soon(F8 ? cta.r_full(i) : cta.full(i), (uint32_t)(n & 1), C::SLEEP_NS, p.wait_ns);
     }
 }
 
@@ -509,7 +513,7 @@ __device__ __forceinline__ void ext_load_q(const ExtendParams &p, ExtCta<T, D, F
     }
     for (int x = 0; x < 2; ++x)
         if (n[x] > 0)
-            mbar_wait_bounded_soon(cta.q_full(x), (uint32_t)((n[x] - 1) & 1), C::SLEEP_NS);
+            mbar_wait_bounded_soon(cta.q_full(x), (uint32_t)((n[x] - 1) & 1), C::SLEEP_NS, p.wait_ns);
 }
 
 // ---------------------------------------------------------------- E4M3 to f16
@@ -816,7 +820,7 @@ __device__ __forceinline__ void ext_mma(const ExtendParams &p, ExtCta<T, D, F8> 
     // every MMA issued here has completed before TMEM is freed
     __syncwarp();
     tc_commit_if(one, cta.fin());
-    if (!mbar_wait_bounded_soon(cta.fin(), 0, C::SLEEP_NS))
+    if (!mbar_wait_bounded_soon(cta.fin(), 0, C::SLEEP_NS, p.wait_ns))
         cta.dead = true;
 }
 
@@ -1050,7 +1054,7 @@ __global__ void __launch_bounds__(ExtCfg<T, D, F8>::THREADS, 1) extend_kernel(co
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the merge waits for this grid's end
     extern __shared__ __align__(1024) unsigned char smem[];           // the swizzle's atoms are 1024 bytes
     const int w = threadIdx.x >> 5;
-    ExtCta<T, D, F8> cta;
+    ExtCta<T, D, F8> cta(p);
     cta.lane = threadIdx.x & 31;
     cta.ring = smem_addr(smem);
     cta.raw = cta.ring + C::STAGES * C::BLOCK_BYTES;

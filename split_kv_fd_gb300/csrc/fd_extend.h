@@ -87,6 +87,7 @@ struct ExtendParams {
     unsigned *status;
     // workspace
     int grid, max_tiles;
+    unsigned long long wait_ns;   // after which a wait is given up
     ExtPlanHeader *header;
     int *tile_start;         // [B] tiles before each sequence
     int *tile_blk;           // [max_tiles] blocks of the sorted tiles
@@ -97,6 +98,19 @@ struct ExtendParams {
     float *part_o;           // [slots][2 * EXT_M][d] sums of weights times V
     float2 *part_ml;         // [slots][2 * EXT_M] (reference max, sum of weights)
 };
+
+// How long a wait of the main kernel may last: 1 s, and what a role may
+// rightly wait for.  That is the plan, which deals with a tile in some 0.04
+// us (12 M sequences of a token: 0.46 s with the attention), and another
+// role's whole segment (the next load of Q waits for the last block of the
+// segment before), whose blocks take 1.1 to 1.5 us each; both several times
+// over, for other work on the GPU.  1 s alone would end calls over some 85 M
+// keys a sequence.
+inline unsigned long long ext_wait_ns(long long max_tiles, long long max_keys)
+{
+    return 1000000000ull + 1000ull * (unsigned long long)max_tiles +
+           10000ull * (unsigned long long)(max_keys / EXT_CT);
+}
 
 // Partial results: the piece that ends at a cut and the one that starts there.
 inline int ext_slots(int grid) { return 2 * (grid + 1); }

@@ -11,7 +11,8 @@ namespace fd {
 // Bounded wait by a whole warp for a phase that is often complete already:
 // one try first, and the clock is read only when that fails (a read of
 // %globaltimer costs about as much as a short wait).
-__device__ __forceinline__ bool mbar_wait_bounded_soon(uint32_t bar, uint32_t parity, uint32_t hint_ns)
+__device__ __forceinline__ bool mbar_wait_bounded_soon(uint32_t bar, uint32_t parity, uint32_t hint_ns,
+                                                       const unsigned long long &limit_ns)
 {
     bool ok = mbar_try_wait(bar, parity);
     if (!ok) {
@@ -21,7 +22,7 @@ __device__ __forceinline__ bool mbar_wait_bounded_soon(uint32_t bar, uint32_t pa
                 ok = true;
                 break;
             }
-            if (global_ns() - t0 > WAIT_LIMIT_NS)
+            if (global_ns() - t0 > limit_ns)
                 break;
         }
     }

@@ -153,6 +153,7 @@ fd_status run_extend(ExtendParams &p, float scale, void *workspace, size_t works
     p.tps = l.tps;
     p.grid = l.grid;
     p.max_tiles = (int)l.max_tiles;
+    p.wait_ns = ext_wait_ns(l.max_tiles, p.paged ? (long long)p.page_size * p.max_pages : p.total_k);
     char *ws = static_cast<char *>(workspace);
     p.header = reinterpret_cast<ExtPlanHeader *>(ws + l.header);
     p.tile_start = reinterpret_cast<int *>(ws + l.tile_start);
