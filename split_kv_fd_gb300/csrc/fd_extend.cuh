@@ -140,9 +140,7 @@ __device__ __forceinline__ int ext_blocks(const ExtSeg &g) { return max(g.end0, 
 struct ExtOrder {
     bool ahead;
     int n;
-    __device__ __forceinline__ int k_at(int i) const { return ahead && i ? 2 * i - 1 : 2 * i; }
-    __device__ __forceinline__ int v_at(int i) const { return ahead && i < n - 1 ? 2 * i + 2 : 2 * i + 1; }
-    // The other way round: item t of 2n is V (or K) of block i.
+    // Item t of 2n is V (or K) of block i.
     __device__ __forceinline__ bool item(int t, int &i) const
     {
         if (!ahead || t == 0 || t == 2 * n - 1) {
