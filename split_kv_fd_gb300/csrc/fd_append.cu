@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(AT) append_kernel(const AppendParams p)
                 continue;
             const long long row = ((long long)(slot[u] / p.page_size) * p.H + h) * p.page_size + slot[u] % p.page_size;
             char *to = pages + (row * p.d + e) * (F8 ? 1 : (int)sizeof(T));
-            if (F8) {
+            if constexpr (F8) {
                 float f[EL];
 #pragma unroll
                 for (int k = 0; k < SRC; ++k)
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(AT) append_kernel(const AppendParams p)
                         w[k] = e4m3x4(__fdiv_rn(f[4 * k], sc[u]), __fdiv_rn(f[4 * k + 1], sc[u]),
                                       __fdiv_rn(f[4 * k + 2], sc[u]), __fdiv_rn(f[4 * k + 3], sc[u]));
                 }
-                *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[EL / 4 - 2], w[EL / 4 - 1]);
+                *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[2], w[3]);
             } else {
                 *reinterpret_cast<uint4 *>(to) = x[u][0];
             }
