@@ -568,9 +568,9 @@ fd_status fd_extend_paged(const void *q, const void *k_pages, const void *v_page
  * fd_extend_paged over E4M3 pages with the scales of fd_decode_gqa_paged_fp8
  * (k_scale, v_scale [B*Hkv] float32); q_dtype f16 or bf16.  Both products
  * are of float16 operands (an E4M3 value is one exactly): the weights are
- * rounded to float16, and a bf16 query row is scaled by a power of two to a
- * largest magnitude of 2^8, which keeps its values down to 2^-22 of that
- * exact.
+ * rounded to float16, and a bf16 query row is scaled by a power of two (2^120
+ * at most) to a largest magnitude in [2^8, 2^9), which keeps its values down
+ * to 2^-22 of that exact.  A K scale may be zero or negative.
  */
 fd_status fd_extend_paged_fp8(const void *q, fd_dtype q_dtype, const void *k_pages, const void *v_pages,
                               const float *k_scale, const float *v_scale, const int32_t *block_table,
