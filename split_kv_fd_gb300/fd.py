@@ -707,10 +707,21 @@ def workspace_size_extend(B, total_q, Hq, Hkv, d) -> int:
 
 
 @functools.lru_cache(maxsize=1024)
-def _extend_bytes(dev, *sizes):
-    """workspace_size_extend on a device, which depends on nothing else."""
+def _known_extend_bytes(dev, *sizes):
     with torch.cuda.device(dev):
-        return max(workspace_size_extend(*sizes), 256)
+        n = workspace_size_extend(*sizes)
+    if n == 0:   # an exception is not remembered: a CUDA error may be over by the next call
+        raise LookupError
+    return n
+
+
+def _extend_bytes(dev, *sizes):
+    """workspace_size_extend on a device, which depends on nothing else; some
+    bytes where it gives none, so that the call itself says why."""
+    try:
+        return _known_extend_bytes(dev, *sizes)
+    except LookupError:
+        return 256
 
 
 def _extend_out(dev, q, B, Hkv, out_dtype, out, lse, return_lse, workspace, stream):

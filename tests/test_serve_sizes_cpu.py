@@ -1,6 +1,7 @@
 """Sizes at the ends of 32 bits in the calls around decode, without a GPU:
 refused where an index could not hold them, by the library and by the
 binding."""
+import contextlib
 import ctypes
 
 import pytest
@@ -79,3 +80,17 @@ def test_sequences_are_counted_in_32_bits(lib):
     assert lib.fd_append_paged_fp8(X, X, X, X, X, X, (1 << 30) + 1, 2, 2, 128, 256, 256, 2, X, X, 16, 9, None) == INVALID
     assert lib.fd_workspace_size_extend((1 << 30) + 1, 1, 1, 1, 64) == 0
     assert lib.fd_workspace_size_extend(1 << 20, 1, 1 << 11, 1 << 11, 64) == 0
+
+
+def test_a_failed_workspace_query_is_not_remembered(monkeypatch):
+    """The query gives 0 on a CUDA error, or where the library has no such sizes."""
+    answers = iter([0, 0, 4096, 8192])
+    monkeypatch.setattr(fdmod, "workspace_size_extend", lambda *sizes: next(answers))
+    monkeypatch.setattr(torch.cuda, "device", lambda dev: contextlib.nullcontext())
+    sizes = (0, 7, 7, 7, 7, 64)
+    try:
+        assert [fdmod._extend_bytes(*sizes) for _ in range(4)] == [256, 256, 4096, 4096]
+    finally:
+        for f in vars(fdmod).values():     # nothing made up stays for later calls
+            if hasattr(f, "cache_clear"):
+                f.cache_clear()
