@@ -532,7 +532,10 @@ size_t fd_workspace_size_extend(int B, int total_q, int Hq, int Hkv, int d);
  *   workspace    fd_workspace_size_extend(...) bytes, 256-byte aligned
  * d must be 64 or 128; any Hq / Hkv.  A query that sees no key gives out = 0
  * and lse = -inf.  The scores are float32; the weights exp(s - m) are
- * rounded to in_dtype for the product with V, which is summed in float32.
+ * rounded to in_dtype for the product with V, which is summed in float32: by
+ * the tensor cores over at most 64 K keys (they cut a product at the last
+ * bits of the running sum, some 6e-9 of it a key), and rounded to nearest
+ * beyond.
  * Keys that a query does not see do not touch it, whatever K holds there; a
  * V row that is not finite reaches every query of its sequence whose tile
  * of 128 keys holds it, seen or not.  Rows behind a sequence's keys, or of

@@ -22,6 +22,9 @@
 // takes every other block and the two results are joined at the end, so
 // that the time of a block is half that of the chain S, softmax, P.V.
 //
+// Sums over more than EXT_LINK blocks are taken in links, each a segment of
+// its own, joined in the CTA's two slots of the workspace (ext_join).
+//
 // P lies in the columns of its S, and S of an engine's next block follows
 // P.V of the one before, so S's commit also says that P.V is done.  (At
 // d = 64 there is room for P beside S; with S of the next block issued as
@@ -127,9 +130,16 @@ struct ExtSeg {
     int h, slice, b;
     int m, lim, k0;
     int blk0, end0, end1;   // blocks [blk0, end x) of sub-tile x
-    int twin;            // one sub-tile, its blocks dealt to both engines
+    int flags;           // see below
     int slot;            // partial result, or -1: the whole item
     __device__ __forceinline__ int end(int x) const { return x ? end1 : end0; }
+    // one sub-tile, its blocks dealt to both engines
+    __device__ __forceinline__ bool twin() const { return flags & 1; }
+    // a link of a chain (the first, one between, the last), or none of one
+    enum { ALONE, FIRST, INNER, LAST };
+    __device__ __forceinline__ int link() const { return (flags >> 1) & 3; }
+    // where the chain's result goes, as `slot`
+    __device__ __forceinline__ int target() const { return flags >> 3; }
 };
 
 __device__ __forceinline__ int ext_blocks(const ExtSeg &g) { return max(g.end0, g.end1) - g.blk0; }
@@ -318,7 +328,7 @@ template <typename T, int D, bool F8> struct ExtCta {
         g.blk0 = x.blk0;
         g.end0 = x.end0;
         g.end1 = x.end1;
-        g.twin = x.twin;
+        g.flags = x.flags;
         g.slot = x.slot;
         arrive(g_empty(s));
         ++sg;
@@ -338,7 +348,7 @@ __device__ __forceinline__ void ext_schedule(const ExtendParams &p, ExtCta<T, D,
     const ExtCut a = p.cuts[c], e = p.cuts[c + 1];
     int sg = 0;
     // a segment of item `it`, blocks [blk0, blk1)
-    auto push = [&](int it, const ExtTile &t, int blk0, int blk1, int slot) {
+    auto push = [&](int it, const ExtTile &t, int blk0, int blk1, int slot, int link, int target) {
         const int s = sg % C::SEGS;
         if (sg >= C::SEGS &&
             !mbar_wait_bounded_sleep_thread(cta.g_empty(s), (uint32_t)(((sg / C::SEGS) - 1) & 1), C::SLEEP_NS,
@@ -365,10 +375,26 @@ __device__ __forceinline__ void ext_schedule(const ExtendParams &p, ExtCta<T, D,
             const int end = see > 0 ? (see + C::CT - 1) / C::CT : 0;
             (x ? g.end1 : g.end0) = max(blk0, min(blk1, end));
         }
-        g.twin = t.ntok <= p.tps && blk1 - blk0 > 1;
+        g.flags = (t.ntok <= p.tps && blk1 - blk0 > 1 ? 1 : 0) | link << 1 | target * 8;
         g.slot = slot;
         mbar_arrive(cta.g_full(s));
         ++sg;
+    };
+    // the same, as a chain where the range is long: links of like lengths (so
+    // all of them are twins or none is), the first one's result in the CTA's
+    // first slot, the others' in its second
+    auto pieces = [&](int it, const ExtTile &t, int blk0, int blk1, int slot) {
+        const int n = blk1 - blk0;
+        if (n <= EXT_LINK) {
+            push(it, t, blk0, blk1, slot, ExtSeg::ALONE, 0);
+            return;
+        }
+        const int links = (n + EXT_LINK - 1) / EXT_LINK, own = 2 * (G + 1) + 2 * c;
+        for (int k = 0, b = blk0; k < links && !cta.dead; ++k) {
+            const int e = b + (blk1 - b + links - k - 1) / (links - k);
+            push(it, t, b, e, k ? own + 1 : own, k == 0 ? ExtSeg::FIRST : k + 1 < links ? ExtSeg::INNER : ExtSeg::LAST, slot);
+            b = e;
+        }
     };
     for (int it = a.item; it < hd.n_items && !cta.dead; ++it) {
         const bool last = it == e.item;
@@ -380,16 +406,16 @@ __device__ __forceinline__ void ext_schedule(const ExtendParams &p, ExtCta<T, D,
         if (t.nblk == 0 ? !fresh : b1 <= b0)
             continue;
         const bool whole = b0 == 0 && b1 == t.nblk;
-        push(it, t, b0, b1, whole ? -1 : b0 > 0 ? 2 * c + 1 : 2 * (c + 1));
+        pieces(it, t, b0, b1, whole ? -1 : b0 > 0 ? 2 * c + 1 : 2 * (c + 1));
     }
     for (int x = 0; x < hd.waves && !cta.dead; ++x) {
         const int it = x * G + ((x & 1) ? G - 1 - c : c);
         const ExtTile t = p.tiles[it / Hv];
-        push(it, t, 0, t.nblk, -1);
+        pieces(it, t, 0, t.nblk, -1);
     }
     if (!cta.dead) {
         const ExtTile none = {};
-        push(-1, none, 0, 0, -1);
+        push(-1, none, 0, 0, -1, ExtSeg::ALONE, 0);
     }
 }
 
@@ -416,7 +442,7 @@ __device__ __forceinline__ void ext_load_kv(const ExtendParams &p, ExtCta<T, D, 
     ExtSeg g;
     while (cta.next(g)) {
         const int nb = ext_blocks(g);
-        const ExtOrder order = {g.twin != 0, nb};
+        const ExtOrder order = {g.twin(), nb};
         int tok = g.blk0 * C::CT + grp * R;   // this lane's first row of the next K
         int pidx = tok / ps, row = tok % ps;
         const int32_t *table = p.table + (long long)g.b * p.max_pages;
@@ -575,7 +601,7 @@ __device__ __forceinline__ void ext_widen(const ExtendParams &p, ExtCta<T, D, F8
             cta.arrive(cta.q_wide(x));
             ++nq[x];
         }
-        const ExtOrder order = {g.twin != 0, nb};
+        const ExtOrder order = {g.twin(), nb};
         for (int t = 0; t < 2 * nb && !cta.dead; ++t) {
             int i;
             order.item(t, i);
@@ -696,7 +722,7 @@ __device__ __forceinline__ void ext_mma(const ExtendParams &p, ExtCta<T, D, F8> 
         const int nb = ext_blocks(g);
         if (nb == 0)
             continue;
-        const bool twin = g.twin != 0;
+        const bool twin = g.twin();
         // engine x's blocks: its own sub-tile's, or every other one
         const int ahead = twin ? 2 : 1;   // S runs so many blocks ahead of P.V
         const int len0 = twin ? nb : g.end0 - g.blk0, len1 = twin ? nb : g.end1 - g.blk0;
@@ -822,6 +848,81 @@ __device__ __forceinline__ void ext_mma(const ExtendParams &p, ExtCta<T, D, F8> 
         cta.dead = true;
 }
 
+// ---------------------------------------------------------------- chains
+// A thread's row (columns [c0, c1) of it) of a link whose result stands in the
+// CTA's slots, with the reference m and the sum l: the first link's is kept,
+// the others' is joined with what stands there, and the last one's written
+// where the chain's goes.  A thread reads only what it wrote itself (the
+// engines of a twin keep a copy of (m, l) each).
+template <typename T, int D, bool F8>
+__device__ __forceinline__ void ext_join(const ExtendParams &p, const ExtSeg &g, int x, int sub, int row,
+                                         long long qrow, int c0, int c1, float m, float l, float vscale)
+{
+    using C = ExtCfg<T, D, F8>;
+    const long long own = 2 * ((long long)p.grid + 1 + blockIdx.x);   // the CTA's first slot
+    float2 *ml = p.part_ml + (own * 2 + x) * C::M + row;
+    if (g.link() == ExtSeg::FIRST) {
+        *ml = make_float2(m, l);
+        return;
+    }
+    float *before = p.part_o + ((own * 2 + sub) * C::M + row) * D;
+    const float *now = before + 2LL * C::M * D;
+    const float2 b = *ml;
+    const float top = fmaxf(b.x, m);
+    float fb = b.x == -INFINITY ? 0.f : ex2(b.x - top), fn = m == -INFINITY ? 0.f : ex2(m - top);
+    l = fb * b.y + fn * l;
+    const bool any = !(l <= 0.f);       // NaN counts: it is the result then
+    m = any ? top : -INFINITY;
+    const bool last = g.link() == ExtSeg::LAST;
+    const int target = g.target();
+    const bool result = last && target < 0;
+    if (result) {
+        const float inv = any ? vscale / l : 0.f;
+        fb *= inv;
+        fn *= inv;
+    }
+    const long long to = last && target >= 0 ? ((long long)target * 2 + sub) * C::M + row : (own * 2 + sub) * C::M + row;
+    // (8 columns at a time: unrolled further, the code that most calls do not
+    // run cost prompts of a link or less up to 2%)
+#pragma unroll 1
+    for (int c = c0; c < c1; c += 8) {
+        float4 u[2], v[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            u[i] = *reinterpret_cast<const float4 *>(before + c + 4 * i);
+            v[i] = *reinterpret_cast<const float4 *>(now + c + 4 * i);
+        }
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            // (an empty row is 0)
+            o[4 * i] = any ? fmaf(u[i].x, fb, v[i].x * fn) : 0.f;
+            o[4 * i + 1] = any ? fmaf(u[i].y, fb, v[i].y * fn) : 0.f;
+            o[4 * i + 2] = any ? fmaf(u[i].z, fb, v[i].z * fn) : 0.f;
+            o[4 * i + 3] = any ? fmaf(u[i].w, fb, v[i].w * fn) : 0.f;
+        }
+        const long long at = (result ? qrow : to) * D + c;
+        if (!result || p.out_dtype == 0) {
+            float4 *w = reinterpret_cast<float4 *>((result ? static_cast<float *>(p.out) : p.part_o) + at);
+            w[0] = make_float4(o[0], o[1], o[2], o[3]);
+            w[1] = make_float4(o[4], o[5], o[6], o[7]);
+        } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = p.out_dtype == 1 ? Mma<__half>::pack(o[2 * i], o[2 * i + 1])
+                                        : Mma<__nv_bfloat16>::pack(o[2 * i], o[2 * i + 1]);
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+    if (!last)
+        *ml = make_float2(m, l);
+    else if (c0 == 0 && !result)
+        p.part_ml[to] = make_float2(m, l);
+    else if (c0 == 0 && p.lse)
+        p.lse[qrow] = any ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
 // ---------------------------------------------------------------- softmax
 template <typename T, int D, bool F8>
 __device__ __forceinline__ void ext_softmax(const ExtendParams &p, ExtCta<T, D, F8> &cta, uint32_t tmem)
@@ -836,7 +937,7 @@ __device__ __forceinline__ void ext_softmax(const ExtendParams &p, ExtCta<T, D, 
     int nq0 = 0, nq1 = 0;   // E4M3: loads of each sub-tile's Q
     ExtSeg g;
     while (cta.next(g)) {
-        const bool twin = g.twin != 0;
+        const bool twin = g.twin();
         const int sub = twin ? 0 : x;          // whose rows
         const int tok = sub * p.tps + rtok;    // token within the tile
         const int gv = min(p.Gs, p.G - g.slice * p.Gs);
@@ -1042,6 +1143,8 @@ __device__ __forceinline__ void ext_softmax(const ExtendParams &p, ExtCta<T, D, 
             if (!cta.wait(cta.meet(), meets++))
                 break;
         }
+        if (g.link() != ExtSeg::ALONE && live)
+            ext_join<T, D, F8>(p, g, x, sub, row, qrow, c0, c1, any ? M - C::SHIFT : -INFINITY, L, vscale);
     }
 }
 

@@ -18,6 +18,14 @@ constexpr unsigned STATUS_BAD_OFFSETS = 4u;
 constexpr int EXT_M = 128;
 // Keys per block.
 constexpr int EXT_CT = 128;
+// Blocks of a link: longer ranges are taken as a chain of segments, each with
+// sums of its own, joined in float32.  The tensor cores add a product to the
+// running sum cut at that sum's last bits, so values of one sign come out low
+// by some 6.3e-9 a key (measured, f16 and bf16): 4e-4 at a link's 64 K keys,
+// below f16's half step, but 6.6e-3 at a million.  A link's end costs some 16
+// us beside its 600 (2048 tokens of 64 heads over 128 K keys, three links a
+// tile: 5.26 -> 5.48 ms; links of 256 blocks 5.59).
+constexpr int EXT_LINK = 512;
 // CTAs of the main kernel at most: the plan deals with a thread for each.
 constexpr int EXT_MAX_GRID = 255;
 // Boxes of a paged K/V block: at most EXT_CT / 16 row groups.
@@ -112,8 +120,10 @@ inline unsigned long long ext_wait_ns(long long max_tiles, long long max_keys)
            10000ull * (unsigned long long)(max_keys / EXT_CT);
 }
 
-// Partial results: the piece that ends at a cut and the one that starts there.
-inline int ext_slots(int grid) { return 2 * (grid + 1); }
+// Partial results: the piece that ends at a cut and the one that starts
+// there, and two for each CTA: what the links of a chain have given so far,
+// and what its present link gives.
+inline int ext_slots(int grid) { return 2 * (grid + 1) + 2 * grid; }
 
 cudaError_t launch_extend_plan(const ExtendParams &p, cudaStream_t s);
 cudaError_t launch_extend_bf16(const ExtendParams &p, cudaStream_t s);
