@@ -17,6 +17,8 @@
 #include "fd_device.cuh"
 #include "fd_pages.h"
 
+#include <limits.h>
+
 namespace fd {
 namespace {
 
@@ -91,13 +93,13 @@ __device__ __forceinline__ int page_or_none(const ResizeParams &p, int page, uns
 }
 
 // The pages of a chunk of sequences: thread b's are x[b] .. x[b + 1] - 1 of
-// the chunk's, its first one page `page0[b]` of its sequence.  (In 64 bits:
-// lengths that name the same pages many times can pass 2^31 pages.)
+// the chunk's (counted from those that are dropped), its first one page
+// `page0[b]` of its sequence.
 struct Flat {
-    long long x[RT];
+    int x[RT];
     int page0[RT];
     // the thread whose pages i is among
-    __device__ __forceinline__ int owner(long long i) const
+    __device__ __forceinline__ int owner(int i) const
     {
         int lo = 0, hi = RT - 1;   // the last with x <= i
         while (lo < hi) {
@@ -158,12 +160,18 @@ __device__ __forceinline__ void keep_books(const ResizeParams &p)
         if (!once)
             load(b0);
         __syncthreads();   // the pages before have been written
-        flat.x[tid] = sum[0] - own[0];
+        // Lengths that name the same pages many times can pass 2^31 pages, but
+        // those behind the dropped ones are num_pages at most, and a thread's
+        // own fit an int: only the places of threads that own none of the
+        // former are clamped.
+        const long long skip = max(0LL, raised - top - done);
+        flat.x[tid] = (int)min(max(sum[0] - own[0] - skip, (long long)INT_MIN), (long long)INT_MAX);
         flat.page0[tid] = c.pn;
         __syncthreads();
-        for (long long i = max(0LL, raised - top - done) + tid; i < total[0]; i += RT) {
-            const int o = flat.owner(i), b = b0 + o;
-            p.free_pages[raised - 1 - (done + i)] =
+        const unsigned kept = (unsigned)max(0LL, total[0] - skip);
+        for (unsigned u = tid; u < kept; u += RT) {
+            const int i = (int)u, o = flat.owner(i), b = b0 + o;
+            p.free_pages[raised - 1 - (done + skip + i)] =
                 page_or_none(p, p.table[(long long)b * p.max_pages + flat.page0[o] + (i - flat.x[o])], bad);
         }
         done += total[0];
@@ -191,11 +199,11 @@ __device__ __forceinline__ void keep_books(const ResizeParams &p)
         }
         if (all[0] > 0) {
             __syncthreads();   // the pages before have been written
-            flat.x[tid] = two[0] - mine;
+            flat.x[tid] = (int)(two[0] - mine);
             flat.page0[tid] = c.po;
             __syncthreads();
-            for (int i = tid; i < all[0]; i += RT) {
-                const int o = flat.owner(i);
+            for (unsigned u = tid; u < (unsigned)all[0]; u += RT) {
+                const int i = (int)u, o = flat.owner(i);
                 const long long at = top - 1 - (taken + i);
                 p.table[(long long)(b0 + o) * p.max_pages + flat.page0[o] + (i - flat.x[o])] =
                     page_or_none(p, p.free_pages[at], bad);
