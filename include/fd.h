@@ -456,13 +456,15 @@ fd_status fd_decode_noalloc(const void *q, const void *k, const void *v, const i
  * target passes max_pages pages keeps its length and needs nothing; one
  * that needs pages keeps its length when the needs of all up to it exceed
  * what is free, and one that has new tokens when those of all up to it
- * exceed max_tokens (with slots or positions only).  Compare seqlens with
- * target to see which were given.  The result does not depend on the order
- * of threads.  A page belongs to one sequence (one that several tables name
- * would be given back several times).  Ids that name no page (in a released
- * entry, on the stack, in the page that a sequence grows in) are replaced by
- * -1, and the slots of new tokens in such a page are -1; released pages that
- * would raise the stack past num_pages are dropped, those of the first
+ * exceed max_tokens (with slots or positions only).  So a request that is too
+ * large holds back those behind it that need pages in the same call, although
+ * pages for them are free: put running sequences ahead of admissions, or
+ * admit in a call of its own.  Compare seqlens with target to see which were
+ * given.  The result does not depend on the order of threads.  A page belongs
+ * to one sequence (one that several tables name would be given back several
+ * times).  Ids that name no page are stored as -1 where they are released or
+ * taken, and the slots of new tokens in such a page are -1; released pages
+ * that would raise the stack past num_pages are dropped, those of the first
  * sequences before others'.  Both are reported as FD_ERR_BAD_PAGE by
  * fd_device_status.
  * page_size*max_pages and page_size*num_pages must be below 2^31, and B at
@@ -535,7 +537,10 @@ size_t fd_workspace_size_extend(int B, int total_q, int Hq, int Hkv, int d);
  * rounded to in_dtype for the product with V, which is summed in float32: by
  * the tensor cores over at most 64 K keys (they cut a product at the last
  * bits of the running sum, some 6e-9 of it a key), and rounded to nearest
- * beyond.
+ * beyond.  (The grouped-query decode calls take the weights in two 16-bit
+ * parts, close to float32; one part is off by half a step of in_dtype at most,
+ * 2^-8 of a weight for bf16 and 2^-11 for f16.  A token that must have
+ * decode's accuracy goes through decode.)
  * Keys that a query does not see do not touch it, whatever K holds there; a
  * V row that is not finite reaches every query of its sequence whose tile
  * of 128 keys holds it, seen or not.  Rows behind a sequence's keys, or of

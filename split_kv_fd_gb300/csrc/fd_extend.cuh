@@ -54,18 +54,20 @@
 // What bounds it, and what it measured (one GB300, device times; cuBLAS and
 // a copy reach 1889 TFLOP/s and 6794 GB/s):
 //  - long prompts and chunks at d = 128: the tensor cores; 16001 tokens of
-//    64 heads on 8, bf16: 2258 us, 1857 TFLOP/s; f16 chunks of 2048 tokens
-//    over 16K-30K keys 1797.  In a loop the power cap holds it to 0.91-0.96 of
-//    the sustained cuBLAS rate;
+//    64 heads on 8, bf16: 2236-2270 us, 1850-1880 TFLOP/s; f16 chunks of 2048
+//    tokens over 16K-30K keys 1790-1840.  In a loop the power cap holds it to
+//    1640 and 1560, 0.97 and 0.92 of the sustained cuBLAS rate;
 //  - d = 64: the chain of a block, S, maximum, 128 exponentials a row, P.V
-//    (2475 cycles a pair of blocks): 8192 tokens of 32 heads 286 us, 962;
+//    (2475 cycles a pair of blocks): 8192 tokens of 32 heads 281-286 us,
+//    962-978; over an E4M3 cache 773 (2 x 2048 tokens over 4096);
 //  - few new tokens over a long 16-bit cache: memory; 32 sequences of 8
-//    tokens over 4K-32K keys, 64 heads on 8: 325 us, 6590 GB/s;
+//    tokens over 4K-32K keys, 64 heads on 8: 322-327 us, 6.6 TB/s;
 //  - E4M3 caches: shared memory, 224 KB a block of 128 keys in some 2400
-//    cycles: 16 sequences of 5 tokens 139 us, 3545 GB/s;
+//    cycles: 16 sequences of 5 tokens 139 us, 3545 GB/s; 2 x 2048 tokens
+//    over 4096 539 us, 1275 TFLOP/s;
 //  - short and packed prompts: the ends of items.  A CTA's last block, the
 //    drain of P.V and the result take some 9000 cycles beside the next
-//    item's start: 20K tokens in 9 prompts 398 us, 1378 TFLOP/s.
+//    item's start: 20K tokens in 9 prompts 382-407 us, 1345-1430 TFLOP/s.
 #pragma once
 
 #include "fd_extend.h"

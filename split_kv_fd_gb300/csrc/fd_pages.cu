@@ -9,11 +9,13 @@
 // a release undoes the growth before it.  All of it follows from exclusive
 // prefix sums over b, so the result does not depend on any order of threads.
 //
-// The data is a few KB: latency bounds it, the chain of lengths, two scans,
-// stack and table.  So one CTA keeps the books with up to 1024 sequences'
-// numbers in registers, and only the slots and positions, which may be many,
-// are written by the whole cluster behind it.  256 sequences one token on and
-// back: 7.0 us each way; 64 with 48 new ones, 16K tokens: 7.8.
+// The data is a few KB, and what takes the time is a chain of dependent
+// steps: lengths, two scans, stack and table.  So one CTA keeps the books with
+// up to 1024 sequences' numbers in registers, and only the slots and
+// positions, which may be many, are written by the whole cluster behind it.
+// 256 sequences one token on and back: 7.1 us each way; 64 with 48 new ones,
+// 16K tokens: 7.9.  (The scans are of 1024 threads in 64 bits whatever the
+// batch; what fewer and narrower ones would take is not measured.)
 #include "fd_device.cuh"
 #include "fd_pages.h"
 

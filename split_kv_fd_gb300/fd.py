@@ -621,7 +621,9 @@ def resize_pages(seqlens, target, block_table, free_pages, free_count, page_size
     [max_tokens] receive the new tokens' places in the pool and positions
     (-1 and 0 behind the last), cu_new int32 [B+1] the offsets of the
     sequences' new tokens (allocated if only slots or positions are given).
-    Returns ``cu_new``.  A sequence that could not grow keeps its length.
+    Returns ``cu_new``.  A sequence that could not grow keeps its length, and
+    so do those behind it whose pages would only be free without it: running
+    sequences go ahead of admissions.
     """
     dev = _one_device(seqlens, target, block_table, free_pages, free_count, slots, positions, cu_new)
     if seqlens.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
