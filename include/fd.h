@@ -54,7 +54,7 @@ extern "C" {
 
 /* FD_E4M3 (OCP FP8 E4M3, one byte) is a KV-cache element type for
  * fd_decode_fp8, fd_decode_gqa_fp8, fd_decode_gqa_paged_fp8,
- * fd_append_paged_fp8 and fd_extend_paged_fp8 only. */
+ * fd_append_paged_fp8, fd_append_rope_paged_fp8 and fd_extend_paged_fp8 only. */
 typedef enum { FD_F32 = 0, FD_F16 = 1, FD_BF16 = 2, FD_E4M3 = 3 } fd_dtype;
 
 typedef enum {
@@ -66,7 +66,8 @@ typedef enum {
     FD_ERR_DEVICE_TIMEOUT = 5,  /* a kernel gave up waiting on its own copies */
     FD_ERR_SCRATCH_TOO_SMALL = 6, /* fd_decode_noalloc: problem exceeds its scratch */
     FD_ERR_BAD_PAGE = 7,        /* a block-table entry named no page (see fd_decode_paged) */
-    FD_ERR_BAD_OFFSETS = 8      /* sequence offsets that do not ascend within the rows given */
+    FD_ERR_BAD_OFFSETS = 8,     /* sequence offsets that do not ascend within the rows given */
+    FD_ERR_BAD_INDEX = 9        /* a position outside its table, or a parent that is no beam */
 } fd_status;
 
 /* Human-readable name of a status code (static string, never NULL; an
@@ -348,10 +349,10 @@ fd_status fd_merge_lse(const float *o_a, const float *lse_a, const float *o_b, c
 /*
  * Reads (and if `reset` is non-zero, clears) the current device's status
  * word, which a kernel sets when it gives up waiting on its own copies or
- * meets a block-table entry that names no page or offsets that do not
- * ascend.  Synchronises the device.  Returns FD_OK, FD_ERR_DEVICE_TIMEOUT,
- * FD_ERR_BAD_PAGE, FD_ERR_BAD_OFFSETS (the first of these that is set) or
- * FD_ERR_CUDA.
+ * meets a block-table entry that names no page, offsets that do not ascend
+ * or an index outside its range.  Synchronises the device.  Returns FD_OK,
+ * FD_ERR_DEVICE_TIMEOUT, FD_ERR_BAD_PAGE, FD_ERR_BAD_OFFSETS,
+ * FD_ERR_BAD_INDEX (the first of these that is set) or FD_ERR_CUDA.
  */
 fd_status fd_device_status(int reset);
 
@@ -423,7 +424,8 @@ fd_status fd_decode_noalloc(const void *q, const void *k, const void *v, const i
  * Around decode: what fills a paged KV cache and attends with several new
  * tokens a sequence.  A serving step is
  *     fd_resize_pages   every sequence to its new length: pages and slots
- *     fd_append_paged   the new tokens' K and V rows into those slots
+ *     fd_append_paged   the new tokens' K and V rows into those slots (of a
+ *                       rotary model: fd_append_rope_paged)
  *     fd_extend_paged   their attention over the cache (or, with one new
  *                       token a sequence, fd_decode_gqa_paged)
  * and fd_prefill attends over packed prompts without a cache.  The new
@@ -505,6 +507,49 @@ fd_status fd_append_paged_fp8(const void *k, const void *v, const float *k_scale
                               const int32_t *cu_new, const int32_t *slots, int B, int total, int Hkv, int d,
                               long long k_stride, long long v_stride, fd_dtype dtype, void *k_pages, void *v_pages,
                               int page_size, long long num_pages, void *stream);
+
+/*
+ * fd_append_paged with the position rotation applied to K on the way, and q
+ * rotated beside it: what a rotary model's new tokens need ahead of their
+ * attention, in one launch.  The first `rot` elements of a head are rot/2
+ * pairs (x, y), elements i and i + rot/2 (or 2i and 2i + 1 if `interleaved`);
+ * pair i of token t becomes
+ *     x cos - y sin,  y cos + x sin,   cos = rope[positions[t]][i],
+ *                                      sin = rope[positions[t]][rot/2 + i]
+ * with each product and the sum rounded to float32, then to `dtype` once.
+ * Elements from `rot` on and V are moved as they are.
+ *   q         [total, Hq, d] in `dtype`, tokens q_stride elements apart, or
+ *             NULL with Hq = 0
+ *   q_out     [total, Hq, d] in `dtype`, tokens q_out_stride elements apart;
+ *             may be q itself with q's stride, else must not overlap it
+ *   positions [total] int32, in [0, max_position)
+ *   rope      [max_position, rot] float32, 16-byte aligned
+ *   k, v, slots, k_pages, v_pages  as in fd_append_paged
+ * A token with a negative slot is skipped, its q_out row included (rows behind
+ * a batch stay as they were); so is one whose slot is past the pool
+ * (FD_ERR_BAD_PAGE) or whose position has no row (FD_ERR_BAD_INDEX).
+ * d must be 64, 128 or 256, rot a multiple of 16 up to d, Hkv at least 1.
+ */
+fd_status fd_append_rope_paged(const void *q, const void *k, const void *v, const int32_t *slots,
+                               const int32_t *positions, const float *rope, int max_position, int rot,
+                               int interleaved, int total, int Hq, int Hkv, int d, long long q_stride,
+                               long long k_stride, long long v_stride, fd_dtype dtype, void *q_out,
+                               long long q_out_stride, void *k_pages, void *v_pages, int page_size,
+                               long long num_pages, void *stream);
+
+/*
+ * fd_append_rope_paged into E4M3 pages: the rotated K (in float32, not rounded
+ * to `dtype` in between) and V divided by their scales and rounded as in
+ * fd_append_paged_fp8, whose scales and cu_new these are; rows outside
+ * [cu_new[0], cu_new[B]) are skipped, q_out's included.
+ */
+fd_status fd_append_rope_paged_fp8(const void *q, const void *k, const void *v, const float *k_scale,
+                                   const float *v_scale, const int32_t *cu_new, const int32_t *slots,
+                                   const int32_t *positions, const float *rope, int max_position, int rot,
+                                   int interleaved, int B, int total, int Hq, int Hkv, int d, long long q_stride,
+                                   long long k_stride, long long v_stride, fd_dtype dtype, void *q_out,
+                                   long long q_out_stride, void *k_pages, void *v_pages, int page_size,
+                                   long long num_pages, void *stream);
 
 /*
  * Bytes of device workspace fd_prefill, fd_extend_paged and

@@ -7,6 +7,7 @@
 #include "fd_gqa_tc8.cuh"
 #include "fd_host.h"
 #include "fd_internal.h"
+#include "fd_pages.h"
 #include "fd_split.cuh"
 
 #include <algorithm>
@@ -442,6 +443,8 @@ const char *fd_status_str(fd_status status)
     case FD_ERR_DEVICE_TIMEOUT: return "FD_ERR_DEVICE_TIMEOUT: a kernel gave up waiting on its copies";
     case FD_ERR_BAD_OFFSETS:
         return "FD_ERR_BAD_OFFSETS: offsets that do not ascend within the rows given";
+    case FD_ERR_BAD_INDEX:
+        return "FD_ERR_BAD_INDEX: a position outside its table, or a parent that is no beam";
     case FD_ERR_BAD_PAGE:
         return "FD_ERR_BAD_PAGE: a block-table entry named no page (its rows were read from page 0)";
     case FD_ERR_SCRATCH_TOO_SMALL:
@@ -674,7 +677,9 @@ fd_status fd_device_status(int reset)
         return FD_ERR_DEVICE_TIMEOUT;
     if (v & STATUS_BAD_PAGE)
         return FD_ERR_BAD_PAGE;
-    return (v & STATUS_BAD_OFFSETS) ? FD_ERR_BAD_OFFSETS : FD_OK;
+    if (v & STATUS_BAD_OFFSETS)
+        return FD_ERR_BAD_OFFSETS;
+    return (v & STATUS_BAD_INDEX) ? FD_ERR_BAD_INDEX : FD_OK;
 }
 
 size_t fd_workspace_size_gqa(int B, int Hq, int Hkv, int N, int d, int num_splits)

@@ -11,6 +11,7 @@
 // (59 with 4 tokens and an IEEE division an element).  256 tokens: 1.9 and
 // 3.1 us, a launch and two or three dependent loads.
 #include "fd_device.cuh"
+#include "fd_e4m3.cuh"
 #include "fd_pages.h"
 
 namespace fd {
@@ -24,20 +25,6 @@ __device__ __forceinline__ uint4 ldg_stream(const void *p)
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
     return v;
-}
-
-// Two floats to two E4M3 bytes (the first in the lower), to nearest, ties to
-// even, saturated; NaN stays NaN.
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi)
-{
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
-{
-    return e4m3x2(a, b) | e4m3x2(c, d) << 16;
 }
 
 // Threads of a CTA: 8 heads of 128 are 256 pieces in 16 bits, 128 in E4M3
@@ -121,27 +108,8 @@ __global__ void __launch_bounds__(AT) append_kernel(const AppendParams p)
 #pragma unroll
                 for (int k = 0; k < SRC; ++k)
                     Elem<T>::widen(x[u][k], f + k * Elem<T>::VEC);
-                // The quotient lies between the products with a reciprocal
-                // that is a little too small and one that is a little too
-                // large (2^-21, against 3 roundings of 2^-24), and rounding
-                // keeps that order: where both give the same byte, it is the
-                // quotient's.  Else (ties, one in 10^5 otherwise, and scales
-                // whose reciprocal is no normal number) divide.
-                const float r = __frcp_rn(sc[u]);
-                const float r0 = r * (1.f - 0x1p-21f), r1 = r * (1.f + 0x1p-21f);
-                bool same = fabsf(sc[u]) >= 0x1p-126f && fabsf(sc[u]) <= 0x1p125f;
                 uint32_t w[EL / 4];
-#pragma unroll
-                for (int k = 0; k < EL / 4; ++k) {
-                    w[k] = e4m3x4(f[4 * k] * r0, f[4 * k + 1] * r0, f[4 * k + 2] * r0, f[4 * k + 3] * r0);
-                    same &= w[k] == e4m3x4(f[4 * k] * r1, f[4 * k + 1] * r1, f[4 * k + 2] * r1, f[4 * k + 3] * r1);
-                }
-                if (!same) {
-#pragma unroll
-                    for (int k = 0; k < EL / 4; ++k)
-                        w[k] = e4m3x4(__fdiv_rn(f[4 * k], sc[u]), __fdiv_rn(f[4 * k + 1], sc[u]),
-                                      __fdiv_rn(f[4 * k + 2], sc[u]), __fdiv_rn(f[4 * k + 3], sc[u]));
-                }
+                e4m3_quotients<EL>(f, sc[u], w);
                 *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[2], w[3]);
             } else {
                 *reinterpret_cast<uint4 *>(to) = x[u][0];

@@ -439,4 +439,111 @@ fd_status fd_append_paged_fp8(const void *k, const void *v, const float *k_scale
     return append(p, num_pages, stream);
 }
 
+namespace {
+
+fd_status append_rope(RopeParams &p, long long num_pages, void *stream)
+{
+    const int of = p.dtype == FD_F32 ? 4 : 8;   // elements of 16 bytes
+    if (p.T < 0 || p.H < 1 || p.Hq < 0 || p.page_size < 1 || num_pages < 0 || p.d < 1 || p.max_position < 0 ||
+        num_pages > INT_MAX / p.page_size || ((long long)p.Hq + 2LL * p.H) * p.d > INT_MAX)
+        return FD_ERR_INVALID_ARG;
+    if ((p.dtype != FD_F32 && !is16(p.dtype)) || (p.d != 64 && p.d != 128 && p.d != 256) || p.rot < 16 ||
+        p.rot > p.d || p.rot % 16 != 0)
+        return FD_ERR_UNSUPPORTED;
+    const long long row = (long long)p.H * p.d, qrow = (long long)p.Hq * p.d;
+    if (!stride_ok(p.k_stride, p.T, row, of) || !stride_ok(p.v_stride, p.T, row, of) ||
+        (p.Hq > 0 && (!stride_ok(p.q_stride, p.T, qrow, of) || !stride_ok(p.q_out_stride, p.T, qrow, of))))
+        return FD_ERR_INVALID_ARG;
+    if (p.T == 0)
+        return FD_OK;
+    if (!p.k || !p.v || !p.slots || !p.positions || !p.table || !p.k_pages || !p.v_pages || !aligned(p.k, 16) ||
+        !aligned(p.v, 16) || !aligned(p.table, 16) || !aligned(p.k_pages, 16) || !aligned(p.v_pages, 16) ||
+        !aligned(p.slots, 4) || !aligned(p.positions, 4) ||
+        (p.Hq > 0 && (!p.q || !p.q_out || !aligned(p.q, 16) || !aligned(p.q_out, 16))) ||
+        (p.f8 && (p.B < 1 || p.B > MAX_SEQUENCES || !p.cu || !p.k_scale || !p.v_scale || !aligned(p.cu, 4) ||
+                  !aligned(p.k_scale, 4) || !aligned(p.v_scale, 4))))
+        return FD_ERR_INVALID_ARG;
+    p.num_slots = num_pages * p.page_size;
+    p.status = status_ptr();
+    if (!p.status)
+        return FD_ERR_CUDA;
+    return launch_rope(p, stream_of(stream)) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
+}
+
+}  // namespace
+
+fd_status fd_append_rope_paged(const void *q, const void *k, const void *v, const int32_t *slots,
+                               const int32_t *positions, const float *rope, int max_position, int rot,
+                               int interleaved, int total, int Hq, int Hkv, int d, long long q_stride,
+                               long long k_stride, long long v_stride, fd_dtype dtype, void *q_out,
+                               long long q_out_stride, void *k_pages, void *v_pages, int page_size,
+                               long long num_pages, void *stream)
+{
+    RopeParams p;
+    memset(&p, 0, sizeof p);
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.q_out = q_out;
+    p.q_stride = q_stride;
+    p.q_out_stride = q_out_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.positions = positions;
+    p.table = rope;
+    p.max_position = max_position;
+    p.rot = rot;
+    p.pairs = interleaved != 0;
+    p.T = total;
+    p.Hq = Hq;
+    p.H = Hkv;
+    p.d = d;
+    p.dtype = dtype;
+    p.slots = slots;
+    p.k_pages = k_pages;
+    p.v_pages = v_pages;
+    p.page_size = page_size;
+    return append_rope(p, num_pages, stream);
+}
+
+fd_status fd_append_rope_paged_fp8(const void *q, const void *k, const void *v, const float *k_scale,
+                                   const float *v_scale, const int32_t *cu_new, const int32_t *slots,
+                                   const int32_t *positions, const float *rope, int max_position, int rot,
+                                   int interleaved, int B, int total, int Hq, int Hkv, int d, long long q_stride,
+                                   long long k_stride, long long v_stride, fd_dtype dtype, void *q_out,
+                                   long long q_out_stride, void *k_pages, void *v_pages, int page_size,
+                                   long long num_pages, void *stream)
+{
+    RopeParams p;
+    memset(&p, 0, sizeof p);
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.q_out = q_out;
+    p.q_stride = q_stride;
+    p.q_out_stride = q_out_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.positions = positions;
+    p.table = rope;
+    p.max_position = max_position;
+    p.rot = rot;
+    p.pairs = interleaved != 0;
+    p.T = total;
+    p.Hq = Hq;
+    p.H = Hkv;
+    p.d = d;
+    p.dtype = dtype;
+    p.slots = slots;
+    p.k_pages = k_pages;
+    p.v_pages = v_pages;
+    p.page_size = page_size;
+    p.f8 = 1;
+    p.B = B;
+    p.cu = cu_new;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    return append_rope(p, num_pages, stream);
+}
+
 }  // extern "C"

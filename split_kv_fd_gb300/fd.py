@@ -21,7 +21,8 @@ from . import _build_lib
 FD_OK = 0
 STATUS_NAMES = {0: "FD_OK", 1: "FD_ERR_INVALID_ARG", 2: "FD_ERR_UNSUPPORTED",
                 3: "FD_ERR_WORKSPACE", 4: "FD_ERR_CUDA", 5: "FD_ERR_DEVICE_TIMEOUT",
-                6: "FD_ERR_SCRATCH_TOO_SMALL", 7: "FD_ERR_BAD_PAGE", 8: "FD_ERR_BAD_OFFSETS"}
+                6: "FD_ERR_SCRATCH_TOO_SMALL", 7: "FD_ERR_BAD_PAGE", 8: "FD_ERR_BAD_OFFSETS",
+                9: "FD_ERR_BAD_INDEX"}
 
 INT_MAX = 2 ** 31 - 1
 
@@ -34,7 +35,7 @@ EXPORTS = ["fd_status_str", "fd_version", "fd_num_sms", "fd_auto_num_splits",
            "fd_decode_fp8", "fd_merge_lse", "fd_decode_gqa", "fd_workspace_size_gqa",
            "fd_selftest_wait_timeout", "fd_decode_gqa_paged", "fd_decode_gqa_fp8",
            "fd_decode_gqa_paged_fp8", "fd_resize_pages", "fd_append_paged", "fd_append_paged_fp8",
-           "fd_workspace_size_extend", "fd_prefill", "fd_extend_paged", "fd_extend_paged_fp8"]
+           "fd_append_rope_paged", "fd_append_rope_paged_fp8", "fd_workspace_size_extend", "fd_prefill", "fd_extend_paged", "fd_extend_paged_fp8"]
 
 _lock = threading.Lock()
 _lib = None
@@ -114,6 +115,10 @@ def load(build_if_missing: bool = False):
         lib.fd_append_paged.restype = I
         lib.fd_append_paged_fp8.argtypes = [P, P, P, P, P, P, I, I, I, I, L, L, I, P, P, I, L, P]
         lib.fd_append_paged_fp8.restype = I
+        lib.fd_append_rope_paged.argtypes = [P] * 6 + [I] * 7 + [L, L, L, I, P, L, P, P, I, L, P]
+        lib.fd_append_rope_paged.restype = I
+        lib.fd_append_rope_paged_fp8.argtypes = [P] * 9 + [I] * 8 + [L, L, L, I, P, L, P, P, I, L, P]
+        lib.fd_append_rope_paged_fp8.restype = I
         lib.fd_workspace_size_extend.argtypes = [I, I, I, I, I]
         lib.fd_workspace_size_extend.restype = S
         lib.fd_prefill.argtypes = [P, P, P, P, P, I, I, I, I, I, I, L, L, L, I, I, F, P, I, P, P, S, P]
@@ -703,6 +708,71 @@ def append_paged_fp8(k, v, k_scale, v_scale, cu_new, slots, k_pages, v_pages, st
           cu_new.data_ptr(), slots.data_ptr(), B, *args)
 
 
+def _rope_args(k, v, slots, positions, rope, k_pages, v_pages, q, q_out, interleaved, stream):
+    """The arguments of the rotating appends from the positions on, and
+    q_out, checked or allocated."""
+    T, H, d, k_stride, v_stride, *rest = _append_args(k, v, slots, k_pages, v_pages)
+    _int32(positions, (T,), "positions")
+    if rope.dtype != torch.float32 or rope.dim() != 2 or not rope.is_contiguous():
+        raise ValueError("rope must be contiguous float32 [max_position, rot]: cosines, then sines")
+    if max(rope.shape) > INT_MAX:
+        raise ValueError("rope: sizes must be below 2^31")
+    Hq, q_stride, out_stride = 0, 0, 0
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+    else:
+        q_stride = _rows(q, "q")
+        if q.dtype != k.dtype or q.shape[0] != T or q.shape[2] != d:
+            raise ValueError("q must be [T, Hq, d] of k's tokens, head dim and dtype")
+        Hq = q.shape[1]
+        if q_out is None:
+            q_out = _empty(stream, q.shape, dtype=q.dtype, device=q.device)
+        elif q_out.shape != q.shape or q_out.dtype != q.dtype:
+            raise ValueError("q_out must have q's shape and dtype")
+        out_stride = _rows(q_out, "q_out")
+    args = (positions.data_ptr(), rope.data_ptr(), rope.shape[0], rope.shape[1], bool(interleaved))
+    sizes = (T, Hq, H, d, q_stride, k_stride, v_stride, rest[0], _address(q_out) if Hq else None, out_stride, *rest[1:])
+    return args, sizes, q_out
+
+
+def append_rope_paged(k, v, slots, positions, rope, k_pages, v_pages, q=None, q_out=None, interleaved=False, stream=None):
+    """New K and V rows into a paged cache, in place, K rotated by its position
+    on the way, and q beside it (fd_append_rope_paged).  Returns the rotated
+    q, or None without q.
+
+    k, v, slots, pages as in append_paged; positions int32 [T]; rope float32
+    [max_position, rot], a row the cosines of rot/2 angles and then their
+    sines; the pairs are elements i and i + rot/2 of a head, or 2i and 2i + 1
+    with ``interleaved``.  q [T, Hq, d] of k's dtype; q_out [T, Hq, d] may be q.
+    Tokens with a negative slot are skipped, their rows of q_out too.
+    """
+    dev = _one_device(k, v, slots, positions, rope, k_pages, v_pages, q, q_out)
+    args, sizes, q_out = _rope_args(k, v, slots, positions, rope, k_pages, v_pages, q, q_out, interleaved, stream)
+    if k_pages.dtype != k.dtype:
+        raise ValueError("the pages must have k's dtype")
+    _call("fd_append_rope_paged", dev, stream, _address(q) if sizes[1] else None, k.data_ptr(), v.data_ptr(),
+          slots.data_ptr(), *args, *sizes)
+    return q_out
+
+
+def append_rope_paged_fp8(k, v, k_scale, v_scale, cu_new, slots, positions, rope, k_pages, v_pages, q=None, q_out=None,
+                          interleaved=False, stream=None):
+    """append_rope_paged into E4M3 pages (fd_append_rope_paged_fp8): k_scale,
+    v_scale float32 [B, Hkv] and cu_new int32 [B+1] as in append_paged_fp8.
+    Returns the rotated q, or None without q."""
+    dev = _one_device(k, v, k_scale, v_scale, cu_new, slots, positions, rope, k_pages, v_pages, q, q_out)
+    args, sizes, q_out = _rope_args(k, v, slots, positions, rope, k_pages, v_pages, q, q_out, interleaved, stream)
+    if k_pages.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise ValueError("pages must be float8_e4m3fn (or uint8 E4M3 bytes)")
+    B = cu_new.numel() - 1
+    _scales(k_scale, v_scale, (B, sizes[2]))
+    _int32(cu_new, (B + 1,), "cu_new")
+    _call("fd_append_rope_paged_fp8", dev, stream, _address(q) if sizes[1] else None, k.data_ptr(), v.data_ptr(),
+          k_scale.data_ptr(), v_scale.data_ptr(), cu_new.data_ptr(), slots.data_ptr(), *args, B, *sizes)
+    return q_out
+
+
 def workspace_size_extend(B, total_q, Hq, Hkv, d) -> int:
     """Bytes of workspace prefill, extend_paged and extend_paged_fp8 need."""
     return load().fd_workspace_size_extend(B, total_q, Hq, Hkv, d)
@@ -958,6 +1028,6 @@ def selftest_wait_timeout(stream=None) -> None:
 
 
 def device_status(reset: bool = True) -> int:
-    """FD_OK, or what a kernel recorded: FD_ERR_DEVICE_TIMEOUT, FD_ERR_BAD_PAGE
-    or FD_ERR_BAD_OFFSETS (synchronises)."""
+    """FD_OK, or what a kernel recorded: FD_ERR_DEVICE_TIMEOUT, FD_ERR_BAD_PAGE,
+    FD_ERR_BAD_OFFSETS or FD_ERR_BAD_INDEX (synchronises)."""
     return load().fd_device_status(1 if reset else 0)
