@@ -632,6 +632,58 @@ fd_status fd_extend_paged_fp8(const void *q, fd_dtype q_dtype, const void *k_pag
                               float scale, void *out, fd_dtype out_dtype, float *lse, void *workspace,
                               size_t workspace_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Beam search over a paged cache.  A request's W beams are W neighbouring
+ * sequences, and a step of them is
+ *     fd_beam_select    of their W * V continuations the best
+ *     fd_reorder_pages  the beams' block tables and lengths to those of the
+ *                       chosen parents
+ *     fd_copy_pages     (each layer) the partly filled pages that beams can
+ *                       no longer share
+ * and then the calls around decode for the next token.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * Bytes of device workspace fd_beam_select needs on the current device,
+ * whatever the logits' type and strides.  It needs no initialisation; calls
+ * that overlap on the GPU need workspaces of their own.  Returns 0 for sizes
+ * that are not supported, or on a CUDA error.
+ */
+size_t fd_workspace_size_beam(int R, int W, int V, int K);
+
+/*
+ * Beam search's selection: for each of R requests the K continuations with
+ * the largest score among those of its W beams.  Beam w goes on with token v
+ * at the score
+ *     scores[r][w] + x_v - ln sum_u exp(x_u),   x = logits[r][w],
+ * or, if it is finished, with `eos` alone at the score it has.
+ *   logits    [R, W, V] f32, f16 or bf16, a beam's V neighbouring, beams and
+ *             requests any distance (>= 0) apart; any alignment
+ *   scores    [R, W] float32
+ *   finished  [R, W] bytes, non-zero where a beam has ended, or NULL; its
+ *             logits are not read.  Needs an eos
+ *   eos       the token that ends a beam, or -1
+ *   out_scores, out_parents, out_tokens  [R, K], the best first; equal
+ *             scores in order of w * V + v; parents are beams of the request
+ *   out_finished  [R, K] bytes: 1 where the token is eos or the parent was
+ *             finished; or NULL.  Not the buffer of `finished`
+ * A logit of -inf or NaN is no continuation, +inf counts as the largest
+ * finite float32; a beam whose score is not finite has none (all but one at a
+ * request's first token: -inf), nor is one whose score leaves the range of
+ * float32.  Where fewer than K are left the rest is -inf, parent -1, token
+ * -1, finished.
+ * The sum of exponentials is float32, its logarithm and all after it close to
+ * 48 bits: continuations of one beam are ordered as their logits are, those of
+ * two beams as their scores where these differ by more than some 1e-7 of a
+ * sum's rounding.
+ * 1 <= W <= 32, 1 <= K <= 64, K <= W * V, W * V <= 2^30; outputs must not
+ * overlap inputs.
+ */
+fd_status fd_beam_select(const void *logits, fd_dtype dtype, long long request_stride, long long beam_stride,
+                         const float *scores, const uint8_t *finished, int R, int W, int V, int K, int eos,
+                         float *out_scores, int32_t *out_parents, int32_t *out_tokens, uint8_t *out_finished,
+                         void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -2,6 +2,7 @@
 // cache append, attention of new tokens over a paged cache and over packed
 // prompts.  Argument checks and launches.
 #include "fd.h"
+#include "fd_beam.h"
 #include "fd_device.cuh"
 #include "fd_extend.h"
 #include "fd_host.h"
@@ -544,6 +545,96 @@ fd_status fd_append_rope_paged_fp8(const void *q, const void *k, const void *v, 
     p.k_scale = k_scale;
     p.v_scale = v_scale;
     return append_rope(p, num_pages, stream);
+}
+
+namespace {
+
+// The parts of a selection and its workspace, for the type with the most
+// segments (`elem` bytes an element).
+struct SelectLayout {
+    int segs, per_part, parts;
+    size_t part, total;
+};
+
+bool select_sizes_ok(int R, int W, int V, int K)
+{
+    return R >= 0 && W >= 1 && W <= BEAM_MAX_W && V >= 1 && K >= 1 && K <= BEAM_MAX_K &&
+           (long long)W * V <= MAX_SEQUENCES && K <= (long long)W * V && (long long)R * W <= INT_MAX;
+}
+
+SelectLayout select_layout(int R, int W, int V, int elem, int sms)
+{
+    SelectLayout l;
+    l.segs = select_segs(V, elem);
+    // A segment a warp; more where the card has 16 CTAs an SM without.
+    const int warps = SEL_THREADS / 32;
+    const long long most = ((long long)R * W * l.segs + warps - 1) / warps, want = 16LL * sms;
+    const long long rounds = most > want ? most / want : 1;
+    l.per_part = (int)(rounds * warps < l.segs ? rounds * warps : l.segs);
+    l.parts = (l.segs + l.per_part - 1) / l.per_part;
+    l.part = round_up((size_t)R * W * l.segs * sizeof(float), 256);
+    l.total = l.part + (size_t)R * W * l.parts * sizeof(float2);
+    return l;
+}
+
+}  // namespace
+
+size_t fd_workspace_size_beam(int R, int W, int V, int K)
+{
+    const int sms = sm_count();
+    if (!select_sizes_ok(R, W, V, K) || sms <= 0)
+        return 0;
+    const size_t a = select_layout(R, W, V, 4, sms).total, b = select_layout(R, W, V, 2, sms).total;
+    return round_up(a > b ? a : b, 256) + (R == 0 ? 256 : 0);
+}
+
+fd_status fd_beam_select(const void *logits, fd_dtype dtype, long long request_stride, long long beam_stride,
+                         const float *scores, const uint8_t *finished, int R, int W, int V, int K, int eos,
+                         float *out_scores, int32_t *out_parents, int32_t *out_tokens, uint8_t *out_finished,
+                         void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!select_sizes_ok(R, W, V, K) || request_stride < 0 || beam_stride < 0 || eos < -1 || eos >= V ||
+        (finished && eos < 0))
+        return FD_ERR_INVALID_ARG;
+    if (dtype != FD_F32 && !is16(dtype))
+        return FD_ERR_UNSUPPORTED;
+    if (R == 0)
+        return FD_OK;
+    const int elem = dtype == FD_F32 ? 4 : 2;
+    if (!logits || !aligned(logits, elem) || !scores || !aligned(scores, 4) || !out_scores || !out_parents ||
+        !out_tokens || !aligned(out_scores, 4) || !aligned(out_parents, 4) || !aligned(out_tokens, 4))
+        return FD_ERR_INVALID_ARG;
+    const int sms = sm_count();
+    if (sms <= 0)
+        return FD_ERR_CUDA;
+    const SelectLayout l = select_layout(R, W, V, elem, sms);
+    if ((long long)R * W * l.parts > INT_MAX)
+        return FD_ERR_UNSUPPORTED;   // too many rows for a grid
+    if (!workspace || workspace_bytes < l.total || !aligned(workspace, 256))
+        return FD_ERR_WORKSPACE;
+    SelectParams p;
+    memset(&p, 0, sizeof p);
+    p.logits = logits;
+    p.r_stride = request_stride;
+    p.w_stride = beam_stride;
+    p.dtype = dtype;
+    p.scores = scores;
+    p.finished = finished;
+    p.R = R;
+    p.W = W;
+    p.V = V;
+    p.K = K;
+    p.eos = eos;
+    p.out_scores = out_scores;
+    p.out_parents = out_parents;
+    p.out_tokens = out_tokens;
+    p.out_finished = out_finished;
+    p.segs = l.segs;
+    p.per_part = l.per_part;
+    p.parts = l.parts;
+    p.seg_max = static_cast<float *>(workspace);
+    p.part = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + l.part);
+    return launch_select(p, stream_of(stream)) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
 }
 
 }  // extern "C"

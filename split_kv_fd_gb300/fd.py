@@ -35,7 +35,8 @@ EXPORTS = ["fd_status_str", "fd_version", "fd_num_sms", "fd_auto_num_splits",
            "fd_decode_fp8", "fd_merge_lse", "fd_decode_gqa", "fd_workspace_size_gqa",
            "fd_selftest_wait_timeout", "fd_decode_gqa_paged", "fd_decode_gqa_fp8",
            "fd_decode_gqa_paged_fp8", "fd_resize_pages", "fd_append_paged", "fd_append_paged_fp8",
-           "fd_append_rope_paged", "fd_append_rope_paged_fp8", "fd_workspace_size_extend", "fd_prefill", "fd_extend_paged", "fd_extend_paged_fp8"]
+           "fd_append_rope_paged", "fd_append_rope_paged_fp8", "fd_workspace_size_extend", "fd_prefill", "fd_extend_paged", "fd_extend_paged_fp8",
+           "fd_workspace_size_beam", "fd_beam_select"]
 
 _lock = threading.Lock()
 _lib = None
@@ -127,6 +128,10 @@ def load(build_if_missing: bool = False):
         lib.fd_extend_paged.restype = I
         lib.fd_extend_paged_fp8.argtypes = [P, I, P, P, P, P, P, P, P, I, I, I, I, I, L, I, I, L, F, P, I, P, P, S, P]
         lib.fd_extend_paged_fp8.restype = I
+        lib.fd_workspace_size_beam.argtypes = [I, I, I, I]
+        lib.fd_workspace_size_beam.restype = S
+        lib.fd_beam_select.argtypes = [P, I, L, L, P, P, I, I, I, I, I, P, P, P, P, P, S, P]
+        lib.fd_beam_select.restype = I
         _lib = lib
         return lib
 
@@ -915,6 +920,68 @@ def extend_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, cu_seql
           v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), cu_seqlens_q.data_ptr(),
           seqlens.data_ptr(), *args, *_tail(args[4], scale, out, lse, workspace))
     return out, lse
+
+
+def workspace_size_beam(R, W, V, K) -> int:
+    """Bytes of workspace beam_select needs."""
+    return load().fd_workspace_size_beam(R, W, V, K)
+
+
+@functools.lru_cache(maxsize=1024)
+def _known_beam_bytes(dev, *sizes):
+    with torch.cuda.device(dev):
+        n = workspace_size_beam(*sizes)
+    if n == 0:   # as in _known_extend_bytes
+        raise LookupError
+    return n
+
+
+def beam_select(logits, scores, num=None, finished=None, eos=-1, workspace=None, stream=None):
+    """Beam search's selection (fd_beam_select): of the W * V continuations of
+    each request's W beams the ``num`` (default W) with the largest score, the
+    best first.  Returns ``(scores, parents, tokens, finished)``, [R, num]
+    float32, int32, int32 and bool.
+
+    logits [R, W, V] float32, float16 or bfloat16, a beam's V neighbouring (any
+    strides else); scores float32 [R, W]; finished bool [R, W]: beams that go
+    on with ``eos`` alone at the score they have.  Equal scores in order of
+    beam and token.  Where a request has fewer continuations (of -inf, NaN
+    and beams without a finite score there are none) the rest is -inf, -1, -1
+    and finished.
+    """
+    dev = _one_device(logits, scores, finished)
+    if logits.dim() != 3 or logits.dtype not in DTYPE_CODE:
+        raise ValueError("logits must be [R, W, V] float32/float16/bfloat16")
+    (R, W, V), (far, near, one) = logits.shape, logits.stride()
+    if V > 1 and one != 1:
+        raise ValueError("logits: a beam's V must be contiguous")
+    if max(R, W, V) > INT_MAX:
+        raise ValueError("logits: sizes must be below 2^31")
+    if scores.dtype != torch.float32 or scores.shape != (R, W) or not scores.is_contiguous():
+        raise ValueError("scores must be contiguous float32 [R, W]")
+    if finished is not None and (finished.dtype != torch.bool or finished.shape != (R, W) or not finished.is_contiguous()):
+        raise ValueError("finished must be contiguous bool [R, W]")
+    K = W if num is None else num
+    if not 1 <= K <= INT_MAX:
+        raise ValueError("num must be positive")
+    if not -1 <= eos < max(V, 1):
+        raise ValueError("eos must be a token, or -1")
+    where = logits.device
+    if workspace is None:
+        try:
+            n = _known_beam_bytes(dev, R, W, V, K)
+        except LookupError:
+            n = 256   # the call itself says why
+        workspace = _empty(stream, n, dtype=torch.uint8, device=where)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on the logits' device")
+    out = _empty(stream, (R, K), dtype=torch.float32, device=where)
+    parents, tokens = (_empty(stream, (R, K), dtype=torch.int32, device=where) for _ in range(2))
+    over = _empty(stream, (R, K), dtype=torch.bool, device=where)
+    _call("fd_beam_select", dev, stream, logits.data_ptr(), DTYPE_CODE[logits.dtype], far, near, scores.data_ptr(),
+          _address(finished), R, W, V, K, eos, out.data_ptr(), parents.data_ptr(), tokens.data_ptr(), over.data_ptr(),
+          workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return out, parents, tokens, over
 
 
 def decode_split(q, k, v, num_splits, seqlens=None, scale=None, stream=None, o_part=None,
