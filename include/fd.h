@@ -684,6 +684,66 @@ fd_status fd_beam_select(const void *logits, fd_dtype dtype, long long request_s
                          float *out_scores, int32_t *out_parents, int32_t *out_tokens, uint8_t *out_finished,
                          void *workspace, size_t workspace_bytes, void *stream);
 
+/* Bytes of device workspace fd_reorder_pages needs; it needs no
+ * initialisation.  Returns 0 for sizes that are not supported. */
+size_t fd_workspace_size_reorder(int R, int W, int max_pages);
+
+/*
+ * The beams' cached states to those of their parents, in place and on the
+ * GPU: beam w of request r, sequence r*W + w, takes the block table and
+ * length of sequence r*W + parents[r][w].  Full pages are shared: the beams of
+ * a request may name one page at the same place of their tables, which the
+ * attention calls read like any other.  A partly filled last page, which
+ * the next token is written to, is one beam's own: of those that would share
+ * it the first keeps it, the others get pages from the stack, and `copies`
+ * says what fd_copy_pages has to move into them.  Pages that no beam of the
+ * request names any more go on the stack.
+ *   parents      [R, W] int32: beams of the same request; negative: the beam
+ *                ends, its length becomes 0 (all of a request's negative: its
+ *                pages come back).  Behind a prompt that lies with beam 0,
+ *                all 0 starts the others, whose lengths were 0
+ *   seqlens      [R*W] int32, in and out
+ *   block_table  [R*W, max_pages] int32, in and out; entries behind the last
+ *                page stay as they are
+ *   free_pages, free_count   the stack of fd_resize_pages
+ *   copies       [R*W, 3] int32, out: page from, page to, and rows to copy of
+ *                each new beam; -1, -1, 0 where there is nothing to copy
+ *   granted      [R] int32, out, or NULL: 1, or 0 where a request stays as it
+ *                was because pages were missing
+ *   workspace    fd_workspace_size_reorder(R, W, max_pages) bytes, 256-byte
+ *                aligned
+ * Releases come first.  A request that gives back as many pages as it needs is
+ * granted in any case; the others in order, as long as what all up to it need
+ * beyond what they give back is free or left over by the former.  Released
+ * pages go on the stack in reverse order of (request, place, beam), copies
+ * take theirs from the top in order of (request, beam).  The result does not
+ * depend on the order of threads.
+ * Growth is fd_resize_pages' (new pages are a beam's own); it must not shrink
+ * beams into pages that they share.  A page belongs to one request, and
+ * is named at one place of its beams' tables; E4M3 scales are the same for a
+ * request's beams.  A parent of W or more counts as negative, reported as
+ * FD_ERR_BAD_INDEX by fd_device_status; ids that name no page are moved, but
+ * neither released nor copied, and released pages that would raise the stack
+ * past num_pages are dropped: both are reported as FD_ERR_BAD_PAGE.
+ * 1 <= W <= 32; page_size*max_pages and page_size*num_pages below 2^31.
+ */
+fd_status fd_reorder_pages(const int32_t *parents, int R, int W, int32_t *seqlens, int32_t *block_table,
+                           int max_pages, int32_t *free_pages, int32_t *free_count, int num_pages, int page_size,
+                           int32_t *copies, int32_t *granted, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Rows 0 .. copies[i][2]-1 of page copies[i][0] to page copies[i][1], of every
+ * head of K and V; an entry with a negative first page or no rows is skipped,
+ * one that names no page skipped and reported as FD_ERR_BAD_PAGE.  No page
+ * that is copied to may be another entry's source or target.
+ *   copies            [n, 3] int32, device (fd_reorder_pages writes them)
+ *   k_pages, v_pages  [num_pages, Hkv, page_size, d] in dtype (f32, f16, bf16
+ *                     or E4M3)
+ * d must be 64, 128 or 256.
+ */
+fd_status fd_copy_pages(const int32_t *copies, int n, int Hkv, int d, fd_dtype dtype, void *k_pages, void *v_pages,
+                        int page_size, long long num_pages, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

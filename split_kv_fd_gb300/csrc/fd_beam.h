@@ -1,5 +1,6 @@
-// fd_beam.h -- parameter blocks and launchers of beam search's selection
-// (fd_beam_select.cu).
+// fd_beam.h -- parameter blocks and launchers of beam search: selection
+// (fd_beam_select.cu) and the reordering of the beams' cached states
+// (fd_beam_pages.cu).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -40,5 +41,47 @@ inline int select_segs(int V, int elem)
 }
 
 cudaError_t launch_select(const SelectParams &p, cudaStream_t s);
+
+// A request's tables are taken in tiles of this many pages.
+constexpr int REORDER_TILE = 256;
+
+struct ReorderHeader {
+    long long raised;    // the stack's height with all that came back
+    int top, taken;      // its height as far as it is kept, and pages taken from there
+};
+
+struct ReorderParams {
+    const int32_t *parents;      // [R, W]
+    int R, W;
+    int32_t *seqlens;            // [R, W] in, out
+    int32_t *table;              // [R * W, max_pages] in, out
+    int max_pages, page_size;
+    int32_t *free_pages;         // [num_pages] stack, in, out
+    int32_t *free_count;         // [1] in, out
+    int num_pages;
+    int32_t *copies;             // [R, W, 3]: page from, page to, rows
+    int32_t *granted;            // [R] or null
+    unsigned *status;
+    // workspace
+    int tiles;                   // of a request
+    ReorderHeader *header;
+    int32_t *freed;              // [R, tiles] pages that come back
+    long long *freed_before;     // [R, tiles] of granted requests before it
+    int32_t *needed;             // [R] copies
+    int32_t *needed_before;      // [R] of granted requests before it, -1 if it is refused
+};
+
+cudaError_t launch_reorder(const ReorderParams &p, cudaStream_t s);
+
+struct CopyParams {
+    const int32_t *copies;       // [n, 3]
+    int n, H, page_size;
+    int row_vecs;                // 16-byte vectors of a row
+    void *k_pages, *v_pages;     // [num_pages, H, page_size, row]
+    long long num_pages;
+    unsigned *status;
+};
+
+cudaError_t launch_copy_pages(const CopyParams &p, cudaStream_t s);
 
 }  // namespace fd

@@ -637,4 +637,111 @@ fd_status fd_beam_select(const void *logits, fd_dtype dtype, long long request_s
     return launch_select(p, stream_of(stream)) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
 }
 
+namespace {
+
+struct ReorderLayout {
+    int tiles;
+    size_t freed, freed_before, needed, needed_before, total;
+};
+
+bool reorder_layout(int R, int W, int max_pages, ReorderLayout &l)
+{
+    if (R < 0 || W < 1 || W > BEAM_MAX_W || max_pages < 0 || (long long)R * W > MAX_SEQUENCES)
+        return false;
+    l.tiles = max_pages > 0 ? (int)(((long long)max_pages + REORDER_TILE - 1) / REORDER_TILE) : 1;
+    const size_t all = (size_t)R * l.tiles;
+    size_t at = round_up(sizeof(ReorderHeader), 256);
+    auto take = [&](size_t bytes) {
+        const size_t was = at;
+        at += round_up(bytes, 256);
+        return was;
+    };
+    l.freed = take(all * sizeof(int32_t));
+    l.freed_before = take(all * sizeof(long long));
+    l.needed = take((size_t)R * sizeof(int32_t));
+    l.needed_before = take((size_t)R * sizeof(int32_t));
+    l.total = at;
+    return (long long)R * l.tiles <= INT_MAX;
+}
+
+}  // namespace
+
+size_t fd_workspace_size_reorder(int R, int W, int max_pages)
+{
+    ReorderLayout l;
+    return reorder_layout(R, W, max_pages, l) ? l.total : 0;
+}
+
+fd_status fd_reorder_pages(const int32_t *parents, int R, int W, int32_t *seqlens, int32_t *block_table,
+                           int max_pages, int32_t *free_pages, int32_t *free_count, int num_pages, int page_size,
+                           int32_t *copies, int32_t *granted, void *workspace, size_t workspace_bytes, void *stream)
+{
+    ReorderLayout l;
+    if (!reorder_layout(R, W, max_pages, l) || num_pages < 0 || page_size < 1 ||
+        (long long)page_size * max_pages > INT_MAX || (long long)page_size * num_pages > INT_MAX)
+        return FD_ERR_INVALID_ARG;
+    if (R == 0)
+        return FD_OK;
+    if (!parents || !aligned(parents, 4) || !seqlens || !aligned(seqlens, 4) || !free_count ||
+        !aligned(free_count, 4) || (num_pages > 0 && !free_pages) || !aligned(free_pages, 4) ||
+        (max_pages > 0 && !block_table) || !aligned(block_table, 4) || !copies || !aligned(copies, 4) ||
+        !aligned(granted, 4))
+        return FD_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < l.total || !aligned(workspace, 256))
+        return FD_ERR_WORKSPACE;
+    ReorderParams p;
+    memset(&p, 0, sizeof p);
+    p.parents = parents;
+    p.R = R;
+    p.W = W;
+    p.seqlens = seqlens;
+    p.table = block_table;
+    p.max_pages = max_pages;
+    p.page_size = page_size;
+    p.free_pages = free_pages;
+    p.free_count = free_count;
+    p.num_pages = num_pages;
+    p.copies = copies;
+    p.granted = granted;
+    p.status = status_ptr();
+    if (!p.status)
+        return FD_ERR_CUDA;
+    char *ws = static_cast<char *>(workspace);
+    p.tiles = l.tiles;
+    p.header = reinterpret_cast<ReorderHeader *>(ws);
+    p.freed = reinterpret_cast<int32_t *>(ws + l.freed);
+    p.freed_before = reinterpret_cast<long long *>(ws + l.freed_before);
+    p.needed = reinterpret_cast<int32_t *>(ws + l.needed);
+    p.needed_before = reinterpret_cast<int32_t *>(ws + l.needed_before);
+    return launch_reorder(p, stream_of(stream)) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
+}
+
+fd_status fd_copy_pages(const int32_t *copies, int n, int Hkv, int d, fd_dtype dtype, void *k_pages, void *v_pages,
+                        int page_size, long long num_pages, void *stream)
+{
+    if (n < 0 || Hkv < 0 || page_size < 1 || num_pages < 0 || d < 1 || num_pages > INT_MAX / page_size ||
+        (long long)Hkv * d > INT_MAX)
+        return FD_ERR_INVALID_ARG;
+    if ((dtype != FD_F32 && dtype != FD_E4M3 && !is16(dtype)) || (d != 64 && d != 128 && d != 256))
+        return FD_ERR_UNSUPPORTED;
+    if (n == 0 || Hkv == 0)
+        return FD_OK;
+    if (!copies || !aligned(copies, 4) || !k_pages || !v_pages || !aligned(k_pages, 16) || !aligned(v_pages, 16))
+        return FD_ERR_INVALID_ARG;
+    CopyParams p;
+    memset(&p, 0, sizeof p);
+    p.copies = copies;
+    p.n = n;
+    p.H = Hkv;
+    p.page_size = page_size;
+    p.row_vecs = d * (dtype == FD_F32 ? 4 : dtype == FD_E4M3 ? 1 : 2) / 16;
+    p.k_pages = k_pages;
+    p.v_pages = v_pages;
+    p.num_pages = num_pages;
+    p.status = status_ptr();
+    if (!p.status)
+        return FD_ERR_CUDA;
+    return launch_copy_pages(p, stream_of(stream)) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
+}
+
 }  // extern "C"

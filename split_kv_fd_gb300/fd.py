@@ -36,7 +36,7 @@ EXPORTS = ["fd_status_str", "fd_version", "fd_num_sms", "fd_auto_num_splits",
            "fd_selftest_wait_timeout", "fd_decode_gqa_paged", "fd_decode_gqa_fp8",
            "fd_decode_gqa_paged_fp8", "fd_resize_pages", "fd_append_paged", "fd_append_paged_fp8",
            "fd_append_rope_paged", "fd_append_rope_paged_fp8", "fd_workspace_size_extend", "fd_prefill", "fd_extend_paged", "fd_extend_paged_fp8",
-           "fd_workspace_size_beam", "fd_beam_select"]
+           "fd_workspace_size_beam", "fd_beam_select", "fd_workspace_size_reorder", "fd_reorder_pages", "fd_copy_pages"]
 
 _lock = threading.Lock()
 _lib = None
@@ -132,6 +132,12 @@ def load(build_if_missing: bool = False):
         lib.fd_workspace_size_beam.restype = S
         lib.fd_beam_select.argtypes = [P, I, L, L, P, P, I, I, I, I, I, P, P, P, P, P, S, P]
         lib.fd_beam_select.restype = I
+        lib.fd_workspace_size_reorder.argtypes = [I, I, I]
+        lib.fd_workspace_size_reorder.restype = S
+        lib.fd_reorder_pages.argtypes = [P, I, I, P, P, I, P, P, I, I, P, P, P, S, P]
+        lib.fd_reorder_pages.restype = I
+        lib.fd_copy_pages.argtypes = [P, I, I, I, I, P, P, I, L, P]
+        lib.fd_copy_pages.restype = I
         _lib = lib
         return lib
 
@@ -982,6 +988,81 @@ def beam_select(logits, scores, num=None, finished=None, eos=-1, workspace=None,
           _address(finished), R, W, V, K, eos, out.data_ptr(), parents.data_ptr(), tokens.data_ptr(), over.data_ptr(),
           workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out, parents, tokens, over
+
+
+def workspace_size_reorder(R, W, max_pages) -> int:
+    """Bytes of workspace reorder_pages needs."""
+    return load().fd_workspace_size_reorder(R, W, max_pages)
+
+
+def reorder_pages(parents, seqlens, block_table, free_pages, free_count, page_size, copies=None, granted=None, workspace=None,
+                  stream=None):
+    """The beams' cached states to those of their parents, in place
+    (fd_reorder_pages).  Returns ``(copies, granted)``; ``copy_pages`` has to
+    make the copies in each layer's pages.
+
+    parents int32 [R, W]: of every beam the beam of its request that it goes on
+    from, negative where it ends.  Beam w of request r is sequence r*W + w:
+    seqlens int32 [R*W] (or [R, W]); block_table int32 [R*W, max_pages];
+    free_pages int32 [num_pages] and free_count int32 [1], the stack of
+    resize_pages.  copies int32 [R*W, 3]: page from, page to and rows, -1, -1
+    and 0 without a copy; granted int32 [R]: 0 where pages were missing and the
+    request stays as it was.
+    """
+    dev = _one_device(parents, seqlens, block_table, free_pages, free_count, copies, granted)
+    if parents.dim() != 2 or block_table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("parents [R, W], block_table [R*W, max_pages], free_pages [num_pages]")
+    R, W = parents.shape
+    B, width, pool = R * W, block_table.shape[1], free_pages.shape[0]
+    if abs(page_size) > INT_MAX:
+        raise ValueError("page_size must be below 2^31")
+    _int32(parents, (R, W), "parents")
+    _int32(seqlens, (R, W) if seqlens.dim() == 2 else (B,), "seqlens")
+    _int32(block_table, (B, width), "block_table")
+    _int32(free_pages, (pool,), "free_pages")
+    _int32(free_count, (1,), "free_count")
+    where = parents.device
+    if copies is None:
+        copies = _empty(stream, (B, 3), dtype=torch.int32, device=where)
+    else:
+        _int32(copies, (B, 3), "copies")
+    if granted is None:
+        granted = _empty(stream, R, dtype=torch.int32, device=where)
+    else:
+        _int32(granted, (R,), "granted")
+    if workspace is None:
+        workspace = _empty(stream, max(workspace_size_reorder(R, W, width), 256), dtype=torch.uint8, device=where)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on the parents' device")
+    _call("fd_reorder_pages", dev, stream, parents.data_ptr(), R, W, seqlens.data_ptr(), block_table.data_ptr(), width,
+          free_pages.data_ptr(), free_count.data_ptr(), pool, page_size, copies.data_ptr(), granted.data_ptr(),
+          workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return copies, granted
+
+
+def copy_pages(copies, k_pages, v_pages, stream=None):
+    """Rows of pages to other pages, in place (fd_copy_pages): the copies that
+    reorder_pages asks for, of one layer.
+
+    copies int32 [n, 3]: page from, page to, rows; k_pages/v_pages [num_pages,
+    Hkv, page_size, d] float32, float16, bfloat16 or float8_e4m3fn (or uint8
+    E4M3 bytes).
+    """
+    dev = _one_device(copies, k_pages, v_pages)
+    if copies.dim() != 2:
+        raise ValueError("copies must be int32 [n, 3]")
+    _int32(copies, (copies.shape[0], 3), "copies")
+    _whole(k_pages, v_pages)
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype:
+        raise ValueError("k_pages/v_pages must be [num_pages, Hkv, page_size, d]")
+    kind = 3 if k_pages.dtype in (torch.float8_e4m3fn, torch.uint8) else DTYPE_CODE.get(k_pages.dtype)
+    if kind is None:
+        raise ValueError("pages must be float32/float16/bfloat16/float8_e4m3fn (or uint8 E4M3 bytes)")
+    num_pages, Hkv, page_size, d = k_pages.shape
+    if max(Hkv, page_size, d) > INT_MAX:
+        raise ValueError("pages: sizes must be below 2^31")
+    _call("fd_copy_pages", dev, stream, copies.data_ptr(), copies.shape[0], Hkv, d, kind, k_pages.data_ptr(),
+          v_pages.data_ptr(), page_size, num_pages)
 
 
 def decode_split(q, k, v, num_splits, seqlens=None, scale=None, stream=None, o_part=None,

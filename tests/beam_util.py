@@ -80,3 +80,101 @@ def check_select(got, logits, scores, num, finished=None, eos=-1):
             assert torch.equal(f, at[r, :n]), f"request {r}: {f.tolist()} for {at[r, :n].tolist()}"
             same += 1
     return same
+
+
+def reorder_ref(parents, lens, table, free, count, page, num_pages=None):
+    """fd_reorder_pages by plain loops, on lists.  parents [R][W], lens and
+    table by sequence.  Returns lens, table, free, count, copies, granted."""
+    R, W = len(parents), len(parents[0])
+    lens, table, free = list(lens), [list(t) for t in table], list(free)
+    pages = lambda n: -(-n // page)   # noqa: E731
+    plans = []
+    for r in range(R):
+        rows = range(r * W, (r + 1) * W)
+        new = [(table[r * W + q][: pages(lens[r * W + q])], lens[r * W + q]) if 0 <= q < W else ([], 0) for q in parents[r]]
+        width = max((pages(lens[b]) for b in rows), default=0)
+        freed = []
+        for j in range(width):
+            named = {t[j] for t, _ in new if j < len(t)}
+            for b in rows:
+                if j < pages(lens[b]) and table[b][j] not in named:
+                    named.add(table[b][j])
+                    freed.append(table[b][j])
+        copies = []   # (beam, place, rows)
+        for w, (t, n) in enumerate(new):
+            if n % page:
+                j = n // page
+                for v, (u, m) in enumerate(new):
+                    if v != w and j < len(u) and u[j] == t[j] and (m // page > j or v < w):
+                        copies.append((w, j, n % page))
+                        break
+        plans.append((new, freed, copies))
+    short = [max(0, len(c) - len(f)) for _, f, c in plans]
+    left = count + sum(max(0, len(f) - len(c)) for _, f, c in plans)
+    granted, used = [], 0
+    for s in short:
+        used += s
+        granted.append(int(s == 0 or used <= left))
+    back = [p for (_, f, _), g in zip(plans, granted) if g for p in f]
+    for p in reversed(back):
+        free[count] = p
+        count += 1
+    out = [[-1, -1, 0] for _ in range(R * W)]
+    for r, (new, _, copies) in enumerate(plans):
+        if not granted[r]:
+            continue
+        for w, (t, n) in enumerate(new):
+            table[r * W + w][: len(t)] = t
+            lens[r * W + w] = n
+        for w, j, n in copies:
+            count -= 1
+            out[r * W + w] = [table[r * W + w][j], free[count], n]
+            table[r * W + w][j] = free[count]
+    return lens, table, free, count, out, granted
+
+
+class BeamPool:
+    """A pool of pages, and requests whose beams grew by steps of choosing and
+    writing: a state as a search leaves it, on lists."""
+
+    def __init__(self, rng, R, W, page, width, prompt, grown, spare, ragged=False):
+        self.R, self.W, self.page, self.width = R, W, page, width
+        self.table = [[rng.randrange(-9, 99) for _ in range(width)] for _ in range(R * W)]   # what lies behind the lengths
+        self.lens = [0] * (R * W)
+        cap = width * page
+        plan = []
+        for r in range(R):
+            n = min(cap, rng.randint(*prompt))
+            plan.append((n, min(cap - n, rng.randint(*grown))))
+        self.pool = sum(-(-n // page) + W * (2 + -(-g // page)) for n, g in plan) + spare + 1
+        ids = list(range(self.pool))
+        rng.shuffle(ids)
+        self.free, self.count = ids, self.pool
+        for r, (n, g) in enumerate(plan):
+            self._grow(r * W, n)
+            self.step([[0] * W if q == r else list(range(W)) for q in range(R)])
+            left = g
+            while left > 0:
+                move = min(left, rng.randint(1, max(1, page // 2)))
+                for w in range(W):
+                    if not (ragged and rng.random() < 0.2):
+                        self._grow(r * W + w, self.lens[r * W + w] + move)
+                self.step([[rng.randrange(W) for _ in range(W)] if q == r else list(range(W)) for q in range(R)])
+                left -= move
+        for _ in range(max(0, self.count - spare)):   # no more are free than asked for
+            self.count -= 1
+            self.free[self.count] = -1
+
+    def _grow(self, b, n):
+        for j in range(-(-self.lens[b] // self.page), -(-n // self.page)):
+            self.count -= 1
+            self.table[b][j] = self.free[self.count]
+        self.lens[b] = n
+
+    def step(self, parents):
+        self.lens, self.table, self.free, self.count, _, granted = reorder_ref(parents, self.lens, self.table, self.free, self.count, self.page)
+        assert all(granted)
+
+    def tensors(self, device="cuda"):
+        i = lambda x: torch.tensor(x, dtype=torch.int32, device=device)   # noqa: E731
+        return i(self.lens), i(self.table).view(self.R * self.W, self.width), i(self.free), i([self.count])
