@@ -13,8 +13,10 @@ constexpr int BEAM_MAX_K = 64;   // candidates chosen of them
 
 // A row of logits is cut into segments of SEG_BYTES, counted from the 16-byte
 // boundary at or below its first element.
-constexpr int SEG_BYTES = 2048;
+constexpr int SEG_BYTES = 512;
+constexpr int SEL_SEGS = 4;       // segments that a warp reads at a time
 constexpr int SEL_THREADS = 256;
+constexpr int SEL_CTAS = 5;       // of the rows' kernel on an SM
 
 struct SelectParams {
     const void *logits;          // [R, W, V], strides in elements
@@ -29,7 +31,7 @@ struct SelectParams {
     // workspace: of every row the largest value of each segment, and the
     // maximum and sum of exponentials of each part
     int segs;                    // segments of a row
-    int per_part, parts;         // segments of a part, parts of a row
+    int run, parts;              // times SEL_SEGS segments: a part; parts of a row
     float *seg_max;              // [R * W, segs]
     float2 *part;                // [R * W, parts]
 };

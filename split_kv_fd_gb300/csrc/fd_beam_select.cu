@@ -5,14 +5,15 @@
 //
 // Memory bounds it: the logits are read once.  Two kernels.
 //
-// 1. Rows: a warp reads a segment of 2 KB at a time, and keeps the running
-//    maximum m and sum s of exp(x - m) of its segments, and each segment's
-//    maximum.  No candidate is looked for.
+// 1. Rows: a warp reads 2 KB of a row at a time, and keeps the running maximum
+//    m and sum s of exp(x - m), and the maximum of each segment of 512 bytes.
+//    No candidate is looked for.
 // 2. Top: a CTA a request joins the parts' (m, s) and with them brings the
 //    segments' maxima of all its beams to one scale.  The K segments with the
 //    largest of them hold the K best continuations: one outside has K others
 //    before it, each of which has an element at least as large (or as large,
-//    and of a lower index).  Only these K segments are read again.
+//    and of a lower index).  Only some K segments are read again, and the K-th
+//    largest maximum is a bound that few of their elements reach.
 //
 // Across beams the order is decided by sums in two float32 parts, close to 48
 // bits, so that only the sum of exponentials is rounded to less: neighbours
@@ -28,18 +29,12 @@ namespace {
 
 constexpr int ST = SEL_THREADS;
 constexpr int SW = ST / 32;
-constexpr int SEG_VECS = SEG_BYTES / 16;   // 16-byte vectors of a segment
-constexpr int U = SEG_VECS / 32;           // of a lane
+constexpr int SEG_VECS = SEG_BYTES / 16;   // 16-byte vectors of a segment, one a lane
+static_assert(SEG_VECS == 32, "a warp reads a segment with one load");
+constexpr int U = SEL_SEGS;                // segments that a warp reads at a time
 constexpr float LOG2E = 1.4426950408889634f;
 
 __device__ __forceinline__ float minus_inf() { return __int_as_float(0xff800000); }
-
-__device__ __forceinline__ float exp2_fast(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // A logit as the definition takes it: NaN is no candidate (-inf), and +inf
 // the largest finite value.
@@ -97,10 +92,46 @@ template <typename T> __device__ __forceinline__ uint4 load_part(const T *base, 
 
 __device__ __forceinline__ float warp_max(float x)
 {
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-        x = fmaxf(x, __shfl_xor_sync(FULL_MASK, x, o));
-    return x;
+    float y;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The largest element of a vector (of a NaN and a number, the number).
+__device__ __forceinline__ float vec_max(const uint4 &x, const float *)
+{
+    return fmaxf(fmaxf(__uint_as_float(x.x), __uint_as_float(x.y)), fmaxf(__uint_as_float(x.z), __uint_as_float(x.w)));
+}
+template <typename T2> __device__ __forceinline__ T2 max2(uint32_t a, uint32_t b)
+{
+    T2 x, y;
+    memcpy(&x, &a, 4);
+    memcpy(&y, &b, 4);
+    return __hmax2(x, y);
+}
+__device__ __forceinline__ float vec_max(const uint4 &x, const __half *)
+{
+    const float2 f = __half22float2(__hmax2(max2<__half2>(x.x, x.y), max2<__half2>(x.z, x.w)));
+    return fmaxf(f.x, f.y);
+}
+__device__ __forceinline__ float vec_max(const uint4 &x, const __nv_bfloat16 *)
+{
+    const float2 f = __bfloat1622float2(__hmax2(max2<__nv_bfloat162>(x.x, x.y), max2<__nv_bfloat162>(x.z, x.w)));
+    return fmaxf(f.x, f.y);
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
 
 // A row of logits: its address rounded down to 16 bytes, and where its
@@ -117,55 +148,66 @@ template <typename T> struct Place {
     }
 };
 
-__device__ __forceinline__ bool is_live(const SelectParams &p, int row)
+__device__ __forceinline__ bool is_live(const SelectParams &p, long long row)
 {
     return isfinite(p.scores[row]) && !(p.finished && p.finished[row]);
 }
 
-template <typename T> __global__ void __launch_bounds__(ST) rows_kernel(const SelectParams p)
+// A warp a part of a row: `run` times U segments.
+template <typename T> __global__ void __launch_bounds__(ST, SEL_CTAS) rows_kernel(const SelectParams p)
 {
     constexpr int VE = Row<T>::VE, SEG = SEG_VECS * VE;
-    const int row = blockIdx.x / p.parts, part = blockIdx.x % p.parts;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (!is_live(p, row))
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int lane = threadIdx.x & 31;
+    const long long me = blockIdx.x * (long long)SW + (threadIdx.x >> 5);
+    const long long row = me / p.parts;
+    const int part = (int)(me - row * p.parts);
+    if (row >= (long long)p.R * p.W || !is_live(p, row))
         return;
-    const Place<T> at(p, row / p.W, row % p.W);
+    const int r = (int)(row / p.W);
+    const Place<T> at(p, r, (int)(row - (long long)r * p.W));
+    float *seg_max = p.seg_max + row * p.segs;
     float m = minus_inf(), s = 0.f;
-    const int s1 = min((part + 1) * p.per_part, p.segs);
-    for (int g = part * p.per_part + warp; g < s1; g += SW) {
+    const int g1 = min((part + 1) * p.run * U, p.segs);
+    for (int g = part * p.run * U; g < g1; g += U) {
         uint4 x[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            x[u] = load_part(at.base, (long long)g * SEG + (u * 32 + lane) * VE, at.first, at.end);
-        float top = minus_inf();
+            x[u] = load_part(at.base, (long long)(g + u) * SEG + lane * VE, at.first, at.end);
+        float top = minus_inf(), mine = top;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            float f[VE];
-            Elem<T>::widen(x[u], f);
-#pragma unroll
-            for (int i = 0; i < VE; ++i)
-                top = fmaxf(top, f[i]);   // (of a NaN and a number, the number)
+            // (+inf counts as the largest finite value, NaN as -inf)
+            const float t = fminf(fmaxf(warp_max(vec_max(x[u], (const T *)nullptr)), minus_inf()), FLT_MAX);
+            mine = lane == u ? t : mine;
+            top = fmaxf(top, t);
         }
-        top = fminf(warp_max(top), FLT_MAX);
-        if (lane == 0)
-            p.seg_max[(long long)row * p.segs + g] = top;
+        if (lane < U && g + lane < p.segs)
+            seg_max[g + lane] = mine;
         if (top == minus_inf())
             continue;
         if (top > m) {
-            s *= exp2_fast((m - top) * LOG2E);
+            s *= ex2((m - top) * LOG2E);
             m = top;
         }
-        float sum = 0.f;
+        // exp(x - m), two at a time
+        const uint64_t minus_m = pack2(-m, -m), scale = pack2(LOG2E, LOG2E);
+        uint64_t sum2 = 0;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             float f[VE];
             Elem<T>::widen(x[u], f);
 #pragma unroll
-            for (int i = 0; i < VE; ++i)
-                sum += exp2_fast((f[i] - m) * LOG2E);
+            for (int i = 0; i < VE; i += 2) {
+                float a, b;
+                unpack2(mul2(add2(pack2(f[i], f[i + 1]), minus_m), scale), a, b);
+                sum2 = add2(sum2, pack2(ex2(a), ex2(b)));
+            }
         }
-        // a NaN or +inf among them: once more, as the definition takes them
-        if (!(sum <= FLT_MAX)) {
+        float a, b;
+        unpack2(sum2, a, b);
+        float sum = a + b;
+        if (!(sum <= FLT_MAX)) {   // a NaN or +inf among them: once more, as the definition takes them
             sum = 0.f;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -173,7 +215,7 @@ template <typename T> __global__ void __launch_bounds__(ST) rows_kernel(const Se
                 Elem<T>::widen(x[u], f);
 #pragma unroll
                 for (int i = 0; i < VE; ++i)
-                    sum += exp2_fast((sane(f[i]) - m) * LOG2E);
+                    sum += ex2((sane(f[i]) - m) * LOG2E);
             }
         }
         s += sum;
@@ -181,20 +223,8 @@ template <typename T> __global__ void __launch_bounds__(ST) rows_kernel(const Se
 #pragma unroll
     for (int o = 16; o; o >>= 1)
         s += __shfl_xor_sync(FULL_MASK, s, o);
-    __shared__ float2 warps[SW];
     if (lane == 0)
-        warps[warp] = make_float2(m, s);
-    __syncthreads();
-    if (warp == 0) {
-        const float2 v = lane < SW ? warps[lane] : make_float2(minus_inf(), 0.f);
-        m = warp_max(v.x);
-        s = v.y > 0.f ? v.y * exp2_fast((v.x - m) * LOG2E) : 0.f;
-#pragma unroll
-        for (int o = 16; o; o >>= 1)
-            s += __shfl_xor_sync(FULL_MASK, s, o);
-        if (lane == 0)
-            p.part[blockIdx.x] = make_float2(m, s);
-    }
+        p.part[me] = make_float2(m, s);
 }
 
 // ------------------------------------------------------------------ top
@@ -239,6 +269,7 @@ __device__ __forceinline__ uint64_t value_key(const Base &b, float v)
 
 constexpr int CHUNK = 8 * ST;               // keys that are offered between two looks at the list
 constexpr int ROOM = CHUNK + BEAM_MAX_K;
+constexpr int MAX_SEGS = 1024;              // segments that are looked through without a second thought
 
 struct Lists {
     Cand a[ROOM];
@@ -247,6 +278,8 @@ struct Lists {
     Cand edge;      // nothing behind it is wanted
     int n, nb;
 };
+static_assert(sizeof(Cand[BEAM_MAX_K * ((ROOM + ST - 1) / ST)]) >= MAX_SEGS * sizeof(int), "the segments lie in `b`");
+static_assert(sizeof(Cand[ST]) >= ST * sizeof(float), "the threads' largest maxima lie in `best`");
 
 // Adds this thread's candidate to the list (every thread of the warp calls).
 __device__ __forceinline__ void offer(Lists &l, uint64_t key, int idx, const Cand &edge)
@@ -315,66 +348,47 @@ __device__ __forceinline__ void prune(Lists &l, int K)
     __syncthreads();
 }
 
-template <typename T> __global__ void __launch_bounds__(ST) top_kernel(const SelectParams p)
+// ln(s + e) in two parts, e what rounding cut off s: s = 2^k f with f in
+// [0.75, 1.5), k ln 2 by two parts of ln 2, of which the first has so few bits
+// that its product is exact (Cody and Waite), and ln f, whose half step is
+// 2^-26 there.
+__device__ __forceinline__ void log2parts(float s, float e, float &hi, float &lo)
+{
+    const int k = (__float_as_int(s) - 0x3f400000) >> 23;
+    const float f = __int_as_float(__float_as_int(s) - (k << 23));
+    constexpr float LN2_HI = 0x1.62e4p-1f, LN2_LO = (float)(0.693147180559945309417 - 0x1.62e4p-1);
+    const float a = (float)k * LN2_HI, b = logf(f);
+    hi = a + b;
+    const float z = hi - a;
+    lo = (a - (hi - z)) + (b - z) + ((float)k * LN2_LO + __fdividef(e, s));
+}
+
+// The K best where the bound leaves too many: the list is pruned whenever it
+// is full.  (Every thread of the block calls.)
+template <typename T>
+__device__ __noinline__ void top_of_many(const SelectParams &p, Lists &l, const Base *base, int *seg)
 {
     constexpr int VE = Row<T>::VE, SEG = SEG_VECS * VE;
-    __shared__ Lists l;
-    __shared__ Base base[BEAM_MAX_W];
-    __shared__ bool live[BEAM_MAX_W];
-    __shared__ int seg[BEAM_MAX_K];   // w * segs + segment
-    __shared__ int nsegs;
-    const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int row0 = r * p.W;
-
-    // the beams' scales, a warp a beam
-    for (int w = warp; w < p.W; w += SW) {
-        const int row = row0 + w;
-        bool ok = is_live(p, row);
-        float m = minus_inf();
-        double s = 0.0;
-        if (ok) {
-            const float2 *part = p.part + (long long)row * p.parts;
-            for (int i = lane; i < p.parts; i += 32)
-                m = fmaxf(m, part[i].x);
-            m = warp_max(m);
-            for (int i = lane; i < p.parts; i += 32) {
-                const float2 v = part[i];
-                if (v.y > 0.f)
-                    s += (double)(v.y * expf(v.x - m));
-            }
-#pragma unroll
-            for (int o = 16; o; o >>= 1)
-                s += __shfl_xor_sync(FULL_MASK, s, o);
-            ok = m > minus_inf();
-        }
-        if (lane == 0) {
-            live[w] = ok;
-            if (ok) {
-                const double b = (double)p.scores[row] - log(s);
-                base[w].m = m;
-                base[w].hi = (float)b;
-                base[w].lo = (float)(b - (double)base[w].hi);
-            }
-        }
-    }
+    const int r = blockIdx.x, tid = threadIdx.x;
+    const long long row0 = (long long)r * p.W;
+    __syncthreads();
     if (tid == 0) {
         l.n = 0;
         l.edge = Cand{0, INT_MAX};
     }
     __syncthreads();
-
-    // the K segments with the largest maxima (a segment's index: its first element's)
+    // the K segments with the largest maxima (a segment's index stands for its first element's)
     const int all = p.W * p.segs;
     for (int g0 = 0; g0 < all; g0 += CHUNK) {
         const Cand edge = l.edge;
-#pragma unroll
+#pragma unroll 1
         for (int u = 0; u < CHUNK / ST; ++u) {
             const int g = g0 + u * ST + tid;
             uint64_t key = 0;
             if (g < all) {
                 const int w = g / p.segs;
-                if (live[w]) {
-                    const float v = p.seg_max[(long long)row0 * p.segs + g];
+                if (isfinite(base[w].m)) {
+                    const float v = p.seg_max[row0 * p.segs + g];
                     key = v > minus_inf() ? value_key(base[w], v) : 0;
                 }
             }
@@ -387,20 +401,12 @@ template <typename T> __global__ void __launch_bounds__(ST) top_kernel(const Sel
         seg[tid] = l.a[tid].idx;
     __syncthreads();
     if (tid == 0) {
-        nsegs = found;
         l.n = 0;
         // no element behind the K-th segment's largest is among the first K
         l.edge = Cand{found == p.K ? l.a[p.K - 1].key : 0, INT_MAX};
     }
     __syncthreads();
-
-    // a finished beam continues in one way, at no cost
-    if (warp == 0) {
-        const bool over = lane < p.W && p.finished && p.finished[row0 + lane];
-        const float score = lane < p.W ? p.scores[row0 + lane] : 0.f;
-        offer(l, over && isfinite(score) ? key_of(score, 0.f) : 0, lane * p.V + p.eos, Cand{0, INT_MAX});
-    }
-    const int vecs = nsegs * SEG_VECS;
+    const int vecs = found * SEG_VECS;
     for (int v0 = 0; v0 < vecs; v0 += ST) {
         // (as long as the list has room for a vector of every thread)
         __syncthreads();
@@ -426,6 +432,175 @@ template <typename T> __global__ void __launch_bounds__(ST) top_kernel(const Sel
         }
     }
     prune(l, p.K);
+}
+
+template <typename T> __global__ void __launch_bounds__(ST) top_kernel(const SelectParams p)
+{
+    constexpr int VE = Row<T>::VE, SEG = SEG_VECS * VE;
+    __shared__ __align__(16) Lists l;
+    __shared__ Base base[BEAM_MAX_W];
+    __shared__ float limit[BEAM_MAX_W];
+    __shared__ int seg[BEAM_MAX_K];   // w * segs + segment
+    __shared__ int nsegs;
+    __shared__ unsigned bound;
+    const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const long long row0 = (long long)r * p.W;
+    if (tid == 0) {
+        l.n = nsegs = 0;
+        bound = ~0u;
+    }
+    // (scores and flags are older than the rows' kernel)
+    bool over = false;
+    float score = 0.f;
+    if (lane < p.W) {
+        score = p.scores[row0 + lane];
+        over = p.finished && p.finished[row0 + lane];
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    // the beams' scales, a warp a beam
+    for (int w = warp; w < p.W; w += SW) {
+        const float sc = __shfl_sync(FULL_MASK, score, w);
+        const bool done = __shfl_sync(FULL_MASK, (int)over, w);
+        float m = minus_inf(), s = 0.f, e = 0.f;
+        if (isfinite(sc) && !done) {
+            const float2 *part = p.part + (row0 + w) * p.parts;
+            for (int i = lane; i < p.parts; i += 32)
+                m = fmaxf(m, part[i].x);
+            m = warp_max(m);
+            // sums with what their roundings cut off
+            for (int i = lane; i < p.parts; i += 32) {
+                const float2 v = part[i];
+                const float x = v.y > 0.f ? v.y * expf(v.x - m) : 0.f;
+                const float t = s + x, z = t - s;
+                e += (s - (t - z)) + (x - z);
+                s = t;
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) {
+                const float x = __shfl_xor_sync(FULL_MASK, s, o);
+                e += __shfl_xor_sync(FULL_MASK, e, o);
+                const float t = s + x, z = t - s;
+                e += (s - (t - z)) + (x - z);
+                s = t;
+            }
+        }
+        if (lane == 0) {
+            Base b = {__int_as_float(0x7f800000), 0.f, 0.f};   // m = inf: no element is a candidate
+            if (m > minus_inf()) {
+                float hi, lo;
+                log2parts(s, e, hi, lo);
+                b.m = m;
+                b.hi = sc - hi;
+                const float z = b.hi - sc;
+                b.lo = ((sc - (b.hi - z)) + (-hi - z)) - lo;
+            }
+            base[w] = b;
+        }
+    }
+    __syncthreads();
+
+    // The K-th largest of the threads' largest maxima, roughly: K segments and
+    // so K elements reach it.
+    const int all = p.W * p.segs;
+    const float *seg_max = p.seg_max + row0 * p.segs;
+    const int dw = ST / p.segs, di = ST - dw * p.segs;   // a thread's step through beams and segments
+    float top = minus_inf();
+    {
+        int w = tid / p.segs, i = tid - w * p.segs;
+#pragma unroll 8
+        for (int g = tid; g < all; g += ST) {
+            top = fmaxf(top, (seg_max[g] - base[w].m) + base[w].hi);   // (NaN where no beam wrote: not taken)
+            w += dw;
+            if ((i += di) >= p.segs)
+                i -= p.segs, ++w;
+        }
+    }
+    float *tops = reinterpret_cast<float *>(l.best);
+    tops[tid] = top;
+    __syncthreads();
+    {
+        int larger = 0;
+        const float4 *t4 = reinterpret_cast<const float4 *>(tops);
+#pragma unroll 16
+        for (int i = 0; i < ST / 4; ++i) {
+            const float4 t = t4[i];
+            larger += (t.x > top) + (t.y > top) + (t.z > top) + (t.w > top);
+        }
+        const unsigned lowest = __reduce_min_sync(FULL_MASK, larger < p.K ? ordered(top) : ~0u);
+        if (lane == 0)
+            atomicMin(&bound, lowest);
+    }
+    __syncthreads();
+    // What a beam's logit must reach.  With the rounding of these sums (some
+    // steps of each of their terms) on the safe side.
+    const float thr = unordered(bound);
+    if (tid < p.W) {
+        const Base b = base[tid];
+        const float need = thr - b.hi;
+        const float slack = 0x1p-20f * fabsf(thr) + 0x1p-20f * fabsf(b.hi) + 0x1p-20f * fabsf(b.m) + 0x1p-20f * fabsf(need);
+        limit[tid] = !isfinite(b.m) ? b.m : thr > minus_inf() ? (b.m + need) - slack : minus_inf();
+    }
+    // a finished beam continues in one way, at no cost
+    if (warp == 0) {
+        const bool some = over && isfinite(score);
+        offer(l, some ? key_of(score, 0.f) : 0, lane * p.V + p.eos, Cand{0, INT_MAX});
+    }
+    __syncthreads();
+    int *list = reinterpret_cast<int *>(l.b);
+    {
+        int w = tid / p.segs, i = tid - w * p.segs;
+#pragma unroll 8
+        for (int g = tid; g < all; g += ST) {
+            const float v = seg_max[g];
+            if (v >= limit[w] && isfinite(v)) {
+                const int to = atomicAdd(&nsegs, 1);
+                if (to < MAX_SEGS)
+                    list[to] = w << 24 | i;
+            }
+            w += dw;
+            if ((i += di) >= p.segs)
+                i -= p.segs, ++w;
+        }
+    }
+    __syncthreads();
+    const int found = nsegs;
+    if (found <= MAX_SEGS) {
+        const int vecs = found * SEG_VECS;
+#pragma unroll 4
+        for (int v = tid; v < vecs; v += ST) {
+            const int g = list[v / SEG_VECS], w = g >> 24;
+            const Place<T> at(p, r, w);
+            const int i = (g & 0xffffff) * SEG + v % SEG_VECS * VE;
+            const uint4 x = load_part(at.base, i, at.first, at.end);
+            const float lim = limit[w];
+            if (vec_max(x, (const T *)nullptr) >= lim) {
+                float f[VE];
+                Elem<T>::widen(x, f);
+#pragma unroll
+                for (int k = 0; k < VE; ++k) {
+                    if (f[k] >= lim && f[k] > minus_inf()) {
+                        const uint64_t key = value_key(base[w], sane(f[k]));
+                        const int to = key ? atomicAdd(&l.n, 1) : ROOM;
+                        if (to < ROOM)
+                            l.a[to] = Cand{key, w * p.V + i + k - at.first};
+                    }
+                }
+            }
+        }
+    }
+    __syncthreads();
+    if (found > MAX_SEGS || l.n > ROOM) {
+        top_of_many<T>(p, l, base, seg);
+        // the finished beams once more, behind the others
+        if (warp == 0) {
+            const bool some = over && isfinite(score);
+            offer(l, some ? key_of(score, 0.f) : 0, lane * p.V + p.eos, Cand{0, INT_MAX});
+        }
+    } else if (tid == 0) {
+        l.edge = Cand{0, INT_MAX};
+    }
+    prune(l, p.K);
 
     for (int k = tid; k < p.K; k += ST) {
         const bool some = k < l.n;
@@ -442,9 +617,22 @@ template <typename T> __global__ void __launch_bounds__(ST) top_kernel(const Sel
 
 template <typename T> cudaError_t launch_t(const SelectParams &p, cudaStream_t s)
 {
-    rows_kernel<T><<<(unsigned)(p.R * p.W * p.parts), ST, 0, s>>>(p);
-    top_kernel<T><<<p.R, ST, 0, s>>>(p);
-    return cudaGetLastError();
+    const long long warps = (long long)p.R * p.W * p.parts;
+    rows_kernel<T><<<(unsigned)((warps + SW - 1) / SW), ST, 0, s>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess)
+        return e;
+    // its CTAs start while the rows' last ones end
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.R);
+    cfg.blockDim = dim3(ST);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, top_kernel<T>, p);
 }
 
 }  // namespace

@@ -552,7 +552,7 @@ namespace {
 // The parts of a selection and its workspace, for the type with the most
 // segments (`elem` bytes an element).
 struct SelectLayout {
-    int segs, per_part, parts;
+    int segs, run, parts;
     size_t part, total;
 };
 
@@ -566,12 +566,15 @@ SelectLayout select_layout(int R, int W, int V, int elem, int sms)
 {
     SelectLayout l;
     l.segs = select_segs(V, elem);
-    // A segment a warp; more where the card has 16 CTAs an SM without.
-    const int warps = SEL_THREADS / 32;
-    const long long most = ((long long)R * W * l.segs + warps - 1) / warps, want = 16LL * sms;
-    const long long rounds = most > want ? most / want : 1;
-    l.per_part = (int)(rounds * warps < l.segs ? rounds * warps : l.segs);
-    l.parts = (l.segs + l.per_part - 1) / l.per_part;
+    // As many warps as the card holds, if there is that much to read.
+    const int reads = (l.segs + SEL_SEGS - 1) / SEL_SEGS;   // of a row
+    const long long all = (long long)R * W * reads, warps = (long long)sms * SEL_CTAS * (SEL_THREADS / 32);
+    const long long least = (all + warps - 1) / warps;
+    l.run = (int)(least < 1 ? 1 : least < reads ? least : reads);
+    // (a row's last part is shorter: without this a few CTAs would wait for all others)
+    while (l.run > 1 && l.run < reads && (long long)R * W * ((reads + l.run - 1) / l.run) > warps)
+        ++l.run;
+    l.parts = (reads + l.run - 1) / l.run;
     l.part = round_up((size_t)R * W * l.segs * sizeof(float), 256);
     l.total = l.part + (size_t)R * W * l.parts * sizeof(float2);
     return l;
@@ -608,8 +611,6 @@ fd_status fd_beam_select(const void *logits, fd_dtype dtype, long long request_s
     if (sms <= 0)
         return FD_ERR_CUDA;
     const SelectLayout l = select_layout(R, W, V, elem, sms);
-    if ((long long)R * W * l.parts > INT_MAX)
-        return FD_ERR_UNSUPPORTED;   // too many rows for a grid
     if (!workspace || workspace_bytes < l.total || !aligned(workspace, 256))
         return FD_ERR_WORKSPACE;
     SelectParams p;
@@ -630,7 +631,7 @@ fd_status fd_beam_select(const void *logits, fd_dtype dtype, long long request_s
     p.out_tokens = out_tokens;
     p.out_finished = out_finished;
     p.segs = l.segs;
-    p.per_part = l.per_part;
+    p.run = l.run;
     p.parts = l.parts;
     p.seg_max = static_cast<float *>(workspace);
     p.part = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + l.part);
