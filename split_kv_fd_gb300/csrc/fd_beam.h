@@ -16,7 +16,8 @@ constexpr int BEAM_MAX_K = 64;   // candidates chosen of them
 constexpr int SEG_BYTES = 512;
 constexpr int SEL_SEGS = 4;       // segments that a warp reads at a time
 constexpr int SEL_THREADS = 256;
-constexpr int SEL_CTAS = 5;       // of the rows' kernel on an SM
+constexpr int SEL_CTAS = 4;       // of the rows' kernel on an SM
+constexpr int SEL_STAGES = 3;     // reads under way or taken, of a warp
 
 struct SelectParams {
     const void *logits;          // [R, W, V], strides in elements

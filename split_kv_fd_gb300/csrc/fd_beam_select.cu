@@ -63,26 +63,29 @@ template <> struct Row<__nv_bfloat16> {
     }
 };
 
+__device__ __forceinline__ uint4 load_vec(const uint4 *p)
+{
+    uint4 x;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                 : "l"(p));
+    return x;
+}
+
 // The vector of elements i .. i + VE - 1 of a row, of which only those in
 // [first, end) are the row's: the others are -inf and are not read.
-template <typename T> __device__ __forceinline__ uint4 load_part(const T *base, long long i, int first, int end)
+template <typename T> __device__ __forceinline__ uint4 load_part(const T *base, int i, int first, int end)
 {
     constexpr int VE = Row<T>::VE;
-    uint4 x;
-    if (i >= first && i + VE <= end) {
-        const uint4 *p = reinterpret_cast<const uint4 *>(base + i);
-        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                     : "l"(p));
-        return x;
-    }
+    if (i >= first && i + VE <= end)
+        return load_vec(reinterpret_cast<const uint4 *>(base + i));
     uint32_t w[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         uint32_t e[4 / sizeof(T)];
 #pragma unroll
         for (int j = 0; j < (int)(4 / sizeof(T)); ++j) {
-            const long long at = i + k * (int)(4 / sizeof(T)) + j;
+            const int at = i + k * (int)(4 / sizeof(T)) + j;
             e[j] = at >= first && at < end ? Row<T>::bits(base + at) : Row<T>::NONE;
         }
         w[k] = sizeof(T) == 4 ? e[0] : e[0] | e[4 / sizeof(T) - 1] << 16;
@@ -153,13 +156,28 @@ __device__ __forceinline__ bool is_live(const SelectParams &p, long long row)
     return isfinite(p.scores[row]) && !(p.finished && p.finished[row]);
 }
 
-// A warp a part of a row: `run` times U segments.
+// 16 bytes of a row to this thread's own place in shared memory.
+__device__ __forceinline__ void copy_ahead(uint4 *to, const uint4 *from)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All copies but those of the last N groups have landed.
+template <int N> __device__ __forceinline__ void copies_landed()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A warp a part of a row: `run` times U segments.  Those that lie within the
+// row are copied AHEAD of their turn, each 16 bytes by the thread that takes
+// them: no thread waits for another, and what is under way costs no register.
 template <typename T> __global__ void __launch_bounds__(ST, SEL_CTAS) rows_kernel(const SelectParams p)
 {
-    constexpr int VE = Row<T>::VE, SEG = SEG_VECS * VE;
+    constexpr int VE = Row<T>::VE, SEG = SEG_VECS * VE, STAGES = SEL_STAGES, AHEAD = STAGES - 1;
+    extern __shared__ uint4 stages[];   // [warp][stage][U][lane]
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int lane = threadIdx.x & 31;
-    const long long me = blockIdx.x * (long long)SW + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long me = blockIdx.x * (long long)SW + warp;
     const long long row = me / p.parts;
     const int part = (int)(me - row * p.parts);
     if (row >= (long long)p.R * p.W || !is_live(p, row))
@@ -167,23 +185,49 @@ template <typename T> __global__ void __launch_bounds__(ST, SEL_CTAS) rows_kerne
     const int r = (int)(row / p.W);
     const Place<T> at(p, r, (int)(row - (long long)r * p.W));
     float *seg_max = p.seg_max + row * p.segs;
-    float m = minus_inf(), s = 0.f;
-    const int g1 = min((part + 1) * p.run * U, p.segs);
-    for (int g = part * p.run * U; g < g1; g += U) {
-        uint4 x[U];
+    uint4 *mine = stages + warp * STAGES * U * 32 + lane;
+    const uint4 *from = reinterpret_cast<const uint4 *>(at.base) + lane;
+    const int g0 = part * p.run * U, g1 = min(g0 + p.run * U, p.segs);
+    auto within = [&](int g) { return g < g1 && g * SEG >= at.first && (g + U) * SEG <= at.end; };
+    auto ahead = [&](int g, int stage) {
+        if (within(g)) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            x[u] = load_part(at.base, (long long)(g + u) * SEG + lane * VE, at.first, at.end);
-        float top = minus_inf(), mine = top;
+            for (int u = 0; u < U; ++u)
+                copy_ahead(mine + (stage * U + u) * 32, from + (g + u) * SEG_VECS);
+        }
+        copies_issued();
+    };
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+        ahead(g0 + i * U, i);
+
+    float m = minus_inf(), s = 0.f;
+    int stage = 0;
+    for (int g = g0; g < g1; g += U) {
+        const int next = stage == 0 ? AHEAD : stage - 1;   // the stage that was taken last
+        ahead(g + AHEAD * U, next);
+        copies_landed<AHEAD>();
+        uint4 x[U];
+        if (within(g)) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                x[u] = mine[(stage * U + u) * 32];
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                x[u] = load_part(at.base, (g + u) * SEG + lane * VE, at.first, at.end);
+        }
+        stage = stage == AHEAD ? 0 : stage + 1;
+        float top = minus_inf(), seg = top;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            // (+inf counts as the largest finite value, NaN as -inf)
-            const float t = fminf(fmaxf(warp_max(vec_max(x[u], (const T *)nullptr)), minus_inf()), FLT_MAX);
-            mine = lane == u ? t : mine;
+            const float t = warp_max(vec_max(x[u], (const T *)nullptr));
+            seg = lane == u ? t : seg;
             top = fmaxf(top, t);
         }
         if (lane < U && g + lane < p.segs)
-            seg_max[g + lane] = mine;
+            seg_max[g + lane] = sane(seg);
+        top = fminf(top, FLT_MAX);
         if (top == minus_inf())
             continue;
         if (top > m) {
@@ -279,7 +323,6 @@ struct Lists {
     int n, nb;
 };
 static_assert(sizeof(Cand[BEAM_MAX_K * ((ROOM + ST - 1) / ST)]) >= MAX_SEGS * sizeof(int), "the segments lie in `b`");
-static_assert(sizeof(Cand[ST]) >= ST * sizeof(float), "the threads' largest maxima lie in `best`");
 
 // Adds this thread's candidate to the list (every thread of the warp calls).
 __device__ __forceinline__ void offer(Lists &l, uint64_t key, int idx, const Cand &edge)
@@ -434,20 +477,35 @@ __device__ __noinline__ void top_of_many(const SelectParams &p, Lists &l, const 
     prune(l, p.K);
 }
 
+// A request's k-th continuation: c, or none.  `ended`: the finished beams.
+__device__ __forceinline__ void emit(const SelectParams &p, int k, bool some, const Cand &c, unsigned ended)
+{
+    const long long to = (long long)blockIdx.x * p.K + k;
+    const int parent = some ? c.idx / p.V : -1, token = some ? c.idx - parent * p.V : -1;
+    p.out_scores[to] = some ? unordered((uint32_t)(c.key >> 32)) : minus_inf();
+    p.out_parents[to] = parent;
+    p.out_tokens[to] = token;
+    if (p.out_finished)
+        p.out_finished[to] = !some || token == p.eos || (ended >> parent & 1);
+}
+
 template <typename T> __global__ void __launch_bounds__(ST) top_kernel(const SelectParams p)
 {
     constexpr int VE = Row<T>::VE, SEG = SEG_VECS * VE;
+    constexpr int HELD = 16;          // maxima that a thread holds
     __shared__ __align__(16) Lists l;
     __shared__ Base base[BEAM_MAX_W];
-    __shared__ float limit[BEAM_MAX_W];
+    __shared__ __align__(16) float tops[ST];
     __shared__ int seg[BEAM_MAX_K];   // w * segs + segment
     __shared__ int nsegs;
-    __shared__ unsigned bound;
+    __shared__ unsigned bound, spread;
     const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long row0 = (long long)r * p.W;
     if (tid == 0) {
         l.n = nsegs = 0;
+        l.edge = Cand{0, INT_MAX};
         bound = ~0u;
+        spread = 0;
     }
     // (scores and flags are older than the rows' kernel)
     bool over = false;
@@ -456,26 +514,45 @@ template <typename T> __global__ void __launch_bounds__(ST) top_kernel(const Sel
         score = p.scores[row0 + lane];
         over = p.finished && p.finished[row0 + lane];
     }
+    const bool ends = over && isfinite(score);
+    const unsigned ended = __ballot_sync(FULL_MASK, over);
+    __syncthreads();
+    // a finished beam continues in one way, at no cost
+    if (warp == 0)
+        offer(l, ends ? key_of(score, 0.f) : 0, lane * p.V + p.eos, Cand{0, INT_MAX});
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    // the beams' scales, a warp a beam
+    // the segments' maxima, on their way while the beams' scales are computed
+    const int all = p.W * p.segs;
+    const float *seg_max = p.seg_max + row0 * p.segs;
+    float v[HELD];
+#pragma unroll
+    for (int u = 0; u < HELD; ++u)
+        v[u] = u * ST + tid < all ? seg_max[u * ST + tid] : minus_inf();
+
+    // the scales, a warp a beam
     for (int w = warp; w < p.W; w += SW) {
         const float sc = __shfl_sync(FULL_MASK, score, w);
         const bool done = __shfl_sync(FULL_MASK, (int)over, w);
         float m = minus_inf(), s = 0.f, e = 0.f;
         if (isfinite(sc) && !done) {
             const float2 *part = p.part + (row0 + w) * p.parts;
-            for (int i = lane; i < p.parts; i += 32)
-                m = fmaxf(m, part[i].x);
-            m = warp_max(m);
-            // sums with what their roundings cut off
-            for (int i = lane; i < p.parts; i += 32) {
-                const float2 v = part[i];
-                const float x = v.y > 0.f ? v.y * expf(v.x - m) : 0.f;
-                const float t = s + x, z = t - s;
-                e += (s - (t - z)) + (x - z);
-                s = t;
+            float2 x[4];   // (as many as most rows have, loaded at once)
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                x[u] = u * 32 + lane < p.parts ? part[u * 32 + lane] : make_float2(minus_inf(), 0.f);
+            float mine = fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x));
+            for (int i = 128 + lane; i < p.parts; i += 32)
+                mine = fmaxf(mine, part[i].x);
+            m = warp_max(mine);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                s += x[u].y > 0.f ? x[u].y * expf(x[u].x - m) : 0.f;
+            for (int i = 128 + lane; i < p.parts; i += 32) {
+                const float2 y = part[i];
+                s += y.y > 0.f ? y.y * expf(y.x - m) : 0.f;
             }
+            // the sum with what its roundings cut off
 #pragma unroll
             for (int o = 16; o; o >>= 1) {
                 const float x = __shfl_xor_sync(FULL_MASK, s, o);
@@ -494,131 +571,151 @@ template <typename T> __global__ void __launch_bounds__(ST) top_kernel(const Sel
                 b.hi = sc - hi;
                 const float z = b.hi - sc;
                 b.lo = ((sc - (b.hi - z)) + (-hi - z)) - lo;
+                atomicMax(&spread, __float_as_uint(fabsf(b.hi) * 0.5f + fabsf(m) * 0.5f));
             }
             base[w] = b;
         }
     }
     __syncthreads();
 
-    // The K-th largest of the threads' largest maxima, roughly: K segments and
-    // so K elements reach it.
-    const int all = p.W * p.segs;
-    const float *seg_max = p.seg_max + row0 * p.segs;
+    // All maxima on one scale, roughly.  (What no beam wrote gives -inf or
+    // NaN, and is not taken.)
     const int dw = ST / p.segs, di = ST - dw * p.segs;   // a thread's step through beams and segments
+    const int w0 = tid / p.segs, i0 = tid - w0 * p.segs;
     float top = minus_inf();
-    {
-        int w = tid / p.segs, i = tid - w * p.segs;
-#pragma unroll 8
-        for (int g = tid; g < all; g += ST) {
-            top = fmaxf(top, (seg_max[g] - base[w].m) + base[w].hi);   // (NaN where no beam wrote: not taken)
+    int w = w0, i = i0;
+#pragma unroll
+    for (int u = 0; u < HELD; ++u) {
+        if (u * ST + tid < all) {
+            v[u] = (v[u] - base[w].m) + base[w].hi;
+            top = fmaxf(top, v[u]);
             w += dw;
             if ((i += di) >= p.segs)
                 i -= p.segs, ++w;
         }
     }
-    float *tops = reinterpret_cast<float *>(l.best);
-    tops[tid] = top;
+    for (int g = HELD * ST + tid; g < all; g += ST) {
+        top = fmaxf(top, (seg_max[g] - base[w].m) + base[w].hi);
+        w += dw;
+        if ((i += di) >= p.segs)
+            i -= p.segs, ++w;
+    }
+    // The K-th largest of the largest ones of groups of four threads: K
+    // segments, and so K elements, reach it.  (Of single threads where K is
+    // more than half of the groups, whose last ones lie far down.)
+    const bool four = p.K <= ST / 8;
+    if (four) {
+        top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, 2));
+    }
+    if (!four || (lane & 3) == 0)
+        tops[four ? tid / 4 : tid] = top;
     __syncthreads();
     {
-        int larger = 0;
+        int larger[4] = {0, 0, 0, 0};
         const float4 *t4 = reinterpret_cast<const float4 *>(tops);
-#pragma unroll 16
-        for (int i = 0; i < ST / 4; ++i) {
+        const int n = four ? ST / 16 : ST / 4;
+#pragma unroll 8
+        for (int i = 0; i < n; ++i) {
             const float4 t = t4[i];
-            larger += (t.x > top) + (t.y > top) + (t.z > top) + (t.w > top);
+            larger[0] += t.x > top;
+            larger[1] += t.y > top;
+            larger[2] += t.z > top;
+            larger[3] += t.w > top;
         }
-        const unsigned lowest = __reduce_min_sync(FULL_MASK, larger < p.K ? ordered(top) : ~0u);
-        if (lane == 0)
+        const bool in = (larger[0] + larger[1]) + (larger[2] + larger[3]) < p.K;
+        const unsigned lowest = __reduce_min_sync(FULL_MASK, in ? ordered(top) : ~0u);
+        if (lane == 0 && lowest != ~0u)
             atomicMin(&bound, lowest);
     }
     __syncthreads();
-    // What a beam's logit must reach.  With the rounding of these sums (some
-    // steps of each of their terms) on the safe side.
-    const float thr = unordered(bound);
-    if (tid < p.W) {
-        const Base b = base[tid];
-        const float need = thr - b.hi;
-        const float slack = 0x1p-20f * fabsf(thr) + 0x1p-20f * fabsf(b.hi) + 0x1p-20f * fabsf(b.m) + 0x1p-20f * fabsf(need);
-        limit[tid] = !isfinite(b.m) ? b.m : thr > minus_inf() ? (b.m + need) - slack : minus_inf();
-    }
-    // a finished beam continues in one way, at no cost
-    if (warp == 0) {
-        const bool some = over && isfinite(score);
-        offer(l, some ? key_of(score, 0.f) : 0, lane * p.V + p.eos, Cand{0, INT_MAX});
-    }
-    __syncthreads();
+    // ... less what these sums may be off, some steps of each of their terms
+    const float kth = unordered(bound), size = __uint_as_float(spread);
+    const float thr = (kth - 0x1p-19f * fabsf(kth)) - 0x1p-18f * size;
     int *list = reinterpret_cast<int *>(l.b);
-    {
-        int w = tid / p.segs, i = tid - w * p.segs;
-#pragma unroll 8
-        for (int g = tid; g < all; g += ST) {
-            const float v = seg_max[g];
-            if (v >= limit[w] && isfinite(v)) {
-                const int to = atomicAdd(&nsegs, 1);
-                if (to < MAX_SEGS)
-                    list[to] = w << 24 | i;
-            }
+    auto wanted = [&](float x, int w, int i) {
+        if (x >= thr && x > minus_inf()) {
+            const int to = atomicAdd(&nsegs, 1);
+            if (to < MAX_SEGS)
+                list[to] = w << 24 | i;
+        }
+    };
+    w = w0, i = i0;
+#pragma unroll
+    for (int u = 0; u < HELD; ++u) {
+        if (u * ST + tid < all) {
+            wanted(v[u], w, i);
             w += dw;
             if ((i += di) >= p.segs)
                 i -= p.segs, ++w;
         }
+    }
+    for (int g = HELD * ST + tid; g < all; g += ST) {
+        wanted((seg_max[g] - base[w].m) + base[w].hi, w, i);
+        w += dw;
+        if ((i += di) >= p.segs)
+            i -= p.segs, ++w;
     }
     __syncthreads();
     const int found = nsegs;
     if (found <= MAX_SEGS) {
         const int vecs = found * SEG_VECS;
 #pragma unroll 4
-        for (int v = tid; v < vecs; v += ST) {
-            const int g = list[v / SEG_VECS], w = g >> 24;
+        for (int k = tid; k < vecs; k += ST) {
+            const int g = list[k / SEG_VECS], w = g >> 24;
             const Place<T> at(p, r, w);
-            const int i = (g & 0xffffff) * SEG + v % SEG_VECS * VE;
+            const int i = (g & 0xffffff) * SEG + k % SEG_VECS * VE;
             const uint4 x = load_part(at.base, i, at.first, at.end);
-            const float lim = limit[w];
-            if (vec_max(x, (const T *)nullptr) >= lim) {
+            const Base b = base[w];
+            const float need = thr - b.hi;
+            const float limit = (b.m + need) - (0x1p-20f * fabsf(b.m) + 0x1p-20f * fabsf(need));
+            if (vec_max(x, (const T *)nullptr) >= limit) {
                 float f[VE];
                 Elem<T>::widen(x, f);
 #pragma unroll
-                for (int k = 0; k < VE; ++k) {
-                    if (f[k] >= lim && f[k] > minus_inf()) {
-                        const uint64_t key = value_key(base[w], sane(f[k]));
+                for (int e = 0; e < VE; ++e) {
+                    if (f[e] >= limit && f[e] > minus_inf()) {
+                        const uint64_t key = value_key(b, sane(f[e]));
                         const int to = key ? atomicAdd(&l.n, 1) : ROOM;
                         if (to < ROOM)
-                            l.a[to] = Cand{key, w * p.V + i + k - at.first};
+                            l.a[to] = Cand{key, w * p.V + i + e - at.first};
                     }
                 }
             }
         }
     }
     __syncthreads();
-    if (found > MAX_SEGS || l.n > ROOM) {
+    const int n = l.n;
+    if (found > MAX_SEGS || n > ROOM) {
         top_of_many<T>(p, l, base, seg);
-        // the finished beams once more, behind the others
-        if (warp == 0) {
-            const bool some = over && isfinite(score);
-            offer(l, some ? key_of(score, 0.f) : 0, lane * p.V + p.eos, Cand{0, INT_MAX});
+        if (warp == 0)   // the finished beams once more, behind the others
+            offer(l, ends ? key_of(score, 0.f) : 0, lane * p.V + p.eos, Cand{0, INT_MAX});
+        prune(l, p.K);
+    } else if (n <= ST) {
+        if (tid < n) {
+            const Cand c = l.a[tid];
+            int rank = 0;
+            for (int j = 0; j < n; ++j)
+                rank += l.a[j].before(c.key, c.idx);
+            if (rank < p.K)
+                emit(p, rank, true, c, ended);
+        } else if (tid < p.K) {
+            emit(p, tid, false, Cand{0, 0}, ended);
         }
-    } else if (tid == 0) {
-        l.edge = Cand{0, INT_MAX};
+        return;
+    } else {
+        prune(l, p.K);
     }
-    prune(l, p.K);
-
-    for (int k = tid; k < p.K; k += ST) {
-        const bool some = k < l.n;
-        const int idx = some ? l.a[k].idx : -1;
-        const int parent = some ? idx / p.V : -1, token = some ? idx % p.V : -1;
-        const long long to = (long long)r * p.K + k;
-        p.out_scores[to] = some ? unordered((uint32_t)(l.a[k].key >> 32)) : minus_inf();
-        p.out_parents[to] = parent;
-        p.out_tokens[to] = token;
-        if (p.out_finished)
-            p.out_finished[to] = !some || token == p.eos || (p.finished && p.finished[row0 + parent]);
-    }
+    if (tid < p.K)
+        emit(p, tid, tid < l.n, l.a[tid], ended);
 }
 
 template <typename T> cudaError_t launch_t(const SelectParams &p, cudaStream_t s)
 {
     const long long warps = (long long)p.R * p.W * p.parts;
-    rows_kernel<T><<<(unsigned)((warps + SW - 1) / SW), ST, 0, s>>>(p);
+    constexpr int smem = ST * SEL_STAGES * U * 16;
+    static_assert(smem <= 48 * 1024, "no attribute is set");
+    rows_kernel<T><<<(unsigned)((warps + SW - 1) / SW), ST, smem, s>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
