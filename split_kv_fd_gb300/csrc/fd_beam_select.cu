@@ -123,6 +123,25 @@ __device__ __forceinline__ float vec_max(const uint4 &x, const __nv_bfloat16 *)
     return fmaxf(f.x, f.y);
 }
 
+// Element e of a vector (chosen, not indexed: it lies in registers).
+__device__ __forceinline__ uint32_t word_of(const uint4 &x, int i)
+{
+    return i < 2 ? (i == 0 ? x.x : x.y) : i == 2 ? x.z : x.w;
+}
+__device__ __forceinline__ float element(const uint4 &x, int e, const float *)
+{
+    return __uint_as_float(word_of(x, e));
+}
+__device__ __forceinline__ float element(const uint4 &x, int e, const __half *)
+{
+    return __half2float(__ushort_as_half((unsigned short)(word_of(x, e >> 1) >> (e & 1) * 16)));
+}
+__device__ __forceinline__ float element(const uint4 &x, int e, const __nv_bfloat16 *)
+{
+    const uint32_t w = word_of(x, e >> 1);
+    return __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16);
+}
+
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
 {
     uint64_t d;
@@ -501,12 +520,8 @@ template <typename T> __global__ void __launch_bounds__(ST) top_kernel(const Sel
     __shared__ unsigned bound, spread;
     const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long row0 = (long long)r * p.W;
-    if (tid == 0) {
-        l.n = nsegs = 0;
-        l.edge = Cand{0, INT_MAX};
-        bound = ~0u;
-        spread = 0;
-    }
+    Cand *few = l.best;               // the candidates, where the bound leaves no more than FEW
+    constexpr int FEW = ST;
     // (scores and flags are older than the rows' kernel)
     bool over = false;
     float score = 0.f;
@@ -516,31 +531,44 @@ template <typename T> __global__ void __launch_bounds__(ST) top_kernel(const Sel
     }
     const bool ends = over && isfinite(score);
     const unsigned ended = __ballot_sync(FULL_MASK, over);
-    __syncthreads();
     // a finished beam continues in one way, at no cost
-    if (warp == 0)
-        offer(l, ends ? key_of(score, 0.f) : 0, lane * p.V + p.eos, Cand{0, INT_MAX});
+    const unsigned ending = __ballot_sync(FULL_MASK, ends);
+    if (warp == 0 && ends)
+        few[__popc(ending & ((1u << lane) - 1))] = Cand{key_of(score, 0.f), lane * p.V + p.eos};
+    if (tid == 0) {
+        l.n = __popc(ending);
+        nsegs = 0;
+        bound = ~0u;
+        spread = 0;
+    }
+    __syncthreads();
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    // the segments' maxima, on their way while the beams' scales are computed
+    // The scales, a warp a beam; the segments' maxima are on their way
+    // meanwhile.
     const int all = p.W * p.segs;
     const float *seg_max = p.seg_max + row0 * p.segs;
     float v[HELD];
+    auto load_maxima = [&] {
 #pragma unroll
-    for (int u = 0; u < HELD; ++u)
-        v[u] = u * ST + tid < all ? seg_max[u * ST + tid] : minus_inf();
-
-    // the scales, a warp a beam
+        for (int u = 0; u < HELD; ++u)
+            v[u] = u * ST + tid < all ? seg_max[u * ST + tid] : minus_inf();
+    };
+    if (warp >= p.W)
+        load_maxima();
     for (int w = warp; w < p.W; w += SW) {
         const float sc = __shfl_sync(FULL_MASK, score, w);
         const bool done = __shfl_sync(FULL_MASK, (int)over, w);
         float m = minus_inf(), s = 0.f, e = 0.f;
-        if (isfinite(sc) && !done) {
-            const float2 *part = p.part + (row0 + w) * p.parts;
-            float2 x[4];   // (as many as most rows have, loaded at once)
+        const bool counts = isfinite(sc) && !done;
+        const float2 *part = p.part + (row0 + w) * p.parts;
+        float2 x[4];   // (as many as most rows have, loaded at once)
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                x[u] = u * 32 + lane < p.parts ? part[u * 32 + lane] : make_float2(minus_inf(), 0.f);
+        for (int u = 0; u < 4; ++u)
+            x[u] = counts && u * 32 + lane < p.parts ? part[u * 32 + lane] : make_float2(minus_inf(), 0.f);
+        if (w == warp)
+            load_maxima();
+        if (counts) {
             float mine = fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x));
             for (int i = 128 + lane; i < p.parts; i += 32)
                 mine = fmaxf(mine, part[i].x);
@@ -581,9 +609,8 @@ template <typename T> __global__ void __launch_bounds__(ST) top_kernel(const Sel
     // All maxima on one scale, roughly.  (What no beam wrote gives -inf or
     // NaN, and is not taken.)
     const int dw = ST / p.segs, di = ST - dw * p.segs;   // a thread's step through beams and segments
-    const int w0 = tid / p.segs, i0 = tid - w0 * p.segs;
+    int w = tid / p.segs, i = tid - w * p.segs;
     float top = minus_inf();
-    int w = w0, i = i0;
 #pragma unroll
     for (int u = 0; u < HELD; ++u) {
         if (u * ST + tid < all) {
@@ -594,6 +621,7 @@ template <typename T> __global__ void __launch_bounds__(ST) top_kernel(const Sel
                 i -= p.segs, ++w;
         }
     }
+    const int w1 = w, i1 = i;
     for (int g = HELD * ST + tid; g < all; g += ST) {
         top = fmaxf(top, (seg_max[g] - base[w].m) + base[w].hi);
         w += dw;
@@ -633,79 +661,100 @@ template <typename T> __global__ void __launch_bounds__(ST) top_kernel(const Sel
     const float kth = unordered(bound), size = __uint_as_float(spread);
     const float thr = (kth - 0x1p-19f * fabsf(kth)) - 0x1p-18f * size;
     int *list = reinterpret_cast<int *>(l.b);
-    auto wanted = [&](float x, int w, int i) {
-        if (x >= thr && x > minus_inf()) {
-            const int to = atomicAdd(&nsegs, 1);
-            if (to < MAX_SEGS)
-                list[to] = w << 24 | i;
-        }
-    };
-    w = w0, i = i0;
+    unsigned wanted = 0;
 #pragma unroll
-    for (int u = 0; u < HELD; ++u) {
-        if (u * ST + tid < all) {
-            wanted(v[u], w, i);
+    for (int u = 0; u < HELD; ++u)
+        wanted |= (v[u] >= thr && v[u] > minus_inf()) << u;
+    auto add = [&](int g) {
+        const int to = atomicAdd(&nsegs, 1);
+        const int w = g / p.segs;
+        if (to < MAX_SEGS)
+            list[to] = w << 24 | (g - w * p.segs);
+    };
+    for (; wanted; wanted &= wanted - 1)
+        add((__ffs(wanted) - 1) * ST + tid);
+    if (all > HELD * ST) {
+        w = w1, i = i1;
+        for (int g = HELD * ST + tid; g < all; g += ST) {
+            const float x = (seg_max[g] - base[w].m) + base[w].hi;
+            if (x >= thr && x > minus_inf())
+                add(g);
             w += dw;
             if ((i += di) >= p.segs)
                 i -= p.segs, ++w;
         }
     }
-    for (int g = HELD * ST + tid; g < all; g += ST) {
-        wanted((seg_max[g] - base[w].m) + base[w].hi, w, i);
-        w += dw;
-        if ((i += di) >= p.segs)
-            i -= p.segs, ++w;
-    }
     __syncthreads();
     const int found = nsegs;
     if (found <= MAX_SEGS) {
+        // A batch of segments' vectors, each to its thread's own place, all of
+        // them on their way before the first is looked at.
+        uint4 *stage = reinterpret_cast<uint4 *>(l.a);
+        constexpr int BATCH = sizeof(l.a) / (ST * 16) * ST;
         const int vecs = found * SEG_VECS;
-#pragma unroll 4
-        for (int k = tid; k < vecs; k += ST) {
-            const int g = list[k / SEG_VECS], w = g >> 24;
-            const Place<T> at(p, r, w);
-            const int i = (g & 0xffffff) * SEG + k % SEG_VECS * VE;
-            const uint4 x = load_part(at.base, i, at.first, at.end);
-            const Base b = base[w];
-            const float need = thr - b.hi;
-            const float limit = (b.m + need) - (0x1p-20f * fabsf(b.m) + 0x1p-20f * fabsf(need));
-            if (vec_max(x, (const T *)nullptr) >= limit) {
+        auto place = [&](int k, int &w, int &i) {
+            const int g = list[k / SEG_VECS];
+            w = g >> 24;
+            i = (g & 0xffffff) * SEG + k % SEG_VECS * VE;
+            return Place<T>(p, r, w);
+        };
+        for (int k0 = 0; k0 < vecs; k0 += BATCH) {
+            const int end = min(vecs, k0 + BATCH);
+            int w, i;
+#pragma unroll 1
+            for (int k = k0 + tid; k < end; k += ST) {
+                const Place<T> at = place(k, w, i);
+                if (i >= at.first && i + VE <= at.end)
+                    copy_ahead(stage + (k - k0), reinterpret_cast<const uint4 *>(at.base + i));
+                else
+                    stage[k - k0] = load_part(at.base, i, at.first, at.end);
+            }
+            copies_issued();
+            copies_landed<0>();
+#pragma unroll 1
+            for (int k = k0 + tid; k < end; k += ST) {
+                const Place<T> at = place(k, w, i);
+                const uint4 x = stage[k - k0];
+                const Base b = base[w];
+                const float need = thr - b.hi;
+                const float limit = (b.m + need) - (0x1p-20f * fabsf(b.m) + 0x1p-20f * fabsf(need));
+                unsigned some = 0;
                 float f[VE];
                 Elem<T>::widen(x, f);
 #pragma unroll
-                for (int e = 0; e < VE; ++e) {
-                    if (f[e] >= limit && f[e] > minus_inf()) {
-                        const uint64_t key = value_key(b, sane(f[e]));
-                        const int to = key ? atomicAdd(&l.n, 1) : ROOM;
-                        if (to < ROOM)
-                            l.a[to] = Cand{key, w * p.V + i + e - at.first};
-                    }
+                for (int e = 0; e < VE; ++e)
+                    some |= (f[e] >= limit && f[e] > minus_inf()) << e;
+                for (; some; some &= some - 1) {
+                    const int e = __ffs(some) - 1;
+                    const uint64_t key = value_key(b, sane(element(x, e, (const T *)nullptr)));
+                    const int to = key ? atomicAdd(&l.n, 1) : FEW;
+                    if (to < FEW)
+                        few[to] = Cand{key, w * p.V + i + e - at.first};
                 }
             }
         }
     }
     __syncthreads();
     const int n = l.n;
-    if (found > MAX_SEGS || n > ROOM) {
-        top_of_many<T>(p, l, base, seg);
-        if (warp == 0)   // the finished beams once more, behind the others
-            offer(l, ends ? key_of(score, 0.f) : 0, lane * p.V + p.eos, Cand{0, INT_MAX});
-        prune(l, p.K);
-    } else if (n <= ST) {
-        if (tid < n) {
-            const Cand c = l.a[tid];
+    if (found <= MAX_SEGS && n <= FEW) {
+        // a warp a candidate: how many are before it
+        for (int i = warp; i < n; i += SW) {
+            const Cand c = few[i];
             int rank = 0;
-            for (int j = 0; j < n; ++j)
-                rank += l.a[j].before(c.key, c.idx);
-            if (rank < p.K)
+            for (int j = lane; j < n; j += 32)
+                rank += few[j].before(c.key, c.idx);
+            rank = __reduce_add_sync(FULL_MASK, rank);
+            if (lane == 0 && rank < p.K)
                 emit(p, rank, true, c, ended);
-        } else if (tid < p.K) {
-            emit(p, tid, false, Cand{0, 0}, ended);
         }
+        if (tid >= n && tid < p.K)
+            emit(p, tid, false, Cand{0, 0}, ended);
         return;
-    } else {
-        prune(l, p.K);
     }
+    top_of_many<T>(p, l, base, seg);
+    if (warp == 0)   // the finished beams, behind the others
+        offer(l, ends ? key_of(score, 0.f) : 0, lane * p.V + p.eos, Cand{0, INT_MAX});
+    prune(l, p.K);
     if (tid < p.K)
         emit(p, tid, tid < l.n, l.a[tid], ended);
 }
