@@ -45,12 +45,16 @@ inline int select_segs(int V, int elem)
 
 cudaError_t launch_select(const SelectParams &p, cudaStream_t s);
 
-// A request's tables are taken in tiles of this many pages.
+// A request's tables are taken in tiles of this many places.
 constexpr int REORDER_TILE = 256;
+// Up to this many tiles (and requests) every CTA adds up what lies before it
+// by itself; a kernel of its own does for more.
+constexpr int REORDER_SCAN = 1024;
 
 struct ReorderHeader {
-    long long raised;    // the stack's height with all that came back
-    int top, taken;      // its height as far as it is kept, and pages taken from there
+    int count;           // the stack's height before the call
+    int top, taken;      // its height with what came back, as far as that is kept, and pages taken from there
+    long long back;      // pages that came back
 };
 
 struct ReorderParams {
@@ -68,9 +72,12 @@ struct ReorderParams {
     // workspace
     int tiles;                   // of a request
     ReorderHeader *header;
-    int32_t *freed;              // [R, tiles] pages that come back
-    long long *freed_before;     // [R, tiles] of granted requests before it
-    int32_t *needed;             // [R] copies
+    int32_t *lens;               // [R, W] lengths before the call
+    unsigned *copied;            // [R] new beams that need a copy
+    int32_t *freed;              // [R, tiles] pages that come back ...
+    int32_t *pages;              // [R, tiles, W * REORDER_TILE] ... and which
+    unsigned *moved;             // [R, tiles, REORDER_TILE / 32] places whose entries change hands
+    long long *freed_before;     // [R, tiles] of granted requests before it (more than REORDER_SCAN)
     int32_t *needed_before;      // [R] of granted requests before it, -1 if it is refused
 };
 

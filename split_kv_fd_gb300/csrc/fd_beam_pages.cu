@@ -15,335 +15,449 @@
 // request's first step come back in the order that undoes it; it follows from
 // sums over requests and tiles, not from the order of threads.
 //
-// Four phases: what comes back and what is needed, a CTA a tile of a request's
-// tables; the sums and who is granted, one CTA; the stack and the tables; the
-// pages for copies and the lengths, a warp a request.
+// Two kernels, a CTA a tile of a request's tables in each: what comes back, what
+// is needed and which places change; then, with the sums of these, the stack,
+// the tables and the lengths.  The data is small, and what takes the time is the
+// chain of dependent loads.
 #include "fd_beam.h"
 #include "fd_device.cuh"
 #include "fd_pages.h"
-
-#include <limits.h>
 
 namespace fd {
 namespace {
 
 constexpr int RT = REORDER_TILE;   // threads of a CTA, one a place
 constexpr int RW = RT / 32;
-constexpr int ST = 1024;           // threads of the sums
+constexpr int ST = 1024;           // threads of the sums' own kernel
+static_assert(REORDER_SCAN == 4 * RT, "four numbers a thread");
 
 __device__ __forceinline__ bool is_page(const ReorderParams &p, int page) { return page >= 0 && page < p.num_pages; }
 
-// A request's beams: lengths, pages, parents (-1: none).
+__device__ __forceinline__ int pages_of(const ReorderParams &p, int len)
+{
+    return (int)(((long long)len + p.page_size - 1) / p.page_size);
+}
+
+// What comes back of a place: bit w where beam w is the first to name a page
+// that no parent's table has there.
 struct Beams {
-    int len[BEAM_MAX_W], pages[BEAM_MAX_W], parent[BEAM_MAX_W];
+    int len[BEAM_MAX_W], pages[BEAM_MAX_W], parent[BEAM_MAX_W];   // parent: -1 for none
     unsigned parents;   // those that are a parent
 };
 
-// (The block's first warp loads; all threads call.)
-__device__ __forceinline__ void load_beams(const ReorderParams &p, int r, Beams &b, bool report)
-{
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        const int w = threadIdx.x;
-        int parent = -1;
-        if (w < p.W) {
-            const long long cap = (long long)p.max_pages * p.page_size;
-            const int len = (int)min(max((long long)p.seqlens[r * p.W + w], 0LL), cap);
-            b.len[w] = len;
-            b.pages[w] = (int)(((long long)len + p.page_size - 1) / p.page_size);
-            parent = p.parents[r * p.W + w];
-            if (parent >= p.W) {
-                parent = -1;
-                if (report)
-                    atomicOr(p.status, STATUS_BAD_INDEX);
-            }
-            b.parent[w] = max(parent, -1);
-        }
-        const unsigned mine = parent >= 0 ? 1u << parent : 0u;
-        const unsigned all = __reduce_or_sync(FULL_MASK, mine);
-        if (w == 0)
-            b.parents = all;
-    }
-    __syncthreads();
-}
-
-// The entries of a tile: place j0 + thread of every beam that has it.
-struct Tile {
-    int e[BEAM_MAX_W][RT];
-};
-
-__device__ __forceinline__ void load_tile(const ReorderParams &p, int r, int j, const Beams &b, Tile &t)
-{
-#pragma unroll 8
-    for (int w = 0; w < p.W; ++w)
-        if (j < b.pages[w])
-            t.e[w][threadIdx.x] = p.table[(long long)(r * p.W + w) * p.max_pages + j];
-}
-
-// The beams whose page at place j comes back, the first to name each.
-__device__ __forceinline__ unsigned released(const ReorderParams &p, int j, const Beams &b, const Tile &t, bool &bad)
-{
-    const int tid = threadIdx.x;
-    unsigned gone = 0;
-    for (int w = 0; w < p.W; ++w) {
-        if ((b.parents >> w & 1) || j >= b.pages[w])
-            continue;   // a parent's pages stay
-        const int page = t.e[w][tid];
-        bool stays = !is_page(p, page);
-        bad |= stays;
-        for (int v = 0; v < p.W && !stays; ++v)
-            if (j < b.pages[v] && ((b.parents >> v & 1) || (gone >> v & 1)))
-                stays = t.e[v][tid] == page;
-        if (!stays)
-            gone |= 1u << w;
-    }
-    return gone;
-}
-
-__device__ __forceinline__ int block_sum(int x, int *warps)
-{
-    x = __reduce_add_sync(FULL_MASK, x);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0)
-        warps[threadIdx.x >> 5] = x;
-    __syncthreads();
-    int all = 0;
-    for (int i = 0; i < RW; ++i)
-        all += warps[i];
-    return all;
-}
-
-// Phase 1: pages that come back of each tile; the copies a request needs.
-__global__ void __launch_bounds__(RT) count_kernel(const ReorderParams p)
+__global__ void __launch_bounds__(RT) look_kernel(const ReorderParams p)
 {
     __shared__ Beams b;
-    __shared__ Tile t;
+    __shared__ int e[BEAM_MAX_W][RT + 1];
     __shared__ int warps[RW];
-    const int r = blockIdx.x / p.tiles, tile = blockIdx.x % p.tiles;
-    load_beams(p, r, b, tile == 0);
-    const int j = tile * RT + threadIdx.x;
-    load_tile(p, r, j, b, t);
-    bool bad = false;
-    const unsigned gone = released(p, j, b, t, bad);
-    if (bad)
-        atomicOr(p.status, STATUS_BAD_PAGE);
-    const int n = block_sum(__popc(gone), warps);
-    if (threadIdx.x == 0)
-        p.freed[blockIdx.x] = n;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int r = blockIdx.x / p.tiles, tile = blockIdx.x - r * p.tiles;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, W = p.W;
+    const int row0 = r * W, j = tile * RT + tid;
 
-    if (tile == 0 && threadIdx.x < 32) {
-        // new beam w: its parent's last page, if that is partly filled
-        const int w = threadIdx.x;
-        const int parent = w < p.W ? b.parent[w] : -1;
-        const int rows = parent >= 0 ? b.len[parent] % p.page_size : 0;
-        bool copy = false;
-        int page = -1;
-        if (rows) {
-            const int at = b.len[parent] / p.page_size;
-            page = p.table[(long long)(r * p.W + parent) * p.max_pages + at];
-            for (int v = 0; v < p.W && !copy; ++v) {
-                const int q = b.parent[v];
-                if (v == w || q < 0 || at >= b.pages[q])
-                    continue;
-                // named by a beam before it, or as a full page by any
-                if (v < w || b.len[q] / p.page_size > at)
-                    copy = p.table[(long long)(r * p.W + q) * p.max_pages + at] == page;
+    // Lengths and parents, while the entries of the place are on their way
+    // (those behind a length are read and not looked at).
+    int mine[8];
+    auto fetch = [&](int w0) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            mine[k] = w0 + k < W && j < p.max_pages ? p.table[(long long)(row0 + w0 + k) * p.max_pages + j] : 0;
+    };
+    fetch(0);
+    if (warp == 0) {
+        int parent = -1;
+        if (lane < W) {
+            const long long cap = (long long)p.max_pages * p.page_size;
+            const int len = (int)min(max((long long)p.seqlens[row0 + lane], 0LL), cap);
+            parent = max(p.parents[row0 + lane], -1);
+            if (parent >= W) {
+                parent = -1;
+                if (tile == 0)
+                    atomicOr(p.status, STATUS_BAD_INDEX);
             }
-            if (!is_page(p, page)) {
-                copy = false;
-                atomicOr(p.status, STATUS_BAD_PAGE);
+            b.len[lane] = len;
+            b.pages[lane] = pages_of(p, len);
+            b.parent[lane] = parent;
+            if (tile == 0)
+                p.lens[row0 + lane] = len;
+        }
+        const unsigned all = __reduce_or_sync(FULL_MASK, parent >= 0 ? 1u << parent : 0u);
+        if (lane == 0)
+            b.parents = all;
+        if (blockIdx.x == 0 && lane == 0)
+            p.header->count = min(max(*p.free_count, 0), p.num_pages);
+    }
+    for (int w0 = 0; w0 < W; w0 += 8) {
+        if (w0)
+            fetch(w0);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (w0 + k < W)
+                e[w0 + k][tid] = mine[k];
+    }
+    __syncthreads();
+
+    // Most places are of a part that all beams share: one page, named by all.
+    unsigned have = 0;
+    int first = 0;
+    bool same = true, shorter = false;
+    for (int w = 0; w < W; ++w) {
+        if (j < b.pages[w]) {
+            first = have ? first : e[w][tid];
+            same &= e[w][tid] == first;
+            have |= 1u << w;
+        } else if (b.parent[w] >= 0) {
+            shorter |= j < b.pages[b.parent[w]];
+        }
+    }
+    bool bad = false;
+    unsigned gone = 0;
+    if (same && have && !(have & b.parents)) {
+        bad = !is_page(p, first);
+        gone = bad ? 0 : have & (0u - have);
+    }
+    // The others a warp at a time, a beam a lane.
+    for (unsigned left = __ballot_sync(FULL_MASK, !same); left; left &= left - 1) {
+        const int c = __ffs(left) - 1, jc = tile * RT + warp * 32 + c;
+        const bool in = lane < W && jc < b.pages[lane];
+        const int page = lane < W ? e[lane][warp * 32 + c] : 0;
+        const unsigned who = __ballot_sync(FULL_MASK, in);
+        bool mine = false;
+        if (in) {
+            const unsigned peers = __match_any_sync(who, page);
+            mine = !(peers & b.parents) && lane == __ffs(peers) - 1;
+            if (mine && !is_page(p, page)) {
+                mine = false;
+                bad = true;
             }
         }
-        if (w < p.W) {
-            int32_t *c = p.copies + (long long)(r * p.W + w) * 3;
+        const unsigned g = __ballot_sync(FULL_MASK, mine);
+        if (lane == c)
+            gone = g;
+    }
+    if (bad)
+        atomicOr(p.status, STATUS_BAD_PAGE);
+    const unsigned changes = __ballot_sync(FULL_MASK, have && (!same || shorter));
+    if (lane == 0)
+        p.moved[(long long)blockIdx.x * RW + warp] = changes;
+
+    // what comes back, in order of place and beam
+    const int own = __popc(gone);
+    int sum = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(FULL_MASK, sum, o);
+        if (lane >= o)
+            sum += y;
+    }
+    if (lane == 31)
+        warps[warp] = sum;
+    __syncthreads();
+    int before = sum - own, all = 0;
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+        before += i < warp ? warps[i] : 0;
+        all += warps[i];
+    }
+    if (tid == 0)
+        p.freed[blockIdx.x] = all;
+    int32_t *to = p.pages + (long long)blockIdx.x * W * RT + before;
+    for (; gone; gone &= gone - 1)
+        *to++ = e[__ffs(gone) - 1][tid];
+
+    // The copies, by the last warp (whose places are the rarest to be used).
+    // New beam w: its parent's last page, if that is partly filled.
+    if (tile == 0 && warp == RW - 1) {
+        const int w = lane;
+        const int parent = w < W ? b.parent[w] : -1;
+        const int rows = parent >= 0 ? b.len[parent] % p.page_size : 0;
+        const int at = rows ? b.len[parent] / p.page_size : 0;
+        const int page = rows ? p.table[(long long)(row0 + parent) * p.max_pages + at] : -1;
+        bool copy = false;
+#pragma unroll 8
+        for (int v = 0; v < W; ++v) {
+            const int q = b.parent[v];
+            // named by a beam before it, or as a full page by any
+            if (rows && v != w && q >= 0 && at < b.pages[q] && (v < w || b.len[q] / p.page_size > at))
+                copy |= p.table[(long long)(row0 + q) * p.max_pages + at] == page;
+        }
+        if (rows && !is_page(p, page)) {
+            copy = false;
+            atomicOr(p.status, STATUS_BAD_PAGE);
+        }
+        if (w < W) {
+            int32_t *c = p.copies + (long long)(row0 + w) * 3;
             c[0] = copy ? page : -1;
             c[1] = -1;
             c[2] = copy ? rows : 0;
         }
         const unsigned who = __ballot_sync(FULL_MASK, copy);
-        if (w == 0)
-            p.needed[r] = __popc(who);
+        if (lane == 0)
+            p.copied[r] = who;
     }
 }
 
-// Inclusive sums of N values over the block of ST threads, and their totals.
-template <int N> struct Scan {
-    long long warp[N][ST / 32];
-    __device__ __forceinline__ void run(long long (&x)[N], long long (&total)[N])
+// Inclusive sums over the block of NT threads, and their total.
+template <int NT> struct Scan {
+    long long warp[NT / 32];
+    __device__ __forceinline__ long long run(long long x, long long &total)
     {
         const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const long long y = __shfl_up_sync(FULL_MASK, x[i], o);
-                if (lane >= o)
-                    x[i] += y;
-            }
+            const long long y = __shfl_up_sync(FULL_MASK, x, o);
+            if (lane >= o)
+                x += y;
         }
         __syncthreads();   // the sums of the previous call have been read
-        if (lane == 31) {
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                warp[i][w] = x[i];
-        }
+        if (lane == 31)
+            warp[w] = x;
         __syncthreads();
+        long long all = 0;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const long long s = warp[i][lane];
-            long long before = lane < w ? s : 0, all = s;
-#pragma unroll
-            for (int o = 16; o; o >>= 1) {
-                before += __shfl_xor_sync(FULL_MASK, before, o);
-                all += __shfl_xor_sync(FULL_MASK, all, o);
-            }
-            x[i] += before;
-            total[i] = all;
+        for (int i = 0; i < NT / 32; ++i) {
+            x += i < w ? warp[i] : 0;
+            all += warp[i];
         }
+        total = all;
+        return x;
     }
 };
 
-// Phase 2: who is granted, and what lies before each.  A request that gives
-// back as many pages as it needs is; of the others, in order, those up to
-// which the needs (less what they give back) do not pass what is free and
+// The stack's header from the totals.
+__device__ __forceinline__ ReorderHeader heights(const ReorderParams &p, int count, long long back, long long taken)
+{
+    ReorderHeader h;
+    // (pages given back twice could pass the stack's end)
+    const long long raised = count + back, top = min(raised, (long long)p.num_pages);
+    h.count = count;
+    h.top = (int)top;
+    h.taken = (int)min(taken, top);
+    h.back = back;
+    return h;
+}
+
+// Who is granted, and what lies before each, for many tiles.  A request that
+// gives back as many pages as it needs is; of the others, in order, those up
+// to which the needs (less what they give back) do not pass what is free and
 // what the former leave over.
 __global__ void __launch_bounds__(ST) settle_kernel(const ReorderParams p)
 {
-    __shared__ Scan<2> scan2;
-    __shared__ Scan<1> scan1;
-    const long long count0 = min(max(*p.free_count, 0), p.num_pages);
-    long long left = count0;   // free, with what requests leave over
+    __shared__ Scan<ST> scan;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int count = p.header->count;
     auto freed_of = [&](int r) {
         long long n = 0;
         for (int i = 0; i < p.tiles; ++i)
             n += p.freed[(long long)r * p.tiles + i];
         return n;
     };
+    long long left = count, all;   // free, with what requests leave over
     for (int r0 = 0; r0 < p.R; r0 += ST) {
         const int r = r0 + (int)threadIdx.x;
-        long long x[1] = {r < p.R ? max(0LL, freed_of(r) - p.needed[r]) : 0}, all[1];
-        scan1.run(x, all);
-        left += all[0];
+        scan.run(r < p.R ? max(0LL, freed_of(r) - __popc(p.copied[r])) : 0, all);
+        left += all;
     }
     long long wanted = 0, back = 0, taken = 0;
     for (int r0 = 0; r0 < p.R; r0 += ST) {
         const int r = r0 + (int)threadIdx.x;
-        const long long f = r < p.R ? freed_of(r) : 0, c = r < p.R ? p.needed[r] : 0;
-        long long x[1] = {max(0LL, c - f)}, all[1];
-        scan1.run(x, all);
-        const bool given = r < p.R && (c <= f || wanted + x[0] <= left);
-        wanted += all[0];
-        long long y[2] = {given ? f : 0, given ? c : 0}, sums[2];
-        scan2.run(y, sums);
+        const long long f = r < p.R ? freed_of(r) : 0, c = r < p.R ? __popc(p.copied[r]) : 0;
+        const long long x = scan.run(max(0LL, c - f), all);
+        const bool given = r < p.R && (c <= f || wanted + x <= left);
+        wanted += all;
+        long long allf, allc;
+        const long long sf = scan.run(given ? f : 0, allf), sc = scan.run(given ? c : 0, allc);
         if (r < p.R) {
-            p.needed_before[r] = given ? (int)(taken + y[1] - c) : -1;
-            if (p.granted)
-                p.granted[r] = given;
-            long long before = back + y[0] - f;
-            for (int i = 0; i < p.tiles && given; ++i) {
+            p.needed_before[r] = given ? (int)(taken + sc - c) : -1;
+            long long before = back + sf - f;
+            for (int i = 0; i < p.tiles; ++i) {
                 p.freed_before[(long long)r * p.tiles + i] = before;
-                before += p.freed[(long long)r * p.tiles + i];
+                before += given ? p.freed[(long long)r * p.tiles + i] : 0;
             }
         }
-        back += sums[0];
-        taken += sums[1];
+        back += allf;
+        taken += allc;
     }
-    if (threadIdx.x == 0) {
-        // (pages given back twice could pass the stack's end)
-        const long long raised = count0 + back, top = min(raised, (long long)p.num_pages);
-        p.header->raised = raised;
-        p.header->top = (int)top;
-        p.header->taken = (int)min(taken, top);
-        if (raised > top)
+    if (threadIdx.x == 0)
+        *p.header = heights(p, count, back, taken);
+}
+
+// The stack, the tables and the lengths.
+template <bool SETTLED> __global__ void __launch_bounds__(RT) move_kernel(const ReorderParams p)
+{
+    __shared__ int e[BEAM_MAX_W][RT + 1];
+    __shared__ int pages[BEAM_MAX_W], parent[BEAM_MAX_W], place[BEAM_MAX_W], taken_page[BEAM_MAX_W];
+    __shared__ int freed_before[SETTLED ? 1 : REORDER_SCAN], needed_before[SETTLED ? 1 : REORDER_SCAN];
+    __shared__ Scan<RT> scan;
+    const int r = blockIdx.x / p.tiles, tile = blockIdx.x - r * p.tiles;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, W = p.W;
+    const int row0 = r * W, j = tile * RT + tid, items = p.R * p.tiles;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    const int nfreed = p.freed[blockIdx.x];
+    const bool moves = p.moved[(long long)blockIdx.x * RW + warp] >> lane & 1;
+    ReorderHeader h;
+    int need0;          // copies of granted requests before this one, -1 if it is refused
+    long long free0;    // pages that come back before this tile's
+    if (SETTLED) {
+        h = *p.header;
+        need0 = p.needed_before[r];
+        free0 = p.freed_before[blockIdx.x];
+    } else {
+        // the sums over all tiles and requests, four a thread
+        h.count = p.header->count;
+        int f[4], c[4];
+        long long total, sum = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            f[k] = tid * 4 + k < items ? p.freed[tid * 4 + k] : 0;
+            c[k] = tid * 4 + k < p.R ? __popc(p.copied[tid * 4 + k]) : 0;
+        }
+        auto before = [&](const int (&x)[4], int *to) {   // exclusive sums of x, and all of it
+            const int s = x[0] + x[1] + x[2] + x[3];
+            long long all;
+            int at = (int)scan.run(s, all) - s;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                to[tid * 4 + k] = at;
+                at += x[k];
+            }
+            return all;
+        };
+        const long long back0 = before(f, freed_before);
+        __syncthreads();
+        // what a request needs beyond what it gives back, and what it leaves
+        long long lacks[4], leaves = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int q = tid * 4 + k;
+            const int end = (q + 1) * p.tiles;
+            const int own = q < p.R ? (end < items ? freed_before[end] : (int)back0) - freed_before[q * p.tiles] : 0;
+            lacks[k] = max(0, c[k] - own);
+            leaves += max(0, own - c[k]);
+            sum += lacks[k];
+        }
+        long long left, lack;
+        scan.run(leaves, left);
+        left += h.count;
+        long long at = scan.run(sum, lack) - sum;
+        if (lack <= left) {   // all are granted
+            need0 = 0;
+            total = back0;
+        } else {
+            unsigned given = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                at += lacks[k];
+                given |= (lacks[k] == 0 || at <= left) << k;
+                c[k] = given >> k & 1 ? c[k] : 0;
+            }
+            __shared__ bool refused[REORDER_SCAN];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                refused[tid * 4 + k] = !(given >> k & 1);
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                f[k] = tid * 4 + k < items && refused[(tid * 4 + k) / p.tiles] ? 0 : f[k];
+            total = before(f, freed_before);
+            need0 = refused[r] ? -1 : 0;
+        }
+        const long long taken = before(c, needed_before);
+        __syncthreads();
+        h = heights(p, h.count, total, taken);
+        need0 = need0 < 0 ? -1 : needed_before[r];
+        free0 = freed_before[blockIdx.x];
+    }
+    if (blockIdx.x == 0 && tid == 0) {
+        *p.free_count = h.top - h.taken;
+        if (h.count + h.back > h.top)
             atomicOr(p.status, STATUS_BAD_PAGE);
     }
-}
-
-// Phase 3: what comes back onto the stack; the tables' entries to their
-// beams' children.
-__global__ void __launch_bounds__(RT) apply_kernel(const ReorderParams p)
-{
-    __shared__ Beams b;
-    __shared__ Tile t;
-    __shared__ int warps[RW];
-    const int r = blockIdx.x / p.tiles, tile = blockIdx.x % p.tiles, tid = threadIdx.x;
-    if (p.needed_before[r] < 0)
+    if (tile == 0 && tid == 0 && p.granted)
+        p.granted[r] = need0 >= 0;
+    if (need0 < 0) {
+        if (tile == 0 && tid < W) {
+            int32_t *c = p.copies + (long long)(row0 + tid) * 3;
+            c[0] = -1;
+            c[2] = 0;
+        }
         return;
-    load_beams(p, r, b, false);
-    const int j = tile * RT + tid;
-    load_tile(p, r, j, b, t);
-    bool bad = false;
-    unsigned gone = released(p, j, b, t, bad);
-    if (p.freed[blockIdx.x] > 0) {
-        int before = __popc(gone);
-        const int lane = tid & 31, warp = tid >> 5;
-        const int own = before;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(FULL_MASK, before, o);
-            if (lane >= o)
-                before += y;
-        }
-        if (lane == 31)
-            warps[warp] = before;
-        __syncthreads();
-        for (int i = 0; i < warp; ++i)
-            before += warps[i];
-        long long at = p.header->raised - 1 - (p.freed_before[blockIdx.x] + before - own);
-        for (; gone; gone &= gone - 1, --at)
-            if (at >= 0 && at < p.num_pages)
-                p.free_pages[at] = t.e[__ffs(gone) - 1][tid];
     }
-    for (int w = 0; w < p.W; ++w) {
-        const int q = b.parent[w];
-        if (q < 0 || q == w || j >= b.pages[q])
-            continue;
-        if (j >= b.pages[w] || t.e[w][tid] != t.e[q][tid])
-            p.table[(long long)(r * p.W + w) * p.max_pages + j] = t.e[q][tid];
-    }
-}
 
-// Phase 4: pages for the copies, and the lengths.
-__global__ void __launch_bounds__(RT) take_kernel(const ReorderParams p)
-{
-    const int lane = threadIdx.x & 31;
-    const int top = p.header->top;
-    for (long long r = blockIdx.x * RW + (threadIdx.x >> 5); r < p.R; r += (long long)gridDim.x * RW) {
-        const long long row = r * p.W + lane;
-        const bool in = lane < p.W;
-        const int before = p.needed_before[r];
-        int32_t *c = p.copies + row * 3;
-        if (before < 0) {
-            if (in) {
-                c[0] = c[1] = -1;
-                c[2] = 0;
+    // what comes back onto the stack, the first on top
+    const int32_t *list = p.pages + (long long)blockIdx.x * W * RT;
+    const long long raised = h.count + h.back;
+    for (int i = tid; i < nfreed; i += RT) {
+        const long long at = raised - 1 - (free0 + i);
+        if (at >= 0 && at < p.num_pages)
+            p.free_pages[at] = list[i];
+    }
+
+    // Lengths, and the pages for this request's copies: of those that came
+    // back the t-th, or one that was free before.
+    if (warp == 0) {
+        const int q = lane < W ? p.parents[row0 + lane] : -1;
+        const bool some = q >= 0 && q < W;
+        const int old = lane < W ? p.lens[row0 + lane] : 0;
+        const int len = __shfl_sync(FULL_MASK, old, some ? q : 0);
+        const unsigned who = p.copied[r];
+        const bool copy = who >> lane & 1;
+        int page = -1;
+        const int last = copy ? len / p.page_size : -1;
+        if (copy && last / RT == tile) {
+            const int t = need0 + __popc(who & ((1u << lane) - 1));
+            const int at = h.top - 1 - t;
+            if (at >= h.count) {
+                const long long x = raised - 1 - at;   // the x-th that came back: of the last tile with no more before it
+                int lo = 0, hi = items - 1;
+                while (lo < hi) {
+                    const int mid = (int)(((long long)lo + hi + 1) >> 1);
+                    if ((SETTLED ? p.freed_before[mid] : (long long)freed_before[SETTLED ? 0 : mid]) <= x)
+                        lo = mid;
+                    else
+                        hi = mid - 1;
+                }
+                page = p.pages[(long long)lo * W * RT + (x - (SETTLED ? p.freed_before[lo] : (long long)freed_before[SETTLED ? 0 : lo]))];
+            } else if (at >= 0) {
+                page = p.free_pages[at];
             }
-            continue;
-        }
-        const long long cap = (long long)p.max_pages * p.page_size;
-        const int old = in ? (int)min(max((long long)p.seqlens[row], 0LL), cap) : 0;
-        const int parent = in ? p.parents[row] : -1;
-        const bool some = parent >= 0 && parent < p.W;
-        const int len = __shfl_sync(FULL_MASK, old, some ? parent : 0);
-        const bool copy = in && c[0] >= 0;
-        const unsigned who = __ballot_sync(FULL_MASK, copy);
-        if (copy) {
-            const int at = top - 1 - (before + __popc(who & ((1u << lane) - 1)));
-            const int page = at >= 0 ? p.free_pages[at] : -1;
-            const bool ok = is_page(p, page);
-            if (!ok) {
+            int32_t *c = p.copies + (long long)(row0 + lane) * 3;
+            if (!is_page(p, page)) {
+                page = -1;
                 atomicOr(p.status, STATUS_BAD_PAGE);
                 c[0] = -1;
                 c[2] = 0;
             }
-            c[1] = ok ? page : -1;
-            p.table[row * p.max_pages + len / p.page_size] = ok ? page : -1;
+            c[1] = page;
         }
-        if (in)
-            p.seqlens[row] = some ? len : 0;
+        if (lane < W) {
+            pages[lane] = pages_of(p, old);
+            parent[lane] = some ? q : -1;
+            place[lane] = last;
+            taken_page[lane] = page;
+            if (tile == 0)
+                p.seqlens[row0 + lane] = some ? len : 0;
+        }
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0)
-        *p.free_count = top - p.header->taken;
+    __syncthreads();
+    if (moves) {
+#pragma unroll 8
+        for (int w = 0; w < W; ++w)
+            if (j < pages[w])
+                e[w][tid] = p.table[(long long)(row0 + w) * p.max_pages + j];
+        for (int w = 0; w < W; ++w) {
+            const int q = parent[w];
+            if (q >= 0 && q != w && j < pages[q] && j != place[w] && !(j < pages[w] && e[w][tid] == e[q][tid]))
+                p.table[(long long)(row0 + w) * p.max_pages + j] = e[q][tid];
+        }
+    }
+    // (a beam may keep its parent's table, itself, and still need a copy: no other thread writes there)
+    __syncthreads();
+    if (tid < W && place[tid] >= 0 && place[tid] / RT == tile)
+        p.table[(long long)(row0 + tid) * p.max_pages + place[tid]] = taken_page[tid];
 }
 
 // Rows of a page to another one's, of every head: a CTA a copy and head of K
@@ -374,14 +488,36 @@ __global__ void __launch_bounds__(256) copy_kernel(const CopyParams p)
 
 }  // namespace
 
+namespace {
+
+// A launch whose CTAs may start while the kernel before it ends.
+template <typename P> cudaError_t launch_behind(void (*kernel)(P), dim3 grid, int threads, cudaStream_t s, const P &p)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+}  // namespace
+
 cudaError_t launch_reorder(const ReorderParams &p, cudaStream_t s)
 {
-    const unsigned tiles = (unsigned)p.R * p.tiles;
-    count_kernel<<<tiles, RT, 0, s>>>(p);
-    settle_kernel<<<1, ST, 0, s>>>(p);
-    apply_kernel<<<tiles, RT, 0, s>>>(p);
-    take_kernel<<<(unsigned)min((p.R + RW - 1) / RW, 1024), RT, 0, s>>>(p);
-    return cudaGetLastError();
+    const unsigned items = (unsigned)p.R * p.tiles;
+    look_kernel<<<items, RT, 0, s>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess)
+        return e;
+    if (items <= REORDER_SCAN)
+        return launch_behind(move_kernel<false>, items, RT, s, p);
+    e = launch_behind(settle_kernel, 1, ST, s, p);
+    return e == cudaSuccess ? launch_behind(move_kernel<true>, items, RT, s, p) : e;
 }
 
 cudaError_t launch_copy_pages(const CopyParams &p, cudaStream_t s)

@@ -642,7 +642,7 @@ namespace {
 
 struct ReorderLayout {
     int tiles;
-    size_t freed, freed_before, needed, needed_before, total;
+    size_t lens, copied, freed, pages, moved, freed_before, needed_before, total;
 };
 
 bool reorder_layout(int R, int W, int max_pages, ReorderLayout &l)
@@ -657,9 +657,12 @@ bool reorder_layout(int R, int W, int max_pages, ReorderLayout &l)
         at += round_up(bytes, 256);
         return was;
     };
+    l.lens = take((size_t)R * W * sizeof(int32_t));
+    l.copied = take((size_t)R * sizeof(unsigned));
     l.freed = take(all * sizeof(int32_t));
+    l.pages = take(all * W * REORDER_TILE * sizeof(int32_t));
+    l.moved = take(all * (REORDER_TILE / 8));
     l.freed_before = take(all * sizeof(long long));
-    l.needed = take((size_t)R * sizeof(int32_t));
     l.needed_before = take((size_t)R * sizeof(int32_t));
     l.total = at;
     return (long long)R * l.tiles <= INT_MAX;
@@ -710,9 +713,12 @@ fd_status fd_reorder_pages(const int32_t *parents, int R, int W, int32_t *seqlen
     char *ws = static_cast<char *>(workspace);
     p.tiles = l.tiles;
     p.header = reinterpret_cast<ReorderHeader *>(ws);
+    p.lens = reinterpret_cast<int32_t *>(ws + l.lens);
+    p.copied = reinterpret_cast<unsigned *>(ws + l.copied);
     p.freed = reinterpret_cast<int32_t *>(ws + l.freed);
+    p.pages = reinterpret_cast<int32_t *>(ws + l.pages);
+    p.moved = reinterpret_cast<unsigned *>(ws + l.moved);
     p.freed_before = reinterpret_cast<long long *>(ws + l.freed_before);
-    p.needed = reinterpret_cast<int32_t *>(ws + l.needed);
     p.needed_before = reinterpret_cast<int32_t *>(ws + l.needed_before);
     return launch_reorder(p, stream_of(stream)) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
 }
