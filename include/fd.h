@@ -739,7 +739,7 @@ fd_status fd_reorder_pages(const int32_t *parents, int R, int W, int32_t *seqlen
  *   copies            [n, 3] int32, device (fd_reorder_pages writes them)
  *   k_pages, v_pages  [num_pages, Hkv, page_size, d] in dtype (f32, f16, bf16
  *                     or E4M3)
- * d must be 64, 128 or 256.
+ * d must be 64, 128 or 256; a page of K is below 16 GB.
  */
 fd_status fd_copy_pages(const int32_t *copies, int n, int Hkv, int d, fd_dtype dtype, void *k_pages, void *v_pages,
                         int page_size, long long num_pages, void *stream);

@@ -42,14 +42,20 @@ __device__ __forceinline__ int pages_of(const ReorderParams &p, int len)
 // that no parent's table has there.
 struct Beams {
     int len[BEAM_MAX_W], pages[BEAM_MAX_W], parent[BEAM_MAX_W];   // parent: -1 for none
-    unsigned parents;   // those that are a parent
+    int wants[BEAM_MAX_W];   // pages of the parent's
+    unsigned parents;        // those that are a parent
 };
+
+// (Loops over beams go in steps of BATCH with nothing to wait for within a
+// step: rolled ones cost a latency a beam.)
+constexpr int BATCH = 8;
 
 __global__ void __launch_bounds__(RT) look_kernel(const ReorderParams p)
 {
     __shared__ Beams b;
     __shared__ int e[BEAM_MAX_W][RT + 1];
-    __shared__ int warps[RW];
+    __shared__ int warps[RW], list[RT];
+    __shared__ unsigned back[RT];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int r = blockIdx.x / p.tiles, tile = blockIdx.x - r * p.tiles;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, W = p.W;
@@ -57,58 +63,65 @@ __global__ void __launch_bounds__(RT) look_kernel(const ReorderParams p)
 
     // Lengths and parents, while the entries of the place are on their way
     // (those behind a length are read and not looked at).
-    int mine[8];
+    int mine[2 * BATCH];
     auto fetch = [&](int w0) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 0; k < 2 * BATCH; ++k)
             mine[k] = w0 + k < W && j < p.max_pages ? p.table[(long long)(row0 + w0 + k) * p.max_pages + j] : 0;
     };
     fetch(0);
     if (warp == 0) {
-        int parent = -1;
+        int parent = -1, len = 0;
         if (lane < W) {
             const long long cap = (long long)p.max_pages * p.page_size;
-            const int len = (int)min(max((long long)p.seqlens[row0 + lane], 0LL), cap);
+            len = (int)min(max((long long)p.seqlens[row0 + lane], 0LL), cap);
             parent = max(p.parents[row0 + lane], -1);
             if (parent >= W) {
                 parent = -1;
                 if (tile == 0)
                     atomicOr(p.status, STATUS_BAD_INDEX);
             }
-            b.len[lane] = len;
-            b.pages[lane] = pages_of(p, len);
-            b.parent[lane] = parent;
             if (tile == 0)
                 p.lens[row0 + lane] = len;
         }
+        const int pages = pages_of(p, len), theirs = __shfl_sync(FULL_MASK, pages, max(parent, 0));
+        b.len[lane] = len;
+        b.pages[lane] = pages;
+        b.parent[lane] = parent;
+        b.wants[lane] = parent >= 0 ? theirs : 0;
         const unsigned all = __reduce_or_sync(FULL_MASK, parent >= 0 ? 1u << parent : 0u);
         if (lane == 0)
             b.parents = all;
         if (blockIdx.x == 0 && lane == 0)
             p.header->count = min(max(*p.free_count, 0), p.num_pages);
     }
-    for (int w0 = 0; w0 < W; w0 += 8) {
+    for (int w0 = 0; w0 < W; w0 += 2 * BATCH) {
         if (w0)
             fetch(w0);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (w0 + k < W)
-                e[w0 + k][tid] = mine[k];
+        for (int k = 0; k < 2 * BATCH; ++k)
+            e[w0 + k][tid] = mine[k];
     }
     __syncthreads();
 
     // Most places are of a part that all beams share: one page, named by all.
-    unsigned have = 0;
+    unsigned have = 0, wants = 0;
     int first = 0;
-    bool same = true, shorter = false;
-    for (int w = 0; w < W; ++w) {
-        if (j < b.pages[w]) {
-            first = have ? first : e[w][tid];
-            same &= e[w][tid] == first;
-            have |= 1u << w;
-        } else if (b.parent[w] >= 0) {
-            shorter |= j < b.pages[b.parent[w]];
+    for (int w0 = 0; w0 < W; w0 += BATCH) {
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            const int w = w0 + k;
+            have |= (j < b.pages[w]) << w;
+            wants |= (j < b.wants[w]) << w;
         }
+    }
+    if (have)
+        first = e[__ffs(have) - 1][tid];
+    bool same = true;
+    for (int w0 = 0; w0 < W; w0 += BATCH) {
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k)
+            same &= !(have >> (w0 + k) & 1) || e[w0 + k][tid] == first;
     }
     bool bad = false;
     unsigned gone = 0;
@@ -116,28 +129,50 @@ __global__ void __launch_bounds__(RT) look_kernel(const ReorderParams p)
         bad = !is_page(p, first);
         gone = bad ? 0 : have & (0u - have);
     }
-    // The others a warp at a time, a beam a lane.
-    for (unsigned left = __ballot_sync(FULL_MASK, !same); left; left &= left - 1) {
-        const int c = __ffs(left) - 1, jc = tile * RT + warp * 32 + c;
-        const bool in = lane < W && jc < b.pages[lane];
-        const int page = lane < W ? e[lane][warp * 32 + c] : 0;
-        const unsigned who = __ballot_sync(FULL_MASK, in);
+    // The others by all warps alike, a beam a lane, as many places at a time as
+    // a warp has lanes for.
+    const unsigned odd = __ballot_sync(FULL_MASK, !same);
+    if (lane == 0)
+        warps[warp] = __popc(odd);
+    __syncthreads();
+    int at = 0, odds = 0;
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+        at += i < warp ? warps[i] : 0;
+        odds += warps[i];
+    }
+    if (!same)
+        list[at + __popc(odd & ((1u << lane) - 1))] = tid;
+    __syncthreads();
+    int width = 1;   // lanes of a place
+    while (width < W)
+        width *= 2;
+    const int group = lane / width, w = lane & (width - 1), each = 32 / width;
+    const unsigned in_group = width == 32 ? FULL_MASK : ((1u << width) - 1) << group * width;
+    for (int i = warp * each; i < odds; i += RW * each) {
+        const int c = i + group < odds ? list[i + group] : -1;
+        const bool in = c >= 0 && w < W && tile * RT + c < b.pages[w];
+        const int page = in ? e[w][c] : 0;
+        const unsigned who = __ballot_sync(FULL_MASK, in) & in_group;
         bool mine = false;
         if (in) {
             const unsigned peers = __match_any_sync(who, page);
-            mine = !(peers & b.parents) && lane == __ffs(peers) - 1;
+            mine = !(peers >> group * width & b.parents) && lane == __ffs(peers) - 1;
             if (mine && !is_page(p, page)) {
                 mine = false;
                 bad = true;
             }
         }
-        const unsigned g = __ballot_sync(FULL_MASK, mine);
-        if (lane == c)
-            gone = g;
+        const unsigned g = (__ballot_sync(FULL_MASK, mine) & in_group) >> group * width;
+        if (c >= 0 && w == 0)
+            back[c] = g;
     }
+    __syncthreads();
+    if (!same)
+        gone = back[tid];
     if (bad)
         atomicOr(p.status, STATUS_BAD_PAGE);
-    const unsigned changes = __ballot_sync(FULL_MASK, have && (!same || shorter));
+    const unsigned changes = __ballot_sync(FULL_MASK, have && (!same || (wants & ~have)));
     if (lane == 0)
         p.moved[(long long)blockIdx.x * RW + warp] = changes;
 
@@ -168,18 +203,22 @@ __global__ void __launch_bounds__(RT) look_kernel(const ReorderParams p)
     // The copies, by the last warp (whose places are the rarest to be used).
     // New beam w: its parent's last page, if that is partly filled.
     if (tile == 0 && warp == RW - 1) {
-        const int w = lane;
-        const int parent = w < W ? b.parent[w] : -1;
-        const int rows = parent >= 0 ? b.len[parent] % p.page_size : 0;
-        const int at = rows ? b.len[parent] / p.page_size : 0;
+        const int w = lane, parent = b.parent[w], len = parent >= 0 ? b.len[parent] : 0;
+        const int rows = len % p.page_size, at = len / p.page_size;
         const int page = rows ? p.table[(long long)(row0 + parent) * p.max_pages + at] : -1;
+        // named as its last page by a beam before it
+        const unsigned part = __ballot_sync(FULL_MASK, rows != 0);
         bool copy = false;
-#pragma unroll 8
-        for (int v = 0; v < W; ++v) {
-            const int q = b.parent[v];
-            // named by a beam before it, or as a full page by any
-            if (rows && v != w && q >= 0 && at < b.pages[q] && (v < w || b.len[q] / p.page_size > at))
-                copy |= p.table[(long long)(row0 + q) * p.max_pages + at] == page;
+        if (rows)
+            copy = __match_any_sync(part, (unsigned long long)(unsigned)at << 32 | (unsigned)page) & ((1u << w) - 1);
+        // or as a full page by any (of another length)
+        const int longest = __reduce_max_sync(FULL_MASK, at);
+        if (__any_sync(FULL_MASK, rows && at < longest)) {
+            for (int v = 0; v < W; ++v) {
+                const int q = b.parent[v];
+                if (rows && q >= 0 && b.len[q] / p.page_size > at)
+                    copy |= p.table[(long long)(row0 + q) * p.max_pages + at] == page;
+            }
         }
         if (rows && !is_page(p, page)) {
             copy = false;
@@ -293,11 +332,40 @@ template <bool SETTLED> __global__ void __launch_bounds__(RT) move_kernel(const 
     const int r = blockIdx.x / p.tiles, tile = blockIdx.x - r * p.tiles;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, W = p.W;
     const int row0 = r * W, j = tile * RT + tid, items = p.R * p.tiles;
+    const int q = lane < W ? p.parents[row0 + lane] : -1;   // (older than the kernel before)
+    const bool some = q >= 0 && q < W;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
+    // Everything that is read without the sums, on its way at once.
     const int nfreed = p.freed[blockIdx.x];
-    const bool moves = p.moved[(long long)blockIdx.x * RW + warp] >> lane & 1;
+    const unsigned changes = p.moved[(long long)blockIdx.x * RW + warp], who = p.copied[r];
+    const int old = lane < W ? p.lens[row0 + lane] : 0, count = p.header->count;
+    int f[4], c[4];   // of four tiles and requests a thread
+    if (!SETTLED) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            f[k] = tid * 4 + k < items ? p.freed[tid * 4 + k] : 0;
+            c[k] = tid * 4 + k < p.R ? __popc(p.copied[tid * 4 + k]) : 0;
+        }
+    }
+    const bool moves = changes >> lane & 1;
+    int mine[BATCH];
+    auto fetch = [&](int w0) {
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k)
+            mine[k] = w0 + k < W ? p.table[(long long)(row0 + w0 + k) * p.max_pages + j] : 0;
+    };
+    if (moves)
+        fetch(0);
+    const int len = __shfl_sync(FULL_MASK, old, some ? q : 0);
+    const int last = who >> lane & 1 ? len / p.page_size : -1;   // the place of a copy
+    if (warp == 0) {
+        pages[lane] = pages_of(p, old);
+        parent[lane] = some ? q : -1;
+        place[lane] = last;
+    }
+
     ReorderHeader h;
     int need0;          // copies of granted requests before this one, -1 if it is refused
     long long free0;    // pages that come back before this tile's
@@ -306,68 +374,52 @@ template <bool SETTLED> __global__ void __launch_bounds__(RT) move_kernel(const 
         need0 = p.needed_before[r];
         free0 = p.freed_before[blockIdx.x];
     } else {
-        // the sums over all tiles and requests, four a thread
-        h.count = p.header->count;
-        int f[4], c[4];
-        long long total, sum = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            f[k] = tid * 4 + k < items ? p.freed[tid * 4 + k] : 0;
-            c[k] = tid * 4 + k < p.R ? __popc(p.copied[tid * 4 + k]) : 0;
-        }
-        auto before = [&](const int (&x)[4], int *to) {   // exclusive sums of x, and all of it
-            const int s = x[0] + x[1] + x[2] + x[3];
-            long long all;
-            int at = (int)scan.run(s, all) - s;
+        // The sums over all tiles and requests, four a thread: of what comes
+        // back in the lower half of a word, of what is needed in the upper.
+        long long both;
+        auto sums = [&] {
+            const long long s = (long long)(c[0] + c[1] + c[2] + c[3]) << 32 | (unsigned)(f[0] + f[1] + f[2] + f[3]);
+            const long long at = scan.run(s, both) - s;
+            int fb = (int)at, cb = (int)(at >> 32);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                to[tid * 4 + k] = at;
-                at += x[k];
+                freed_before[tid * 4 + k] = fb;
+                needed_before[tid * 4 + k] = cb;
+                fb += f[k];
+                cb += c[k];
             }
-            return all;
+            __syncthreads();
         };
-        const long long back0 = before(f, freed_before);
-        __syncthreads();
+        sums();
         // what a request needs beyond what it gives back, and what it leaves
-        long long lacks[4], leaves = 0;
+        int lacks[4];
+        long long own2 = 0, all2;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const int q = tid * 4 + k;
-            const int end = (q + 1) * p.tiles;
-            const int own = q < p.R ? (end < items ? freed_before[end] : (int)back0) - freed_before[q * p.tiles] : 0;
+            const int i = tid * 4 + k, end = (i + 1) * p.tiles;
+            const int own = i < p.R ? (end < items ? freed_before[end] : (int)both) - freed_before[i * p.tiles] : 0;
             lacks[k] = max(0, c[k] - own);
-            leaves += max(0, own - c[k]);
-            sum += lacks[k];
+            own2 += (long long)lacks[k] << 32 | (unsigned)max(0, own - c[k]);
         }
-        long long left, lack;
-        scan.run(leaves, left);
-        left += h.count;
-        long long at = scan.run(sum, lack) - sum;
-        if (lack <= left) {   // all are granted
-            need0 = 0;
-            total = back0;
-        } else {
-            unsigned given = 0;
+        long long at = (scan.run(own2, all2) >> 32) - (own2 >> 32);
+        const long long left = (int)all2 + (long long)count;
+        need0 = 0;
+        if ((all2 >> 32) > left) {   // not all are granted: the sums of those that are
+            __shared__ bool refused[REORDER_SCAN];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 at += lacks[k];
-                given |= (lacks[k] == 0 || at <= left) << k;
-                c[k] = given >> k & 1 ? c[k] : 0;
+                refused[tid * 4 + k] = lacks[k] != 0 && at > left;
+                c[k] = refused[tid * 4 + k] ? 0 : c[k];
             }
-            __shared__ bool refused[REORDER_SCAN];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                refused[tid * 4 + k] = !(given >> k & 1);
             __syncthreads();
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 f[k] = tid * 4 + k < items && refused[(tid * 4 + k) / p.tiles] ? 0 : f[k];
-            total = before(f, freed_before);
+            sums();
             need0 = refused[r] ? -1 : 0;
         }
-        const long long taken = before(c, needed_before);
-        __syncthreads();
-        h = heights(p, h.count, total, taken);
+        h = heights(p, count, (int)both, both >> 32);
         need0 = need0 < 0 ? -1 : needed_before[r];
         free0 = freed_before[blockIdx.x];
     }
@@ -387,27 +439,12 @@ template <bool SETTLED> __global__ void __launch_bounds__(RT) move_kernel(const 
         return;
     }
 
-    // what comes back onto the stack, the first on top
-    const int32_t *list = p.pages + (long long)blockIdx.x * W * RT;
+    // The pages for this request's copies: of those that came back the t-th,
+    // or one that was free before.
     const long long raised = h.count + h.back;
-    for (int i = tid; i < nfreed; i += RT) {
-        const long long at = raised - 1 - (free0 + i);
-        if (at >= 0 && at < p.num_pages)
-            p.free_pages[at] = list[i];
-    }
-
-    // Lengths, and the pages for this request's copies: of those that came
-    // back the t-th, or one that was free before.
     if (warp == 0) {
-        const int q = lane < W ? p.parents[row0 + lane] : -1;
-        const bool some = q >= 0 && q < W;
-        const int old = lane < W ? p.lens[row0 + lane] : 0;
-        const int len = __shfl_sync(FULL_MASK, old, some ? q : 0);
-        const unsigned who = p.copied[r];
-        const bool copy = who >> lane & 1;
         int page = -1;
-        const int last = copy ? len / p.page_size : -1;
-        if (copy && last / RT == tile) {
+        if (last >= 0 && last / RT == tile) {
             const int t = need0 + __popc(who & ((1u << lane) - 1));
             const int at = h.top - 1 - t;
             if (at >= h.count) {
@@ -434,55 +471,89 @@ template <bool SETTLED> __global__ void __launch_bounds__(RT) move_kernel(const 
             c[1] = page;
         }
         if (lane < W) {
-            pages[lane] = pages_of(p, old);
-            parent[lane] = some ? q : -1;
-            place[lane] = last;
             taken_page[lane] = page;
             if (tile == 0)
                 p.seqlens[row0 + lane] = some ? len : 0;
         }
     }
-    __syncthreads();
+    // what comes back onto the stack, the first on top
+    const int32_t *list = p.pages + (long long)blockIdx.x * W * RT;
+    for (int i = tid; i < nfreed; i += RT) {
+        const long long at = raised - 1 - (free0 + i);
+        if (at >= 0 && at < p.num_pages)
+            p.free_pages[at] = list[i];
+    }
     if (moves) {
-#pragma unroll 8
-        for (int w = 0; w < W; ++w)
-            if (j < pages[w])
-                e[w][tid] = p.table[(long long)(row0 + w) * p.max_pages + j];
-        for (int w = 0; w < W; ++w) {
-            const int q = parent[w];
-            if (q >= 0 && q != w && j < pages[q] && j != place[w] && !(j < pages[w] && e[w][tid] == e[q][tid]))
-                p.table[(long long)(row0 + w) * p.max_pages + j] = e[q][tid];
+        for (int w0 = 0; w0 < W; w0 += BATCH) {
+            if (w0)
+                fetch(w0);
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k)
+                e[w0 + k][tid] = mine[k];
         }
     }
-    // (a beam may keep its parent's table, itself, and still need a copy: no other thread writes there)
     __syncthreads();
+    if (moves) {
+        for (int w0 = 0; w0 < W; w0 += BATCH) {
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                const int w = w0 + k, from = parent[w];
+                const int entry = e[max(from, 0)][tid];
+                if (from >= 0 && from != w && j < pages[from] && j != place[w] && !(j < pages[w] && e[w][tid] == entry))
+                    p.table[(long long)(row0 + w) * p.max_pages + j] = entry;
+            }
+        }
+    }
+    // (no other thread writes to a copy's place)
     if (tid < W && place[tid] >= 0 && place[tid] / RT == tile)
         p.table[(long long)(row0 + tid) * p.max_pages + place[tid]] = taken_page[tid];
 }
 
-// Rows of a page to another one's, of every head: a CTA a copy and head of K
-// or V.  The rows lie one behind the other.
-__global__ void __launch_bounds__(256) copy_kernel(const CopyParams p)
+// Rows of a page to another one's, of every head of K and V: the filled rows of
+// a head lie one behind the other, and a CTA takes a slice of all of them,
+// COPY_DEEP vectors a thread on their way at once.
+constexpr int COPY_THREADS = 256, COPY_DEEP = 8;
+
+__global__ void __launch_bounds__(COPY_THREADS) copy_kernel(const CopyParams p)
 {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int32_t *c = p.copies + (long long)blockIdx.x * 3;
     const int from = c[0], to = c[1], rows = min(c[2], p.page_size);
     if (from < 0 || rows <= 0)
         return;
     if (from >= p.num_pages || to < 0 || to >= p.num_pages) {
-        if (threadIdx.x == 0)
+        if (threadIdx.x == 0 && blockIdx.y == 0)
             atomicOr(p.status, STATUS_BAD_PAGE);
         return;
     }
-    const long long vecs = (long long)rows * p.row_vecs;
-    const long long head = (long long)p.page_size * p.row_vecs;
-    for (unsigned y = blockIdx.y; y < 2u * p.H; y += gridDim.y) {
-        const bool isv = y >= (unsigned)p.H;
-        uint4 *pages = static_cast<uint4 *>(isv ? p.v_pages : p.k_pages);
-        const int h = (int)(isv ? y - p.H : y);
-        const uint4 *src = pages + (from * (long long)p.H + h) * head;
-        uint4 *dst = pages + (to * (long long)p.H + h) * head;
-        for (long long i = threadIdx.x; i < vecs; i += 256)
-            dst[i] = src[i];
+    const unsigned head = (unsigned)rows * p.row_vecs;   // filled vectors of a head
+    const unsigned all = 2u * p.H * head;                // (below 2^31)
+    const unsigned inverse = 0xffffffffu / head + 1;     // i / head by a product: one too many at most (head >= 4)
+    const long long pitch = (long long)p.page_size * p.row_vecs, src = from * (long long)p.H, dst = to * (long long)p.H;
+    for (unsigned i0 = blockIdx.y * COPY_THREADS * COPY_DEEP; i0 < all; i0 += gridDim.y * COPY_THREADS * COPY_DEEP) {
+        uint4 x[COPY_DEEP];
+        uint4 *at[COPY_DEEP];
+#pragma unroll
+        for (int k = 0; k < COPY_DEEP; ++k) {
+            const unsigned i = i0 + k * COPY_THREADS + threadIdx.x;
+            at[k] = nullptr;
+            if (i < all) {
+                unsigned y = __umulhi(i, inverse), v = i - y * head;
+                if (v >= head) {
+                    --y;
+                    v += head;
+                }
+                const bool isv = y >= (unsigned)p.H;
+                const unsigned h = isv ? y - p.H : y;
+                uint4 *pages = static_cast<uint4 *>(isv ? p.v_pages : p.k_pages);
+                x[k] = pages[(src + h) * pitch + v];
+                at[k] = pages + (dst + h) * pitch + v;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < COPY_DEEP; ++k)
+            if (at[k])
+                *at[k] = x[k];
     }
 }
 
@@ -522,8 +593,8 @@ cudaError_t launch_reorder(const ReorderParams &p, cudaStream_t s)
 
 cudaError_t launch_copy_pages(const CopyParams &p, cudaStream_t s)
 {
-    copy_kernel<<<dim3(p.n, (unsigned)min(2LL * p.H, 65535LL)), 256, 0, s>>>(p);
-    return cudaGetLastError();
+    const long long most = 2LL * p.H * p.page_size * p.row_vecs, slice = COPY_THREADS * COPY_DEEP;
+    return launch_behind(copy_kernel, dim3(p.n, (unsigned)min((most + slice - 1) / slice, 65535LL)), COPY_THREADS, s, p);
 }
 
 }  // namespace fd

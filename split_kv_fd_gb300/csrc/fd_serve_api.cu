@@ -731,6 +731,9 @@ fd_status fd_copy_pages(const int32_t *copies, int n, int Hkv, int d, fd_dtype d
         return FD_ERR_INVALID_ARG;
     if ((dtype != FD_F32 && dtype != FD_E4M3 && !is16(dtype)) || (d != 64 && d != 128 && d != 256))
         return FD_ERR_UNSUPPORTED;
+    const int row_vecs = d * (dtype == FD_F32 ? 4 : dtype == FD_E4M3 ? 1 : 2) / 16;
+    if ((long long)Hkv * page_size > INT_MAX / 2 / row_vecs)
+        return FD_ERR_UNSUPPORTED;   // pages of 16 GB and more
     if (n == 0 || Hkv == 0)
         return FD_OK;
     if (!copies || !aligned(copies, 4) || !k_pages || !v_pages || !aligned(k_pages, 16) || !aligned(v_pages, 16))
@@ -741,7 +744,7 @@ fd_status fd_copy_pages(const int32_t *copies, int n, int Hkv, int d, fd_dtype d
     p.n = n;
     p.H = Hkv;
     p.page_size = page_size;
-    p.row_vecs = d * (dtype == FD_F32 ? 4 : dtype == FD_E4M3 ? 1 : 2) / 16;
+    p.row_vecs = row_vecs;
     p.k_pages = k_pages;
     p.v_pages = v_pages;
     p.num_pages = num_pages;

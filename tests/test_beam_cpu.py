@@ -46,3 +46,50 @@ def test_binding_refuses():
     x, sc = torch.zeros(2, 3, 10), torch.zeros(2, 3)
     with pytest.raises(ValueError):
         fd.beam_select(x, sc)
+
+
+def _reorder(lib, **kw):
+    a = dict(par=X, R=2, W=4, sl=X, table=X, width=4, free=X, count=X, pages=9, page=16, copies=X, granted=X, ws=X, n=1 << 30, stream=None)
+    a.update(kw)
+    return lib.fd_reorder_pages(*a.values())
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(R=-1), INVALID), (dict(W=0), INVALID), (dict(W=33), INVALID), (dict(R=1 << 30, W=2), INVALID), (dict(width=-1), INVALID),
+    (dict(pages=-1), INVALID), (dict(page=0), INVALID), (dict(page=1 << 20, width=1 << 12), INVALID),
+    (dict(page=1 << 20, pages=1 << 12), INVALID), (dict(par=None), INVALID), (dict(par=P(4098)), INVALID), (dict(sl=None), INVALID),
+    (dict(table=None), INVALID), (dict(table=P(4097)), INVALID), (dict(free=None), INVALID), (dict(count=None), INVALID),
+    (dict(copies=None), INVALID), (dict(granted=P(4098)), INVALID), (dict(ws=None), 3), (dict(n=100), 3), (dict(ws=P(4112)), 3),
+    (dict(R=0), 0)])
+def test_reorder_refuses(lib, kw, status):
+    assert _reorder(lib, **kw) == status
+
+
+def _copy(lib, **kw):
+    a = dict(copies=X, n=4, H=2, d=128, dt=BF16, kp=X, vp=X, page=16, pages=9, stream=None)
+    a.update(kw)
+    return lib.fd_copy_pages(*a.values())
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(n=-1), INVALID), (dict(H=-1), INVALID), (dict(page=0), INVALID), (dict(pages=-1), INVALID), (dict(pages=1 << 40), INVALID),
+    (dict(H=1 << 25), INVALID), (dict(d=96), UNSUPPORTED), (dict(d=0), INVALID), (dict(dt=7), UNSUPPORTED),
+    (dict(H=1 << 10, page=1 << 20, pages=9), UNSUPPORTED), (dict(copies=None), INVALID), (dict(copies=P(4098)), INVALID),
+    (dict(kp=None), INVALID), (dict(vp=P(4104)), INVALID), (dict(n=0), 0), (dict(H=0), 0)])
+def test_copy_refuses(lib, kw, status):
+    assert _copy(lib, **kw) == status
+
+
+def test_reorder_workspace_refuses():
+    for args in ((-1, 4, 100), (1, 0, 100), (1, 33, 100), (1, 4, -1), (1 << 30, 2, 4)):
+        assert fd.workspace_size_reorder(*args) == 0
+    assert fd.workspace_size_reorder(0, 4, 100) > 0 and fd.workspace_size_reorder(1, 4, 0) > 0
+
+
+def test_binding_refuses_host_tensors():
+    i = torch.zeros(2, 2, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        fd.reorder_pages(i, i.flatten(), torch.zeros(4, 3, dtype=torch.int32), i[0], i[0, :1], 16)
+    kp = torch.zeros(1, 2, 16, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        fd.copy_pages(torch.zeros(1, 3, dtype=torch.int32), kp, kp)
