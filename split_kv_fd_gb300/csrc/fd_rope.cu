@@ -12,6 +12,10 @@
 // arithmetic is some 3 operations an element.  A thread takes 8 + 8 elements
 // of a head, such that both halves of a pair are its own, and the same ones of
 // every HS-th head, so that its cosines and sines are loaded once a token.
+// 16K tokens of 64 query heads and 8 K/V heads of 128, bf16 (637 MB): 100 us,
+// 6.3 TB/s.  (More rows a thread at a time, or more tokens a CTA, cost registers
+// and so CTAs on an SM: 105-130 us.)  A decode step of 256 such tokens into
+// E4M3 pages: 5.2 us, a launch and the loads slot, table and offsets wait for.
 #include "fd_device.cuh"
 #include "fd_e4m3.cuh"
 #include "fd_pages.h"
@@ -20,6 +24,7 @@ namespace fd {
 namespace {
 
 constexpr int RT = 128;   // threads of a CTA
+constexpr int SMS = 152;
 
 // Not through the read-only path: q may be rotated in place.
 __device__ __forceinline__ uint4 load_once(const void *p)
@@ -94,40 +99,38 @@ __device__ __forceinline__ void turn(float &x, float &y, float c, float s)
     x = a;
 }
 
-// The sequence whose rows cu[b] .. cu[b+1]-1 hold t, or -1.
+// The sequence whose rows cu[b] .. cu[b+1]-1 hold t, or -1: how many of the
+// offsets are at or below t, by whole warps, 32 * TESTS of them at a time (a
+// bisection would wait for eight loads, one behind the other, of 256 sequences).
 __device__ __forceinline__ int sequence_of(const int32_t *cu, int B, int t)
 {
-    int lo = -1, hi = B;   // the last b with cu[b] <= t
-    while (lo < hi) {
-        const int mid = (int)(((long long)lo + hi + 1) >> 1);
-        if (__ldg(cu + mid) <= t)
-            lo = mid;
-        else
-            hi = mid - 1;
+    constexpr int TESTS = 16;
+    const int lane = threadIdx.x & 31;
+    long long lo = 0, n = (long long)B + 1;   // those before lo are, those from lo + n on are not
+    for (;;) {
+        const long long stride = (n + 32 * TESTS - 1) / (32 * TESTS);
+        int below = 0;
+#pragma unroll
+        for (int k = 0; k < TESTS; ++k) {
+            const long long i = (k * 32 + lane + 1) * stride - 1;   // the last of its stretch
+            below += i < n && __ldg(cu + lo + i) <= t;
+        }
+        const long long skip = __reduce_add_sync(FULL_MASK, below) * stride;
+        lo += skip;
+        if (stride == 1)
+            break;
+        n = min(n - skip, stride - 1);
+        if (n <= 0)
+            break;
     }
-    return lo < B ? lo : -1;
+    return lo >= 1 && lo <= B ? (int)lo - 1 : -1;
 }
 
-template <typename T, bool F8, bool PAIRS> __global__ void __launch_bounds__(RT) rope_kernel(const RopeParams p)
+// A CTA a token, or, with gridDim.y > 1, a share of its heads.
+template <typename T, bool F8, bool PAIRS>
+__global__ void __launch_bounds__(RT) rope_kernel(const RopeParams p)
 {
     const int t = blockIdx.x;
-    const int slot = __ldg(p.slots + t);
-    if (slot < 0)
-        return;
-    const int pos = __ldg(p.positions + t);
-    const bool out = slot >= p.num_slots, off = pos < 0 || pos >= p.max_position;
-    if (out || off) {
-        if (threadIdx.x == 0)
-            atomicOr(p.status, (out ? STATUS_BAD_PAGE : 0u) | (off ? STATUS_BAD_INDEX : 0u));
-        return;
-    }
-    int b = 0;
-    if (F8) {
-        b = sequence_of(p.cu, p.B, t);
-        if (b < 0)
-            return;
-    }
-
     const int per = p.d / 16;                  // threads of a head: a power of two
     const int j = threadIdx.x & (per - 1), half = p.rot / 2;
     // this thread's elements, e0 and e1 and the 7 behind each, and whether they turn
@@ -136,6 +139,29 @@ template <typename T, bool F8, bool PAIRS> __global__ void __launch_bounds__(RT)
     if (!PAIRS && turns) {
         e0 = 8 * j;
         e1 = half + 8 * j;
+    }
+    const int heads = p.Hq + 2 * p.H, hs = RT / per, first = threadIdx.x / per + blockIdx.y * hs;
+    Eight<T> x, y;
+    auto load = [&](int h) {
+        const bool isq = h < p.Hq, isv = h >= p.Hq + p.H;
+        const int hk = isq ? h : h - p.Hq - (isv ? p.H : 0);
+        const T *from = static_cast<const T *>(isq ? p.q : isv ? p.v : p.k) +
+                        t * (isq ? p.q_stride : isv ? p.v_stride : p.k_stride) + (long long)hk * p.d;
+        x.load(from + e0);
+        y.load(from + e1);
+    };
+    if (first < heads)
+        load(first);   // (before it is known whether and where to it goes)
+
+    const int slot = __ldg(p.slots + t), pos = __ldg(p.positions + t);
+    const int b = F8 ? sequence_of(p.cu, p.B, t) : 0;
+    if (slot < 0 || b < 0)
+        return;
+    const bool out = slot >= p.num_slots, off = pos < 0 || pos >= p.max_position;
+    if (out || off) {
+        if (threadIdx.x == 0 && blockIdx.y == 0)
+            atomicOr(p.status, (out ? STATUS_BAD_PAGE : 0u) | (off ? STATUS_BAD_INDEX : 0u));
+        return;
     }
     float c[8], s[8];
     if (turns) {
@@ -149,15 +175,11 @@ template <typename T, bool F8, bool PAIRS> __global__ void __launch_bounds__(RT)
         }
     }
     const long long page = slot / p.page_size, at = slot % p.page_size;
-    const int heads = p.Hq + 2 * p.H, hs = RT / per;
-    for (int h = threadIdx.x / per + blockIdx.y * hs; h < heads; h += hs * gridDim.y) {
+    for (int h = first; h < heads; h += hs * gridDim.y) {
         const bool isq = h < p.Hq, isv = h >= p.Hq + p.H;
         const int hk = isq ? h : h - p.Hq - (isv ? p.H : 0);
-        const T *from = static_cast<const T *>(isq ? p.q : isv ? p.v : p.k) +
-                        t * (isq ? p.q_stride : isv ? p.v_stride : p.k_stride) + (long long)hk * p.d;
-        Eight<T> x, y;
-        x.load(from + e0);
-        y.load(from + e1);
+        if (h != first)
+            load(h);
         const bool turn_it = turns && !isv;
         float f[16];
         if (turn_it || (F8 && !isq)) {
@@ -195,7 +217,14 @@ template <typename T, bool F8, bool PAIRS> __global__ void __launch_bounds__(RT)
 
 template <typename T, bool F8> cudaError_t launch_t(const RopeParams &p, cudaStream_t s)
 {
-    const dim3 grid(p.T);
+    // Passes of a CTA over a token's heads; shared between CTAs where a CTA a
+    // token leaves SMs with fewer than four (one token of 32 + 8 heads 2.9 ->
+    // 2.1 us, 256 of 64 + 8 into E4M3 pages 5.2, with twice as many 5.8, with
+    // none 7.7).  16K tokens gain nothing (129 us in five shares, 100 in one:
+    // each reads the table's row).
+    const int passes = (int)((((long long)p.Hq + 2LL * p.H) * (p.d / 16) + RT - 1) / RT);
+    const int share = (4 * SMS + p.T - 1) / p.T;
+    const dim3 grid(p.T, passes < share ? passes : share);
     if (p.pairs)
         rope_kernel<T, F8, true><<<grid, RT, 0, s>>>(p);
     else
