@@ -170,11 +170,6 @@ template <typename T> struct Place {
     }
 };
 
-__device__ __forceinline__ bool is_live(const SelectParams &p, long long row)
-{
-    return isfinite(p.scores[row]) && !(p.finished && p.finished[row]);
-}
-
 // 16 bytes of a row to this thread's own place in shared memory.
 __device__ __forceinline__ void copy_ahead(uint4 *to, const uint4 *from)
 {
@@ -199,7 +194,7 @@ template <typename T> __global__ void __launch_bounds__(ST, SEL_CTAS) rows_kerne
     const long long me = blockIdx.x * (long long)SW + warp;
     const long long row = me / p.parts;
     const int part = (int)(me - row * p.parts);
-    if (row >= (long long)p.R * p.W || !is_live(p, row))
+    if (row >= (long long)p.R * p.W)
         return;
     const int r = (int)(row / p.W);
     const Place<T> at(p, r, (int)(row - (long long)r * p.W));
@@ -219,6 +214,13 @@ template <typename T> __global__ void __launch_bounds__(ST, SEL_CTAS) rows_kerne
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i)
         ahead(g0 + i * U, i);
+    // (the first are on their way before it is known whether the beam counts)
+    const float score = p.scores[row];
+    const bool over = p.finished && p.finished[row];
+    if (!isfinite(score) || over) {
+        copies_landed<0>();
+        return;
+    }
 
     float m = minus_inf(), s = 0.f;
     int stage = 0;

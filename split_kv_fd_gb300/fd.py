@@ -569,7 +569,7 @@ def _call(what, dev, stream, *args):
     (default: the device's current one)."""
     fn = getattr(_lib or load(), what)
     raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         st = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
@@ -600,7 +600,10 @@ def _rows(t, name):
     are contiguous (a view of a fused projection has them further apart)."""
     if t.dim() != 3:
         raise ValueError(f"{name} must be [T, H, d]")
-    (T, H, d), (far, head, one) = t.shape, t.stride()
+    T, H, d = t.shape
+    if t.is_contiguous():
+        return H * d
+    far, head, one = t.stride()
     row = H * d
     if T == 0 or row == 0:
         return row
@@ -738,10 +741,11 @@ def _rope_args(k, v, slots, positions, rope, k_pages, v_pages, q, q_out, interle
             raise ValueError("q must be [T, Hq, d] of k's tokens, head dim and dtype")
         Hq = q.shape[1]
         if q_out is None:
-            q_out = _empty(stream, q.shape, dtype=q.dtype, device=q.device)
+            q_out, out_stride = _empty(stream, q.shape, dtype=q.dtype, device=q.device), Hq * d
         elif q_out.shape != q.shape or q_out.dtype != q.dtype:
             raise ValueError("q_out must have q's shape and dtype")
-        out_stride = _rows(q_out, "q_out")
+        else:
+            out_stride = _rows(q_out, "q_out")
     args = (positions.data_ptr(), rope.data_ptr(), rope.shape[0], rope.shape[1], bool(interleaved))
     sizes = (T, Hq, H, d, q_stride, k_stride, v_stride, rest[0], _address(q_out) if Hq else None, out_stride, *rest[1:])
     return args, sizes, q_out
@@ -995,6 +999,9 @@ def workspace_size_reorder(R, W, max_pages) -> int:
     return load().fd_workspace_size_reorder(R, W, max_pages)
 
 
+_known_reorder_bytes = functools.lru_cache(maxsize=1024)(workspace_size_reorder)   # (of the sizes alone)
+
+
 def reorder_pages(parents, seqlens, block_table, free_pages, free_count, page_size, copies=None, granted=None, workspace=None,
                   stream=None):
     """The beams' cached states to those of their parents, in place
@@ -1031,7 +1038,7 @@ def reorder_pages(parents, seqlens, block_table, free_pages, free_count, page_si
     else:
         _int32(granted, (R,), "granted")
     if workspace is None:
-        workspace = _empty(stream, max(workspace_size_reorder(R, W, width), 256), dtype=torch.uint8, device=where)
+        workspace = _empty(stream, max(_known_reorder_bytes(R, W, width), 256), dtype=torch.uint8, device=where)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous and on the parents' device")
     _call("fd_reorder_pages", dev, stream, parents.data_ptr(), R, W, seqlens.data_ptr(), block_table.data_ptr(), width,
