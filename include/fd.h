@@ -673,9 +673,9 @@ size_t fd_workspace_size_beam(int R, int W, int V, int K);
  * float32.  Where fewer than K are left the rest is -inf, parent -1, token
  * -1, finished.
  * The sum of exponentials is float32, its logarithm and all after it close to
- * 48 bits: continuations of one beam are ordered as their logits are, those of
- * two beams as their scores where these differ by more than some 1e-7 of a
- * sum's rounding.
+ * 48 bits: continuations of one beam are ordered as their logits are (unless
+ * these differ by less than some 2^-46 of the score), those of two beams as
+ * their scores where these differ by more than some 1e-7.
  * 1 <= W <= 32, 1 <= K <= 64, K <= W * V, W * V <= 2^30; outputs must not
  * overlap inputs.
  */

@@ -17,6 +17,7 @@ constexpr int SEG_BYTES = 512;
 constexpr int SEL_SEGS = 4;       // segments that a warp reads at a time
 constexpr int SEL_THREADS = 256;
 constexpr int SEL_CTAS = 4;       // of the rows' kernel on an SM
+constexpr int SEL_RUN = 8;        // reads of a part, at most
 constexpr int SEL_STAGES = 3;     // reads under way or taken, of a warp
 
 struct SelectParams {
@@ -32,7 +33,8 @@ struct SelectParams {
     // workspace: of every row the largest value of each segment, and the
     // maximum and sum of exponentials of each part
     int segs;                    // segments of a row
-    int run, parts;              // times SEL_SEGS segments: a part; parts of a row
+    int parts;                   // of a row
+    int reads, longer;           // of SEL_SEGS segments: a part's, and how many parts have one more
     float *seg_max;              // [R * W, segs]
     float2 *part;                // [R * W, parts]
 };

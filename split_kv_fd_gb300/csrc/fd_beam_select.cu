@@ -182,8 +182,8 @@ template <int N> __device__ __forceinline__ void copies_landed()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A warp a part of a row: `run` times U segments.  Those that lie within the
-// row are copied AHEAD of their turn, each 16 bytes by the thread that takes
+// A warp a part of a row, U segments at a time.  Those that lie within the row
+// are copied AHEAD of their turn, each 16 bytes by the thread that takes
 // them: no thread waits for another, and what is under way costs no register.
 template <typename T> __global__ void __launch_bounds__(ST, SEL_CTAS) rows_kernel(const SelectParams p)
 {
@@ -191,17 +191,16 @@ template <typename T> __global__ void __launch_bounds__(ST, SEL_CTAS) rows_kerne
     extern __shared__ uint4 stages[];   // [warp][stage][U][lane]
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long me = blockIdx.x * (long long)SW + warp;
-    const long long row = me / p.parts;
+    const unsigned me = blockIdx.x * SW + warp, row = me / p.parts, r = row / p.W;
     const int part = (int)(me - row * p.parts);
-    if (row >= (long long)p.R * p.W)
+    if (row >= (unsigned)p.R * p.W)
         return;
-    const int r = (int)(row / p.W);
-    const Place<T> at(p, r, (int)(row - (long long)r * p.W));
-    float *seg_max = p.seg_max + row * p.segs;
+    const Place<T> at(p, (int)r, (int)(row - r * p.W));
+    float *seg_max = p.seg_max + (long long)row * p.segs;
     uint4 *mine = stages + warp * STAGES * U * 32 + lane;
     const uint4 *from = reinterpret_cast<const uint4 *>(at.base) + lane;
-    const int g0 = part * p.run * U, g1 = min(g0 + p.run * U, p.segs);
+    const int g0 = (part * p.reads + min(part, p.longer)) * U;
+    const int g1 = min(g0 + (p.reads + (part < p.longer)) * U, p.segs);
     auto within = [&](int g) { return g < g1 && g * SEG >= at.first && (g + U) * SEG <= at.end; };
     auto ahead = [&](int g, int stage) {
         if (within(g)) {

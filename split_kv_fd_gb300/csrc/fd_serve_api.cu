@@ -552,7 +552,7 @@ namespace {
 // The parts of a selection and its workspace, for the type with the most
 // segments (`elem` bytes an element).
 struct SelectLayout {
-    int segs, run, parts;
+    int segs, parts;
     size_t part, total;
 };
 
@@ -566,15 +566,17 @@ SelectLayout select_layout(int R, int W, int V, int elem, int sms)
 {
     SelectLayout l;
     l.segs = select_segs(V, elem);
-    // As many warps as the card holds, if there is that much to read.
-    const int reads = (l.segs + SEL_SEGS - 1) / SEL_SEGS;   // of a row
-    const long long all = (long long)R * W * reads, warps = (long long)sms * SEL_CTAS * (SEL_THREADS / 32);
-    const long long least = (all + warps - 1) / warps;
-    l.run = (int)(least < 1 ? 1 : least < reads ? least : reads);
-    // (a row's last part is shorter: without this a few CTAs would wait for all others)
-    while (l.run > 1 && l.run < reads && (long long)R * W * ((reads + l.run - 1) / l.run) > warps)
-        ++l.run;
-    l.parts = (reads + l.run - 1) / l.run;
+    // A warp a part: as many as the card holds at once beside a CTA for each
+    // request's choice, which then waits there already (32 requests of 4 beams,
+    // float32: 17.8 us, with all places taken 19.5); and more where a part would
+    // be longer than SEL_RUN reads: shorter ones even out what finished beams
+    // leave over (64 requests of 8 beams, a tenth finished: 30.6, of 14 reads
+    // 34.6).
+    const long long reads = (l.segs + SEL_SEGS - 1) / SEL_SEGS, rows = (long long)R * W;
+    const long long least = (reads + SEL_RUN - 1) / SEL_RUN, ctas = (long long)sms * SEL_CTAS - (R < sms ? R : sms);
+    long long parts = rows > 0 ? ctas * (SEL_THREADS / 32) / rows : 1;
+    parts = parts < least ? least : parts;
+    l.parts = (int)(parts < reads ? parts : reads);
     l.part = round_up((size_t)R * W * l.segs * sizeof(float), 256);
     l.total = l.part + (size_t)R * W * l.parts * sizeof(float2);
     return l;
@@ -611,6 +613,8 @@ fd_status fd_beam_select(const void *logits, fd_dtype dtype, long long request_s
     if (sms <= 0)
         return FD_ERR_CUDA;
     const SelectLayout l = select_layout(R, W, V, elem, sms);
+    if ((long long)R * W * l.parts > INT_MAX)
+        return FD_ERR_UNSUPPORTED;   // more rows than a card holds
     if (!workspace || workspace_bytes < l.total || !aligned(workspace, 256))
         return FD_ERR_WORKSPACE;
     SelectParams p;
@@ -631,8 +635,9 @@ fd_status fd_beam_select(const void *logits, fd_dtype dtype, long long request_s
     p.out_tokens = out_tokens;
     p.out_finished = out_finished;
     p.segs = l.segs;
-    p.run = l.run;
     p.parts = l.parts;
+    p.reads = (l.segs + SEL_SEGS - 1) / SEL_SEGS / l.parts;
+    p.longer = (l.segs + SEL_SEGS - 1) / SEL_SEGS % l.parts;
     p.seg_max = static_cast<float *>(workspace);
     p.part = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + l.part);
     return launch_select(p, stream_of(stream)) == cudaSuccess ? FD_OK : FD_ERR_CUDA;

@@ -199,6 +199,28 @@ def test_rows_outside_the_sequences_stay():
     assert bool((out[:4] == 5.0).all()) and bool((out[21:] == 5.0).all()) and not bool((out[4:21] == 5.0).all(-1).any())
 
 
+@pytest.mark.parametrize("B", [1, 511, 512, 3000, 300000])
+def test_many_sequences(B):
+    """The sequence of each token among many, empty ones between: its scale, seen in the bytes."""
+    g = torch.Generator(device="cuda").manual_seed(B)
+    T = 600
+    cut = torch.randint(1, T - 1, (B + 1,), device="cuda", generator=g).sort().values
+    cu = cut.to(torch.int32)
+    k = torch.ones(T, 1, 64, dtype=torch.bfloat16, device="cuda")
+    scale = 2.0 ** -torch.randint(0, 9, (B, 1), device="cuda", generator=g).float()
+    pos, table = torch.zeros(T, dtype=torch.int32, device="cuda"), _table(1, 64)
+    slots = torch.arange(T, device="cuda", dtype=torch.int32)
+    kp, vp = (torch.zeros(T // 16 + 1, 1, 16, 64, dtype=torch.uint8, device="cuda") for _ in range(2))
+    fd.append_rope_paged_fp8(k, k, scale, scale, cu, slots, pos, table, kp, vp)
+    t = torch.arange(T, device="cuda")
+    b = torch.searchsorted(cut, t, right=True) - 1
+    inside = (b >= 0) & (b < B)
+    want = torch.where(inside, 1.0 / scale[b.clamp(0, B - 1), 0], 0.0)
+    for p in (kp, vp):
+        got = p.view(torch.float8_e4m3fn).float()[t // 16, 0, t % 16]
+        assert torch.equal(got, want[:, None].expand(T, 64))
+
+
 def test_far_positions_and_large_strides():
     """A table past 2^31 bytes' worth of elements, read at its end; rows a long way apart."""
     rot, far = 256, (1 << 23) + 77     # 2^31 elements and more
