@@ -15,9 +15,15 @@
 //    and of a lower index).  Only some K segments are read again, and the K-th
 //    largest maximum is a bound that few of their elements reach.
 //
-// Across beams the order is decided by sums in two float32 parts, close to 48
-// bits, so that only the sum of exponentials is rounded to less: neighbours
-// nearer than some 1e-7 may change places, those of one beam never do.
+// Candidates are ordered by sums in two float32 parts, close to 48 bits, so
+// that only the sum of exponentials is rounded to less: neighbours of two beams
+// nearer than some 1e-7 may change places, those of one beam do not.
+//
+// 64 requests of 8 beams over 131072 tokens, bf16, a tenth of them finished (121
+// MB): 31 us, of which the rows take some 23 (a bare read of as many bytes
+// 20.5) and the top 7; 32 of 4 over 128000 in float32 (66 MB) 17.7, 12.6 and 5;
+// one of 4 over 32000 6.3, where both are chains of dependent steps.  Constant
+// rows, which pass the bound whole, take the slower way: 4 x 32000 22 us.
 #include "fd_beam.h"
 #include "fd_device.cuh"
 
@@ -297,7 +303,8 @@ template <typename T> __global__ void __launch_bounds__(ST, SEL_CTAS) rows_kerne
 struct Cand {
     uint64_t key;
     int idx;
-    __device__ __forceinline__ bool before(uint64_t k, int i) const { return key > k || (key == k && idx < i); }
+    // (no branch: loops of it keep their loads on the way)
+    __device__ __forceinline__ bool before(uint64_t k, int i) const { return (key > k) | ((key == k) & (idx < i)); }
 };
 
 __device__ __forceinline__ uint32_t ordered(float x)
@@ -379,6 +386,7 @@ __device__ __forceinline__ void prune(Lists &l, int K)
             l.nb = 0;
         __syncthreads();
         int rank = 0;
+#pragma unroll 8
         for (int i = 0; i < ST; ++i)
             rank += l.best[i].before(best.key, best.idx);
         if (rank == K - 1)
@@ -396,6 +404,7 @@ __device__ __forceinline__ void prune(Lists &l, int K)
     for (int i = tid; i < have; i += ST) {
         const Cand c = from[i];
         int rank = 0;
+#pragma unroll 8
         for (int j = 0; j < have; ++j)
             rank += from[j].before(c.key, c.idx);
         if (rank < K)
@@ -714,6 +723,8 @@ template <typename T> __global__ void __launch_bounds__(ST) top_kernel(const Sel
             copies_landed<0>();
 #pragma unroll 1
             for (int k = k0 + tid; k < end; k += ST) {
+                if (*(volatile int *)&l.n > FEW)
+                    break;   // it is the slower way
                 const Place<T> at = place(k, w, i);
                 const uint4 x = stage[k - k0];
                 const Base b = base[w];
@@ -725,7 +736,7 @@ template <typename T> __global__ void __launch_bounds__(ST) top_kernel(const Sel
 #pragma unroll
                 for (int e = 0; e < VE; ++e)
                     some |= (f[e] >= limit && f[e] > minus_inf()) << e;
-                for (; some; some &= some - 1) {
+                for (; some && *(volatile int *)&l.n <= FEW; some &= some - 1) {
                     const int e = __ffs(some) - 1;
                     const uint64_t key = value_key(b, sane(element(x, e, (const T *)nullptr)));
                     const int to = key ? atomicAdd(&l.n, 1) : FEW;

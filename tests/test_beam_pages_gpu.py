@@ -179,6 +179,21 @@ def test_many_requests():
     assert sum(granted) == sum(1 for r in range(R) if (r % 12 + 1) % 4 == 0) + 500
 
 
+@pytest.mark.parametrize("spare", [3, 700])
+def test_wide_tables_of_many_requests(spare):
+    """More tiles of tables than are added up in one pass, most of them empty."""
+    rng = random.Random(spare)
+    s = BeamPool(rng, 220, 2, 2, 1300, (1, 40), (0, 10), spare=spare)
+    s.lens[0:2], s.lens[4] = [2599, 2600], 0        # one request over all of its tiles
+    for b, n in ((0, 2599), (1, 2600)):
+        s.table[b] = [100000 + b * 1300 + j if j >= 5 else s.table[b][j] for j in range(1300)]
+    s.free += [-1] * (110000 - s.pool)
+    for _ in range(3):
+        _check(s, [rng.choice([[0, 0], [1, 1], [0, 1], [1, 0], [-1, 0], [1, -1]]) for _ in range(220)])
+    _check(s, [[-1, -1]] * 220)
+    assert not any(s.lens)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16", "e4m3", "u8"])
 @pytest.mark.parametrize("H,page,d", [(1, 16, 64), (8, 64, 128), (3, 7, 256), (2, 256, 128), (40, 1, 64)])
 def test_copies(H, page, d, dtype):

@@ -108,6 +108,21 @@ def test_finished_beams():
     assert not bool(fd.beam_select(x, scores, 2)[3].any())
 
 
+@pytest.mark.parametrize("V,K,W", [(30, 12, 5), (3000, 64, 6), (90000, 20, 32)])
+def test_finished_beams_among_many_equal_ones(V, K, W):
+    """Rows that leave more candidates than fit the short list, with finished beams between, ahead and behind."""
+    x = torch.full((3, W, V), -0.5, device="cuda")
+    x[1] = torch.arange(V, device="cuda") % 5
+    x[2, :, : V // 2] = -math.inf
+    base = -1.0 - math.log(V)
+    scores = torch.full((3, W), -1.0, device="cuda")
+    done = torch.zeros(3, W, dtype=torch.bool, device="cuda")
+    done[:, 1], done[:, W - 1] = True, True
+    scores[:, 1], scores[:, W - 1] = base + 0.01, -50.0
+    for eos in (0, V - 1):
+        check_select(fd.beam_select(x, scores, K, finished=done, eos=eos), x, scores, K, done, eos)
+
+
 def test_few_continuations():
     """Beams without a score, masked tokens, rows that the mask leaves empty."""
     x, scores = _logits(5, 3, 900, "f16", 10)
