@@ -164,3 +164,60 @@ def test_beam_search(R, W, page, Hq, Hkv, d, rot, pairs, dtype, captured):
     # the requests end
     fd.reorder_pages(torch.full_like(parents, -1), lens, table, free, count, page)
     assert int(count) == pool and sorted(free.tolist()) == list(range(pool)) and not bool(lens.any())
+
+
+def test_beams_over_an_e4m3_cache():
+    """A prompt, its state to the beams, a token each and another choice, in
+    E4M3 pages: what each beam reads through its table is its own history,
+    turned and rounded, and its attention that over the same bytes in a row."""
+    R, W, Hq, Hkv, d, page, width = 2, 3, 8, 2, 128, 16, 6
+    B = R * W
+    m = Model(Hq, Hkv, d, 96, False, torch.bfloat16, seed=5)
+    rng = random.Random(5)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")   # noqa: E731
+    # the beams of a request read the same bytes, with the same scales
+    scale = [(torch.rand(R, Hkv, device="cuda", generator=torch.Generator(device="cuda").manual_seed(i)) / 50 + 0.01).repeat_interleave(W, 0)
+             .contiguous() for i in (1, 2)]
+    pool = B * width
+    free, count = torch.arange(pool, device="cuda").to(torch.int32), i32([pool])
+    table, lens = torch.zeros(B, width, dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")
+    kp, vp = (torch.full((pool, Hkv, page, d), 0x7f, dtype=torch.uint8, device="cuda") for _ in range(2))   # NaN
+
+    def write(target, tokens):
+        T = len(tokens)
+        slots, positions = (torch.empty(T, dtype=torch.int32, device="cuda") for _ in range(2))
+        cu = fd.resize_pages(lens, i32(target), table, free, count, page, slots=slots, positions=positions)
+        q, k, v = m.split(0, torch.tensor(tokens, device="cuda"))
+        return fd.append_rope_paged_fp8(k, v, *scale, cu, slots, positions, m.rope, kp.view(torch.float8_e4m3fn),
+                                        vp.view(torch.float8_e4m3fn), q=q)
+
+    beams = [[rng.randrange(VOCAB) for _ in range(n)] for n in (37, 16)]
+    write([len(beams[0]), 0, 0, len(beams[1]), 0, 0], beams[0] + beams[1])
+    beams = [[list(b)] * W for b in beams]
+    for parents in ([[0, 0, 0]] * R, [[2, 0, 0], [1, 1, 2]], [[0, 1, 1], [2, 2, 0]]):
+        copies, granted = fd.reorder_pages(i32(parents), lens, table, free, count, page)
+        fd.copy_pages(copies, kp.view(torch.float8_e4m3fn), vp.view(torch.float8_e4m3fn))
+        assert bool(granted.all())
+        beams = [[beams[r][p] + [rng.randrange(VOCAB)] for p in parents[r]] for r in range(R)]
+        q = write([len(b) for bs in beams for b in bs], [b[-1] for bs in beams for b in bs])
+        out, lse = fd.decode_gqa_paged_fp8(q, kp, vp, *scale, table, lens)
+        for b in range(B):
+            tokens = beams[b // W][b % W]
+            n = len(tokens)
+            at = torch.arange(n, device="cuda")
+            got = [x[table[b, at // page].long(), :, at % page] for x in (kp, vp)]
+            _, k, v = m.split(0, torch.tensor(tokens, device="cuda"))
+            row, half = m.rope[at][:, None], 48
+            f = k.float()
+            y = f.clone()
+            y[..., :half] = f[..., :half] * row[..., :half] - f[..., half:96] * row[..., half:]
+            y[..., half:96] = f[..., half:96] * row[..., :half] + f[..., :half] * row[..., half:]
+            for x, have, sc in ((y, got[0], scale[0]), (v.float(), got[1], scale[1])):
+                want = (x / sc[b][None, :, None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+                assert torch.equal(have, want), f"beam {b}"
+            plain = [x.transpose(0, 1).contiguous()[None] for x in got]   # [1, Hkv, n, d]
+            o, s = fd.decode_gqa_fp8(q[b:b + 1].contiguous(), *plain, scale[0][b:b + 1].contiguous(), scale[1][b:b + 1].contiguous())
+            # both are E4M3 decode on the tensor cores over the same bytes, in 16-bit or in 8-bit parts close to
+            # float32: a step of the output's type, 2^-8, of the largest value there may be
+            top = float((got[1].view(torch.float8_e4m3fn).float().abs().amax() * scale[1][b].amax()))
+            assert float((out[b] - o[0]).float().abs().max()) <= 2.0 ** -8 * top and float((lse[b] - s[0]).abs().max()) <= 1e-3

@@ -59,6 +59,18 @@ def test_strides():
     check_select(fd.beam_select(turned, scores.t().contiguous(), 4), turned, scores.t().contiguous(), 4)
 
 
+def test_rows_far_apart():
+    """Requests and beams whose distance passes 2^31 elements, by an odd number."""
+    V = 3001
+    far = 2 ** 31 + 1037
+    buf = torch.empty(far + 70000, dtype=torch.bfloat16, device="cuda")
+    for R, W, strides in ((2, 3, (far, 20001, 1)), (3, 2, (20001, far, 1))):
+        x = buf.as_strided((R, W, V), strides)
+        x.copy_((torch.randn(R, W, V, device="cuda", generator=torch.Generator(device="cuda").manual_seed(R)) * 3))
+        scores = -torch.rand(R, W, device="cuda", generator=torch.Generator(device="cuda").manual_seed(3))
+        check_select(fd.beam_select(x, scores, 8), x, scores, 8)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("V,K,W", [(64, 8, 4), (5000, 32, 4), (70000, 64, 2), (3000, 7, 1)])
 def test_ties_go_to_the_lowest_index(V, K, W, dtype):

@@ -239,6 +239,18 @@ def test_far_positions_and_large_strides():
     assert torch.equal(kp[0, 0, :4], _turn(k, rows, rot, False, torch.float32)[0][:, 0]) and torch.equal(vp[0, 0, :4], v[:, 0])
 
 
+def test_pages_far_into_a_pool():
+    """Rows behind 2^31 elements of a pool."""
+    P, H, page, d = 2100, 8, 512, 256
+    kp, vp = (torch.empty(P, H, page, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    slots = torch.tensor([P * page - 1, (P - 2) * page + 3, 5], dtype=torch.int32, device="cuda")
+    q, k, v, _, pos, table, _ = _case(3, 1, H, d, 16, 128, "bf16", seed=8)
+    fd.append_rope_paged(k, v, slots, pos, table, kp, vp)
+    want = _turn(k, table[pos.long()], 128, False, torch.float32)[0].bfloat16()
+    for t, s in enumerate(slots.tolist()):
+        assert torch.equal(kp[s // page, :, s % page], want[t]) and torch.equal(vp[s // page, :, s % page], v[t])
+
+
 def test_other_stream_and_graph():
     """On a stream of its own, and captured and replayed with new tokens in the same buffers."""
     q, k, v, slots, pos, table, P = _case(64, 8, 2, 128, 16, 128, "bf16", seed=21)
