@@ -617,7 +617,7 @@ def _rows(t, name):
 
 
 def _int32(t, shape, name):
-    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)}")
     if t.numel() > INT_MAX and max(shape) > INT_MAX:   # the C call's sizes are ints, and ctypes cuts what passes them
         raise ValueError(f"{name}: sizes must be below 2^31")
@@ -724,31 +724,46 @@ def append_paged_fp8(k, v, k_scale, v_scale, cu_new, slots, k_pages, v_pages, st
 
 def _rope_args(k, v, slots, positions, rope, k_pages, v_pages, q, q_out, interleaved, stream):
     """The arguments of the rotating appends from the positions on, and
-    q_out, checked or allocated."""
-    T, H, d, k_stride, v_stride, *rest = _append_args(k, v, slots, k_pages, v_pages)
+    q_out, checked or allocated.  (In one piece: the call is short, and every
+    further function shows in it.)"""
+    k_stride, v_stride = _rows(k, "k"), _rows(v, "v")
+    T, H, d = k.shape
+    kind = k.dtype
+    if v.shape != k.shape or v.dtype != kind or kind not in DTYPE_CODE:
+        raise ValueError("k and v must share one shape and dtype among float32/float16/bfloat16")
+    _int32(slots, (T,), "slots")
     _int32(positions, (T,), "positions")
-    if rope.dtype != torch.float32 or rope.dim() != 2 or not rope.is_contiguous():
+    pages = k_pages.shape
+    if len(pages) != 4 or v_pages.shape != pages or v_pages.dtype != k_pages.dtype or pages[1] != H or pages[3] != d:
+        raise ValueError("k_pages/v_pages must be [num_pages, Hkv, page_size, d] with Hkv, d of k")
+    if not (k_pages.is_contiguous() and v_pages.is_contiguous()):
+        raise ValueError("all tensors but packed rows must be contiguous")
+    table = rope.shape
+    if len(table) != 2 or rope.dtype != torch.float32 or not rope.is_contiguous():
         raise ValueError("rope must be contiguous float32 [max_position, rot]: cosines, then sines")
-    if max(rope.shape) > INT_MAX:
+    far, rot = table
+    if far > INT_MAX or rot > INT_MAX:
         raise ValueError("rope: sizes must be below 2^31")
-    Hq, q_stride, out_stride = 0, 0, 0
-    if q is None:
-        if q_out is not None:
-            raise ValueError("q_out without q")
-    else:
+    Hq, q_stride, out_stride, q_at, out_at = 0, 0, 0, None, None
+    if q is not None:
         q_stride = _rows(q, "q")
-        if q.dtype != k.dtype or q.shape[0] != T or q.shape[2] != d:
+        rows, Hq, dq = q.shape
+        if q.dtype != kind or rows != T or dq != d:
             raise ValueError("q must be [T, Hq, d] of k's tokens, head dim and dtype")
-        Hq = q.shape[1]
         if q_out is None:
-            q_out, out_stride = _empty(stream, q.shape, dtype=q.dtype, device=q.device), Hq * d
-        elif q_out.shape != q.shape or q_out.dtype != q.dtype:
+            q_out, out_stride = _empty(stream, q.shape, dtype=kind, device=q.device), Hq * d
+        elif q_out.shape != q.shape or q_out.dtype != kind:
             raise ValueError("q_out must have q's shape and dtype")
         else:
             out_stride = _rows(q_out, "q_out")
-    args = (positions.data_ptr(), rope.data_ptr(), rope.shape[0], rope.shape[1], bool(interleaved))
-    sizes = (T, Hq, H, d, q_stride, k_stride, v_stride, rest[0], _address(q_out) if Hq else None, out_stride, *rest[1:])
-    return args, sizes, q_out
+        if Hq:
+            q_at, out_at = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    return ((q_at, k.data_ptr(), v.data_ptr()),
+            (slots.data_ptr(), positions.data_ptr(), rope.data_ptr(), far, rot, bool(interleaved)),
+            (T, Hq, H, d, q_stride, k_stride, v_stride, DTYPE_CODE[kind], out_at, out_stride, k_pages.data_ptr(),
+             v_pages.data_ptr(), pages[2], pages[0]), q_out)
 
 
 def append_rope_paged(k, v, slots, positions, rope, k_pages, v_pages, q=None, q_out=None, interleaved=False, stream=None):
@@ -763,11 +778,10 @@ def append_rope_paged(k, v, slots, positions, rope, k_pages, v_pages, q=None, q_
     Tokens with a negative slot are skipped, their rows of q_out too.
     """
     dev = _one_device(k, v, slots, positions, rope, k_pages, v_pages, q, q_out)
-    args, sizes, q_out = _rope_args(k, v, slots, positions, rope, k_pages, v_pages, q, q_out, interleaved, stream)
+    rows, where, sizes, q_out = _rope_args(k, v, slots, positions, rope, k_pages, v_pages, q, q_out, interleaved, stream)
     if k_pages.dtype != k.dtype:
         raise ValueError("the pages must have k's dtype")
-    _call("fd_append_rope_paged", dev, stream, _address(q) if sizes[1] else None, k.data_ptr(), v.data_ptr(),
-          slots.data_ptr(), *args, *sizes)
+    _call("fd_append_rope_paged", dev, stream, *rows, *where, *sizes)
     return q_out
 
 
@@ -777,14 +791,14 @@ def append_rope_paged_fp8(k, v, k_scale, v_scale, cu_new, slots, positions, rope
     v_scale float32 [B, Hkv] and cu_new int32 [B+1] as in append_paged_fp8.
     Returns the rotated q, or None without q."""
     dev = _one_device(k, v, k_scale, v_scale, cu_new, slots, positions, rope, k_pages, v_pages, q, q_out)
-    args, sizes, q_out = _rope_args(k, v, slots, positions, rope, k_pages, v_pages, q, q_out, interleaved, stream)
+    rows, where, sizes, q_out = _rope_args(k, v, slots, positions, rope, k_pages, v_pages, q, q_out, interleaved, stream)
     if k_pages.dtype not in (torch.float8_e4m3fn, torch.uint8):
         raise ValueError("pages must be float8_e4m3fn (or uint8 E4M3 bytes)")
     B = cu_new.numel() - 1
     _scales(k_scale, v_scale, (B, sizes[2]))
     _int32(cu_new, (B + 1,), "cu_new")
-    _call("fd_append_rope_paged_fp8", dev, stream, _address(q) if sizes[1] else None, k.data_ptr(), v.data_ptr(),
-          k_scale.data_ptr(), v_scale.data_ptr(), cu_new.data_ptr(), slots.data_ptr(), *args, B, *sizes)
+    _call("fd_append_rope_paged_fp8", dev, stream, *rows, k_scale.data_ptr(), v_scale.data_ptr(), cu_new.data_ptr(),
+          *where, B, *sizes)
     return q_out
 
 
@@ -965,7 +979,7 @@ def beam_select(logits, scores, num=None, finished=None, eos=-1, workspace=None,
     (R, W, V), (far, near, one) = logits.shape, logits.stride()
     if V > 1 and one != 1:
         raise ValueError("logits: a beam's V must be contiguous")
-    if max(R, W, V) > INT_MAX:
+    if R > INT_MAX or W > INT_MAX or V > INT_MAX:
         raise ValueError("logits: sizes must be below 2^31")
     if scores.dtype != torch.float32 or scores.shape != (R, W) or not scores.is_contiguous():
         raise ValueError("scores must be contiguous float32 [R, W]")
@@ -977,17 +991,20 @@ def beam_select(logits, scores, num=None, finished=None, eos=-1, workspace=None,
     if not -1 <= eos < max(V, 1):
         raise ValueError("eos must be a token, or -1")
     where = logits.device
+    empty = torch.empty if stream is None else functools.partial(_empty, stream)
     if workspace is None:
         try:
             n = _known_beam_bytes(dev, R, W, V, K)
         except LookupError:
             n = 256   # the call itself says why
-        workspace = _empty(stream, n, dtype=torch.uint8, device=where)
+        workspace = empty(n, dtype=torch.uint8, device=where)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous and on the logits' device")
-    out = _empty(stream, (R, K), dtype=torch.float32, device=where)
-    parents, tokens = (_empty(stream, (R, K), dtype=torch.int32, device=where) for _ in range(2))
-    over = _empty(stream, (R, K), dtype=torch.bool, device=where)
+    shape = (R, K)
+    out = empty(shape, dtype=torch.float32, device=where)
+    parents = empty(shape, dtype=torch.int32, device=where)
+    tokens = empty(shape, dtype=torch.int32, device=where)
+    over = empty(shape, dtype=torch.bool, device=where)
     _call("fd_beam_select", dev, stream, logits.data_ptr(), DTYPE_CODE[logits.dtype], far, near, scores.data_ptr(),
           _address(finished), R, W, V, K, eos, out.data_ptr(), parents.data_ptr(), tokens.data_ptr(), over.data_ptr(),
           workspace.data_ptr(), workspace.numel() * workspace.element_size())
@@ -1029,16 +1046,17 @@ def reorder_pages(parents, seqlens, block_table, free_pages, free_count, page_si
     _int32(free_pages, (pool,), "free_pages")
     _int32(free_count, (1,), "free_count")
     where = parents.device
+    empty = torch.empty if stream is None else functools.partial(_empty, stream)
     if copies is None:
-        copies = _empty(stream, (B, 3), dtype=torch.int32, device=where)
+        copies = empty((B, 3), dtype=torch.int32, device=where)
     else:
         _int32(copies, (B, 3), "copies")
     if granted is None:
-        granted = _empty(stream, R, dtype=torch.int32, device=where)
+        granted = empty(R, dtype=torch.int32, device=where)
     else:
         _int32(granted, (R,), "granted")
     if workspace is None:
-        workspace = _empty(stream, max(_known_reorder_bytes(R, W, width), 256), dtype=torch.uint8, device=where)
+        workspace = empty(max(_known_reorder_bytes(R, W, width), 256), dtype=torch.uint8, device=where)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous and on the parents' device")
     _call("fd_reorder_pages", dev, stream, parents.data_ptr(), R, W, seqlens.data_ptr(), block_table.data_ptr(), width,

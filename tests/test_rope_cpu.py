@@ -76,7 +76,7 @@ def test_binding_checks_before_the_call():
         return fdmod._rope_args(k, k, i, positions, rope, kp, kp, q, q_out, False, None)
 
     q = torch.zeros(4, 6, 64, dtype=torch.bfloat16)
-    assert args()[1][:3] == (4, 0, 2)
+    assert args()[2][:4] == (4, 0, 2, 64) and args(q=q)[2][1] == 6
     for bad in (dict(rope=rope.double()), dict(rope=rope[0]), dict(rope=rope.t()), dict(positions=i[:3]), dict(positions=i.long()),
                 dict(q_out=q), dict(q=q.float()), dict(q=q[:3]), dict(q=q[:, :, :32]), dict(q=q, q_out=q[:, :5]),
                 dict(q=q, q_out=q.float())):
