@@ -749,14 +749,18 @@ template <typename T> __global__ void __launch_bounds__(ST) top_kernel(const Sel
     __syncthreads();
     const int n = l.n;
     if (found <= MAX_SEGS && n <= FEW) {
-        // a warp a candidate: how many are before it
-        for (int i = warp; i < n; i += SW) {
-            const Cand c = few[i];
+        // eight threads a candidate: how many are before it
+        for (int i0 = 0; i0 < n; i0 += ST / 8) {
+            const int i = i0 + tid / 8;
+            const Cand c = few[min(i, n - 1)];
             int rank = 0;
-            for (int j = lane; j < n; j += 32)
+#pragma unroll 4
+            for (int j = tid & 7; j < n; j += 8)
                 rank += few[j].before(c.key, c.idx);
-            rank = __reduce_add_sync(FULL_MASK, rank);
-            if (lane == 0 && rank < p.K)
+#pragma unroll
+            for (int o = 4; o; o >>= 1)
+                rank += __shfl_xor_sync(FULL_MASK, rank, o);
+            if ((tid & 7) == 0 && i < n && rank < p.K)
                 emit(p, rank, true, c, ended);
         }
         if (tid >= n && tid < p.K)
