@@ -20,9 +20,9 @@
 // nearer than some 1e-7 may change places, those of one beam do not.
 //
 // 64 requests of 8 beams over 131072 tokens, bf16, a tenth of them finished (121
-// MB): 31 us, of which the rows take some 23 (a bare read of as many bytes
+// MB): 30 us, of which the rows take some 23 (a bare read of as many bytes
 // 20.5) and the top 7; 32 of 4 over 128000 in float32 (66 MB) 17.7, 12.6 and 5;
-// one of 4 over 32000 6.3, where both are chains of dependent steps.  Constant
+// one of 4 over 32000 6, where both are chains of dependent steps.  Constant
 // rows, which pass the bound whole, take the slower way: 4 x 32000 22 us.
 #include "fd_beam.h"
 #include "fd_device.cuh"
