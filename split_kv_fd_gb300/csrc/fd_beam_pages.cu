@@ -39,8 +39,7 @@ __device__ __forceinline__ int pages_of(const ReorderParams &p, int len)
     return (int)(((long long)len + p.page_size - 1) / p.page_size);
 }
 
-// What comes back of a place: bit w where beam w is the first to name a page
-// that no parent's table has there.
+// A request's beams before the step.
 struct Beams {
     int len[BEAM_MAX_W], pages[BEAM_MAX_W], parent[BEAM_MAX_W];   // parent: -1 for none
     int wants[BEAM_MAX_W];   // pages of the parent's
@@ -51,6 +50,9 @@ struct Beams {
 // step: rolled ones cost a latency a beam.)
 constexpr int BATCH = 8;
 
+// What comes back of a tile's places (`gone`: the beams that are the first to
+// name a page that no parent's table has there), the places whose entries
+// change, and, of a request's first tile, the copies it needs.
 __global__ void __launch_bounds__(RT) look_kernel(const ReorderParams p)
 {
     __shared__ Beams b;

@@ -11,7 +11,7 @@
 // Memory bounds it: every element is read once and written once, and the
 // arithmetic is some 3 operations an element.  A thread takes 8 + 8 elements
 // of a head, such that both halves of a pair are its own, and the same ones of
-// every HS-th head, so that its cosines and sines are loaded once a token.
+// every `hs`-th head, so that its cosines and sines are loaded once a token.
 // 16K tokens of 64 query heads and 8 K/V heads of 128, bf16 (637 MB): 100 us,
 // 6.3 TB/s.  (More rows a thread at a time, or more tokens a CTA, cost registers
 // and so CTAs on an SM: 105-130 us.)  A decode step of 256 such tokens into
@@ -24,7 +24,7 @@ namespace fd {
 namespace {
 
 constexpr int RT = 128;   // threads of a CTA
-constexpr int SMS = 152;
+constexpr int SMS = 152;  // of a GB300
 
 // Not through the read-only path: q may be rotated in place.
 __device__ __forceinline__ uint4 load_once(const void *p)
