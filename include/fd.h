@@ -684,8 +684,10 @@ fd_status fd_beam_select(const void *logits, fd_dtype dtype, long long request_s
                          float *out_scores, int32_t *out_parents, int32_t *out_tokens, uint8_t *out_finished,
                          void *workspace, size_t workspace_bytes, void *stream);
 
-/* Bytes of device workspace fd_reorder_pages needs; it needs no
- * initialisation.  Returns 0 for sizes that are not supported. */
+/* Bytes of device workspace fd_reorder_pages needs (about the block table's
+ * own size, max_pages rounded up to 256); it needs no initialisation, and calls
+ * that overlap on the GPU need workspaces of their own.  Returns 0 for sizes
+ * that are not supported. */
 size_t fd_workspace_size_reorder(int R, int W, int max_pages);
 
 /*
