@@ -216,13 +216,16 @@ template <typename T> __global__ void __launch_bounds__(ST, SEL_CTAS) rows_kerne
         }
         copies_issued();
     };
+    // A beam that has ended is not read, so its flag is waited for (one request
+    // of 4 beams 6.0 us, 5.9 with the first reads ahead of it); the score is not,
+    // rows without one may be read.
+    const float score = p.scores[row];
+    if (p.finished && p.finished[row])
+        return;
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i)
         ahead(g0 + i * U, i);
-    // (the first are on their way before it is known whether the beam counts)
-    const float score = p.scores[row];
-    const bool over = p.finished && p.finished[row];
-    if (!isfinite(score) || over) {
+    if (!isfinite(score)) {
         copies_landed<0>();
         return;
     }
