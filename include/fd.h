@@ -672,10 +672,13 @@ size_t fd_workspace_size_beam(int R, int W, int V, int K);
  * request's first token: -inf), nor is one whose score leaves the range of
  * float32.  Where fewer than K are left the rest is -inf, parent -1, token
  * -1, finished.
- * The sum of exponentials is float32, its logarithm and all after it close to
- * 48 bits: continuations of one beam are ordered as their logits are (unless
- * these differ by less than some 2^-46 of the score), those of two beams as
- * their scores where these differ by more than some 1e-7.
+ * Sums of exponentials and their logarithm are float32: a beam's logarithm is
+ * off by less than (90 + 2.25 ln V) 2^-24, 7e-6 at V = 262144 (some 2e-7 on
+ * ordinary rows, up to 1e-6 measured where equal logits lie below a peak), alike
+ * for all its continuations.  What is added to it is kept to close to 48 bits:
+ * continuations of one beam are ordered as their logits are (unless these
+ * differ by less than some 2^-46 of the score), those of two beams as their
+ * scores where these differ by more than twice that error.
  * 1 <= W <= 32, 1 <= K <= 64, K <= W * V, W * V <= 2^30; outputs must not
  * overlap inputs.
  */

@@ -15,9 +15,13 @@
 //    and of a lower index).  Only some K segments are read again, and the K-th
 //    largest maximum is a bound that few of their elements reach.
 //
-// Candidates are ordered by sums in two float32 parts, close to 48 bits, so
-// that only the sum of exponentials is rounded to less: neighbours of two beams
-// nearer than some 1e-7 may change places, those of one beam do not.
+// Sums of exponentials and their logarithm are float32, the parts' sums joined
+// with what rounding cuts off: off by less than (90 + 2.25 ln V) 2^-24 together
+// (derived beside the tests), 2e-7 on ordinary rows and 1e-6 at most measured.
+// More would cost the rows' kernel instructions, of which it has none to spare.
+// That error is a beam's as a whole: what its candidates add to it are sums in
+// two float32 parts, close to 48 bits, so neighbours of two beams nearer than
+// twice the error may change places, those of one beam do not.
 //
 // 64 requests of 8 beams over 131072 tokens, bf16, a tenth of them finished (121
 // MB): 30 us, of which the rows take some 23 (a bare read of as many bytes
@@ -586,21 +590,25 @@ template <typename T> __global__ void __launch_bounds__(ST) top_kernel(const Sel
             for (int i = 128 + lane; i < p.parts; i += 32)
                 mine = fmaxf(mine, part[i].x);
             m = warp_max(mine);
+            // the sum with what its roundings cut off: a row of 2^29 has 2048
+            // parts a lane, which a plain one may leave 3e-5 off
+            auto plus = [&](float x) {
+                const float t = s + x, z = t - s;
+                e += (s - (t - z)) + (x - z);
+                s = t;
+            };
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-                s += x[u].y > 0.f ? x[u].y * expf(x[u].x - m) : 0.f;
+                plus(x[u].y > 0.f ? __fmul_rn(x[u].y, expf(x[u].x - m)) : 0.f);
             for (int i = 128 + lane; i < p.parts; i += 32) {
                 const float2 y = part[i];
-                s += y.y > 0.f ? y.y * expf(y.x - m) : 0.f;
+                plus(y.y > 0.f ? __fmul_rn(y.y, expf(y.x - m)) : 0.f);
             }
-            // the sum with what its roundings cut off
 #pragma unroll
             for (int o = 16; o; o >>= 1) {
                 const float x = __shfl_xor_sync(FULL_MASK, s, o);
                 e += __shfl_xor_sync(FULL_MASK, e, o);
-                const float t = s + x, z = t - s;
-                e += (s - (t - z)) + (x - z);
-                s = t;
+                plus(x);
             }
         }
         if (lane == 0) {
