@@ -669,16 +669,21 @@ size_t fd_workspace_size_beam(int R, int W, int V, int K);
  *             finished; or NULL.  Not the buffer of `finished`
  * A logit of -inf or NaN is no continuation, +inf counts as the largest
  * finite float32; a beam whose score is not finite has none (all but one at a
- * request's first token: -inf), nor is one whose score leaves the range of
- * float32.  Where fewer than K are left the rest is -inf, parent -1, token
- * -1, finished.
+ * request's first token: -inf), nor is one whose score, or whose distance below
+ * the beam's largest logit, leaves the range of float32.  Where fewer than K are
+ * left the rest is -inf, parent -1, token -1, finished.
  * Sums of exponentials and their logarithm are float32: a beam's logarithm is
  * off by less than (90 + 2.25 ln V) 2^-24, 7e-6 at V = 262144 (some 2e-7 on
  * ordinary rows, up to 1e-6 measured where equal logits lie below a peak), alike
  * for all its continuations.  What is added to it is kept to close to 48 bits:
  * continuations of one beam are ordered as their logits are (unless these
  * differ by less than some 2^-46 of the score), those of two beams as their
- * scores where these differ by more than twice that error.
+ * scores where these differ by more than twice that error.  Within it a beam's
+ * scores depend on how its row is cut for the sum, and so on R*W, on where the
+ * row lies from a 16-byte boundary, and on the GPU: the same beam may have other
+ * last bits in another batch, and of two beams with the same logits and scores
+ * either may be ahead where their rows lie differently.  Calls with the same
+ * sizes, strides and alignment give the same bits.
  * 1 <= W <= 32, 1 <= K <= 64, K <= W * V, W * V <= 2^30; outputs must not
  * overlap inputs.
  */

@@ -968,10 +968,12 @@ def beam_select(logits, scores, num=None, finished=None, eos=-1, workspace=None,
 
     logits [R, W, V] float32, float16 or bfloat16, a beam's V neighbouring (any
     strides else); scores float32 [R, W]; finished bool [R, W]: beams that go
-    on with ``eos`` alone at the score they have.  Equal scores in order of
-    beam and token.  Where a request has fewer continuations (of -inf, NaN
-    and beams without a finite score there are none) the rest is -inf, -1, -1
-    and finished.
+    on with ``eos`` alone at the score they have, their logits not read.
+    Equal scores in order of beam and token.  Where a request has fewer
+    continuations (of -inf, NaN and beams without a finite score there are
+    none) the rest is -inf, -1, -1 and finished.  A beam's scores share the
+    error of a float32 sum, below 1e-5 (some 2e-7 on ordinary rows), whose last
+    bits follow the batch's size and the rows' alignment.
     """
     dev = _one_device(logits, scores, finished)
     if logits.dim() != 3 or logits.dtype not in DTYPE_CODE:
