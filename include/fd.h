@@ -462,9 +462,12 @@ fd_status fd_decode_noalloc(const void *q, const void *k, const void *v, const i
  * large holds back those behind it that need pages in the same call, although
  * pages for them are free: put running sequences ahead of admissions, or
  * admit in a call of its own.  Compare seqlens with target to see which were
- * given.  The result does not depend on the order of threads.  A page belongs
- * to one sequence (one that several tables name would be given back several
- * times).  Ids that name no page are stored as -1 where they are released or
+ * given.  The result does not depend on the order of threads.  A page that is
+ * given back belongs to one sequence: one that several tables name would go on
+ * the stack once for each, and later to several sequences.  So the beams of a
+ * request, which share pages (fd_reorder_pages), grow here, but are neither
+ * shrunk nor ended here: negative parents end them there.
+ * Ids that name no page are stored as -1 where they are released or
  * taken, and the slots of new tokens in such a page are -1; released pages
  * that would raise the stack past num_pages are dropped, those of the first
  * sequences before others'.  Both are reported as FD_ERR_BAD_PAGE by
@@ -719,7 +722,9 @@ size_t fd_workspace_size_reorder(int R, int W, int max_pages);
  *   copies       [R*W, 3] int32, out: page from, page to, and rows to copy of
  *                each new beam; -1, -1, 0 where there is nothing to copy
  *   granted      [R] int32, out, or NULL: 1, or 0 where a request stays as it
- *                was because pages were missing
+ *                was because pages were missing: the choice behind `parents` has
+ *                not been made then, so its scores, flags and logits are kept
+ *                too, no token is appended, and it is made again in a later step
  *   workspace    fd_workspace_size_reorder(R, W, max_pages) bytes, 256-byte
  *                aligned
  * Releases come first.  A request that gives back as many pages as it needs is
@@ -728,8 +733,9 @@ size_t fd_workspace_size_reorder(int R, int W, int max_pages);
  * pages go on the stack in reverse order of (request, place, beam), copies
  * take theirs from the top in order of (request, beam).  The result does not
  * depend on the order of threads.
- * Growth is fd_resize_pages' (new pages are a beam's own); it must not shrink
- * beams into pages that they share.  A page belongs to one request, and
+ * Growth is fd_resize_pages' (new pages are a beam's own); it must neither shrink
+ * beams into pages that they share nor end them, which negative parents do: it
+ * would give back a shared page once a beam.  A page belongs to one request, and
  * is named at one place of its beams' tables; E4M3 scales are the same for a
  * request's beams.  A parent of W or more counts as negative, reported as
  * FD_ERR_BAD_INDEX by fd_device_status; ids that name no page are moved, but

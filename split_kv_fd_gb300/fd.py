@@ -642,7 +642,9 @@ def resize_pages(seqlens, target, block_table, free_pages, free_count, page_size
     sequences' new tokens (allocated if only slots or positions are given).
     Returns ``cu_new``.  A sequence that could not grow keeps its length, and
     so do those behind it whose pages would only be free without it: running
-    sequences go ahead of admissions.
+    sequences go ahead of admissions.  Beams that share pages grow here, but are
+    ended by ``reorder_pages`` (negative parents): shrinking them would give a
+    shared page back once for each.
     """
     dev = _one_device(seqlens, target, block_table, free_pages, free_count, slots, positions, cu_new)
     if seqlens.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
@@ -1033,7 +1035,8 @@ def reorder_pages(parents, seqlens, block_table, free_pages, free_count, page_si
     free_pages int32 [num_pages] and free_count int32 [1], the stack of
     resize_pages.  copies int32 [R*W, 3]: page from, page to and rows, -1, -1
     and 0 without a copy; granted int32 [R]: 0 where pages were missing and the
-    request stays as it was.
+    request stays as it was, so that its old scores, flags and logits hold on and
+    the choice is made again in a later step.
     """
     dev = _one_device(parents, seqlens, block_table, free_pages, free_count, copies, granted)
     if parents.dim() != 2 or block_table.dim() != 2 or free_pages.dim() != 1:
