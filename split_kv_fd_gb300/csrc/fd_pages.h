@@ -66,6 +66,7 @@ struct RopeParams {
     int f8, B;
     const int32_t *cu;       // [B + 1]
     const float *k_scale, *v_scale;   // [B, H]
+    int sms;                 // of the device
     unsigned *status;
 };
 

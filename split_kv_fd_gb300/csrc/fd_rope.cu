@@ -24,7 +24,6 @@ namespace fd {
 namespace {
 
 constexpr int RT = 128;   // threads of a CTA
-constexpr int SMS = 152;  // of a GB300
 
 // Not through the read-only path: q may be rotated in place.
 __device__ __forceinline__ uint4 load_once(const void *p)
@@ -223,7 +222,7 @@ template <typename T, bool F8> cudaError_t launch_t(const RopeParams &p, cudaStr
     // none 7.7).  16K tokens gain nothing (129 us in five shares, 100 in one:
     // each reads the table's row).
     const int passes = (int)((((long long)p.Hq + 2LL * p.H) * (p.d / 16) + RT - 1) / RT);
-    const int share = p.T < 4 * SMS ? (4 * SMS + p.T - 1) / p.T : 1;
+    const int ctas = 4 * p.sms, share = p.T < ctas ? (ctas + p.T - 1) / p.T : 1;
     const dim3 grid(p.T, passes < share ? passes : share);
     if (p.pairs)
         rope_kernel<T, F8, true><<<grid, RT, 0, s>>>(p);

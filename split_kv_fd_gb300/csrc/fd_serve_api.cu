@@ -466,7 +466,8 @@ fd_status append_rope(RopeParams &p, long long num_pages, void *stream)
         return FD_ERR_INVALID_ARG;
     p.num_slots = num_pages * p.page_size;
     p.status = status_ptr();
-    if (!p.status)
+    p.sms = sm_count();
+    if (!p.status || p.sms <= 0)
         return FD_ERR_CUDA;
     return launch_rope(p, stream_of(stream)) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
 }
