@@ -465,8 +465,8 @@ fd_status fd_decode_noalloc(const void *q, const void *k, const void *v, const i
  * given.  The result does not depend on the order of threads.  A page that is
  * given back belongs to one sequence: one that several tables name would go on
  * the stack once for each, and later to several sequences.  So the beams of a
- * request, which share pages (fd_reorder_pages), grow here, but are neither
- * shrunk nor ended here: negative parents end them there.
+ * request, which share pages (fd_reorder_pages), grow here and shrink within
+ * pages that are their own, but end there, by negative parents.
  * Ids that name no page are stored as -1 where they are released or
  * taken, and the slots of new tokens in such a page are -1; released pages
  * that would raise the stack past num_pages are dropped, those of the first

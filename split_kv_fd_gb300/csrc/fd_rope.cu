@@ -14,8 +14,11 @@
 // every `hs`-th head, so that its cosines and sines are loaded once a token.
 // 16K tokens of 64 query heads and 8 K/V heads of 128, bf16 (637 MB): 100 us,
 // 6.3 TB/s.  (More rows a thread at a time, or more tokens a CTA, cost registers
-// and so CTAs on an SM: 105-130 us.)  A decode step of 256 such tokens into
-// E4M3 pages: 5.2 us, a launch and the loads slot, table and offsets wait for.
+// and so CTAs on an SM: 105-130 us.)  Into E4M3 pages 108, 0.83 of the copy
+// bandwidth: 70 registers against 48 leave 7 CTAs on an SM.  A decode step of
+// 256 such tokens into E4M3 pages: 5 us, a launch and the loads slot, table and
+// offsets wait for.  A CTA takes one token however few its heads are: 16K tokens
+// of 8 + 1 heads of 64 take 17 us, three times their bytes' time.
 #include "fd_device.cuh"
 #include "fd_e4m3.cuh"
 #include "fd_pages.h"
